@@ -4,6 +4,9 @@ The compute lives in libcpsa.so (hand-written CUDA, C ABI in include/cpsa.h);
 this package is its Python binding plus host-side orchestration:
 
   cpp_kv_cache_write        slot_mapping scatter of the new tokens' K/V
+  cpp_rope_kv_cache_write   rotary position embedding of q and k fused with that append
+  cpp_rope_kv_cache_write_q8
+                            the same into an 8-bit cache (e4m3, a scale per 16 tokens and head)
   cpp_chunked_prefill_attn  causal attention of prefill chunks and decode rows
   cpp_chunked_prefill_attn_write_kv
                             the KV write fused into that attention call
@@ -15,7 +18,8 @@ this package is its Python binding plus host-side orchestration:
                             on one stream or as two micro-batches on two streams
 """
 from ._lib import (  # noqa: F401
-    CpsaError, load, cpp_kv_cache_write, cpp_attn_workspace_bytes, cpp_attn_workspace_min_bytes,
+    CpsaError, load, cpp_kv_cache_write, cpp_rope_kv_cache_write, cpp_rope_kv_cache_write_q8,
+    cpp_attn_workspace_bytes, cpp_attn_workspace_min_bytes,
     cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
     cpp_noalloc_scratch_address,
     cpp_chunked_prefill_attn_write_kv,
@@ -23,6 +27,6 @@ from ._lib import (  # noqa: F401
     cpp_fit_latency_quadratic, cpp_fit_latency_two_var, cpp_selftest_exp2, cpp_selftest_wait_timeout,
     OnlineChunker, BatchScheduler,
     DEV_SLOT_OUT_OF_RANGE, DEV_PAGE_OUT_OF_RANGE, DEV_SEQ_LT_QUERY, DEV_TOKENS_MISMATCH, DEV_SEQ_GT_TABLE,
-    DEV_SPLITS_CLAMPED, DEV_WAIT_TIMEOUT,
+    DEV_SPLITS_CLAMPED, DEV_WAIT_TIMEOUT, DEV_POSITION_OUT_OF_RANGE,
 )
 from .step import AttentionStep  # noqa: F401

@@ -33,6 +33,7 @@ DEV_SEQ_GT_TABLE = 0x10
 DEV_SPLITS_CLAMPED = 0x20
 DEV_WAIT_TIMEOUT = 0x40
 DEV_PLAN_OVERFLOW = 0x80
+DEV_POSITION_OUT_OF_RANGE = 0x100
 
 
 class CpsaError(RuntimeError):
@@ -49,6 +50,12 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     lib.cpp_kv_cache_write.restype = _c_int
     lib.cpp_kv_cache_write.argtypes = [_c_p, _c_p, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_i64, _c_p, _c_p, _c_p, _c_p]
+    lib.cpp_rope_kv_cache_write.restype = _c_int
+    lib.cpp_rope_kv_cache_write.argtypes = [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_int,
+                                            _c_int, _c_p, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_p, _c_p,
+                                            _c_p, _c_p, _c_p]
+    lib.cpp_rope_kv_cache_write_q8.restype = _c_int
+    lib.cpp_rope_kv_cache_write_q8.argtypes = lib.cpp_rope_kv_cache_write.argtypes + [_c_p, _c_p]
     lib.cpp_attn_workspace_bytes.restype = _c_size
     lib.cpp_attn_workspace_bytes.argtypes = [_c_int, _c_i64, _c_int, _c_int, _c_int, _c_int]
     lib.cpp_attn_workspace_min_bytes.restype = _c_size
@@ -149,6 +156,108 @@ def cpp_kv_cache_write(k, v, slot_mapping, k_cache, v_cache, dev_err, stream=Non
                                    _dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"),
                                    _dev(dev_err, torch.int32, "dev_err"), _stream_ptr(stream))
     _check(st, "cpp_kv_cache_write")
+
+
+def _rows(t: torch.Tensor, heads, d, name):
+    """A [T, heads, d] bf16 tensor whose heads are contiguous: its address and its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CpsaError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise CpsaError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+        raise CpsaError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (s[0] if t.shape[0] > 1 else heads * d)
+
+
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _bytes(t: torch.Tensor, kinds, shape, name):
+    """A contiguous one-byte tensor of one of the types `kinds`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CpsaError(f"{name} must be a CUDA tensor")
+    if t.dtype not in kinds:
+        raise CpsaError(f"{name} must be {' or '.join(map(str, kinds))}, got {t.dtype}")
+    if t.shape != shape:
+        raise CpsaError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise CpsaError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _q8_pointers(k_cache, v_cache, k_scale, v_scale):
+    """The four tensors of an 8-bit cache: [pages, Hkv, P, d] bytes and [pages, Hkv, P / min(16, P)] scales."""
+    if k_cache.dim() != 4:
+        raise CpsaError("k_cache must be [pages, kv heads, page size, head dim]")
+    pages, heads, page, _ = k_cache.shape
+    scales = (pages, heads, page // max(1, min(16, page)))
+    return (_bytes(k_cache, _BYTES, k_cache.shape, "k_cache"), _bytes(v_cache, _BYTES, k_cache.shape, "v_cache"),
+            _bytes(k_scale, _SCALES, scales, "k_scale"), _bytes(v_scale, _SCALES, scales, "v_scale"))
+
+
+def _same_device(what, *tensors):
+    """Every tensor on the current device, where the kernel is launched."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise CpsaError(f"{what}: a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _rope_args(what, q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved):
+    """The arguments that both rotary appends share, up to num_pages, and q_out's address."""
+    T, Hkv, d = k.shape
+    pages, Hkv2, P, d2 = k_cache.shape
+    Hq = 0 if q is None else q.shape[1]
+    if v.shape != k.shape or Hkv2 != Hkv or d2 != d or slot_mapping.shape != (T,) \
+            or (q is None) != (q_out is None) or (q is not None and (q.shape != (T, Hq, d) or q_out.shape != q.shape)) \
+            or (cos_sin is None) != (positions is None):
+        raise CpsaError(f"{what}: inconsistent shapes")
+    if cos_sin is not None and (cos_sin.dim() != 2 or positions.shape != (T,)):
+        raise CpsaError(f"{what}: inconsistent shapes")
+    qp, qs = (0, 0) if q is None else _rows(q, Hq, d, "q")
+    kp, ks = _rows(k, Hkv, d, "k")
+    vp, vs = _rows(v, Hkv, d, "v")
+    top, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    return (qp, kp, vp, qs, ks, vs, None if positions is None else _dev(positions, torch.int64, "positions"),
+            None if cos_sin is None else _dev(cos_sin, torch.float32, "cos_sin"), top, rot, int(bool(interleaved)),
+            _dev(slot_mapping, torch.int64, "slot_mapping"), T, Hq, Hkv, d, P, pages,
+            None if q_out is None else _dev(q_out, torch.bfloat16, "q_out"))
+
+
+def cpp_rope_kv_cache_write(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dev_err,
+                            interleaved=False, stream=None):
+    """Rotate q and k by their positions, write q_out, append k and v to the bf16 cache.
+
+    q [T, Hq, d], k, v [T, Hkv, d] bf16, the heads of a token contiguous (slices of one projection's output
+    are fine); positions, slot_mapping [T] int64; cos_sin fp32 [max positions, rotary dim]: the cosines of the
+    rotary dim / 2 angles, then the sines (see rope_table); caches [pages, Hkv, P, d] bf16; q_out [T, Hq, d]
+    bf16, may be q itself when q is contiguous. positions = cos_sin = None rotates nothing; q = q_out = None
+    appends k and v alone."""
+    if v_cache.shape != k_cache.shape:
+        raise CpsaError("cpp_rope_kv_cache_write: inconsistent shapes")
+    args = _rope_args("cpp_rope_kv_cache_write", q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err,
+                      interleaved)
+    caches = (_dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"))
+    err = _dev(dev_err, torch.int32, "dev_err")
+    _same_device("cpp_rope_kv_cache_write", q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dev_err)
+    st = load().cpp_rope_kv_cache_write(*args, *caches, err, _stream_ptr(stream))
+    _check(st, "cpp_rope_kv_cache_write")
+
+
+def cpp_rope_kv_cache_write_q8(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
+                               dev_err, interleaved=False, stream=None):
+    """cpp_rope_kv_cache_write into an 8-bit cache: caches [pages, Hkv, P, d] torch.float8_e4m3fn (or uint8),
+    k_scale, v_scale [pages, Hkv, P / min(16, P)] torch.float8_e8m0fnu (or uint8)."""
+    args = _rope_args("cpp_rope_kv_cache_write_q8", q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err,
+                      interleaved)
+    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale)
+    err = _dev(dev_err, torch.int32, "dev_err")
+    _same_device("cpp_rope_kv_cache_write_q8", q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale,
+                 v_scale, q_out, dev_err)
+    st = load().cpp_rope_kv_cache_write_q8(*args, *caches, err, _stream_ptr(stream))
+    _check(st, "cpp_rope_kv_cache_write_q8")
 
 
 def cpp_attn_workspace_bytes(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_kv_splits=8):

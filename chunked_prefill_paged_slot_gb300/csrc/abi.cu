@@ -180,6 +180,74 @@ int check_attn_shape(int num_reqs, int64_t num_tokens, int num_q_heads, int num_
     return CPSA_OK;
 }
 
+// Both rotary KV appends: the checks, then one launch.
+int rope_append_impl(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                     int rotary_dim, int interleaved, const int64_t *slot_mapping, int64_t num_tokens,
+                     int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages, void *q_out,
+                     void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale, bool q8, uint32_t *dev_err,
+                     void *stream)
+{
+    if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX / 2 || num_q_heads < 0 || num_kv_heads <= 0 ||
+        num_q_heads > 65535 || num_kv_heads > 65535 || num_pages < 0 || max_positions < 0 || rotary_dim < 0)
+        return CPSA_ERR_BAD_SHAPE;
+    if (head_dim != 64 && head_dim != 128)
+        return CPSA_ERR_UNSUPPORTED;
+    if (!(q8 ? pow2_in(page_size, 8, 256) : pow2_in(page_size, 1, 1 << 20)))
+        return CPSA_ERR_UNSUPPORTED;
+    if (rotary_dim > head_dim || rotary_dim % 16 != 0)
+        return CPSA_ERR_UNSUPPORTED;
+    if (num_pages > ((int64_t)1 << 62) / page_size || max_positions > ((int64_t)1 << 55))
+        return CPSA_ERR_BAD_SHAPE;
+    // rows of at least their heads, far below where token * stride would wrap
+    const int64_t most = (int64_t)1 << 31;
+    if ((num_q_heads > 0 && (q_stride < (int64_t)num_q_heads * head_dim || q_stride > most)) ||
+        k_stride < (int64_t)num_kv_heads * head_dim || k_stride > most ||
+        v_stride < (int64_t)num_kv_heads * head_dim || v_stride > most)
+        return CPSA_ERR_BAD_SHAPE;
+    if (num_tokens == 0)
+        return CPSA_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache || !dev_err || (num_q_heads > 0 && (!q || !q_out)) ||
+        (rotary_dim > 0 && (!positions || !cos_sin)) || (q8 && (!k_scale || !v_scale)))
+        return CPSA_ERR_NULL_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out) || q_stride % 8 != 0)) || k_stride % 8 != 0 ||
+        v_stride % 8 != 0 || (rotary_dim > 0 && !aligned16(cos_sin)))
+        return CPSA_ERR_MISALIGNED;
+    // in place only where every row is written back to where it was read
+    if (num_q_heads > 0 && q == q_out && q_stride != (int64_t)num_q_heads * head_dim)
+        return CPSA_ERR_BAD_SHAPE;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return CPSA_ERR_NO_DEVICE;
+    RopeParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.max_positions = max_positions;
+    p.rot = rotary_dim;
+    p.inter = interleaved != 0;
+    p.slot_mapping = slot_mapping;
+    p.num_tokens = num_tokens;
+    p.Hq = num_q_heads;
+    p.Hkv = num_kv_heads;
+    p.page_size = page_size;
+    p.lg_page = __builtin_ctz((unsigned)page_size);
+    p.num_pages = num_pages;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.dev_err = dev_err;
+    return launch_rope_append(p, head_dim, q8, sms, (cudaStream_t)stream) == cudaSuccess ? CPSA_OK : CPSA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -225,6 +293,29 @@ int cpp_kv_cache_write(const void *k, const void *v, const int64_t *slot_mapping
     cudaError_t e = launch_kv_cache_write(k, v, slot_mapping, num_tokens, num_kv_heads, head_dim, page_size,
                                           num_pages, k_cache, v_cache, dev_err, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? CPSA_OK : CPSA_ERR_CUDA;
+}
+
+int cpp_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                            int rotary_dim, int interleaved, const int64_t *slot_mapping, int64_t num_tokens,
+                            int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                            void *q_out, void *k_cache, void *v_cache, uint32_t *dev_err, void *stream)
+{
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, nullptr, nullptr, false, dev_err, stream);
+}
+
+int cpp_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                               int64_t max_positions, int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                               int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                               int64_t num_pages, void *q_out, void *k_cache, void *v_cache, uint8_t *k_scale,
+                               uint8_t *v_scale, uint32_t *dev_err, void *stream)
+{
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, true, dev_err, stream);
 }
 
 size_t cpp_attn_workspace_bytes(int num_reqs, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -70,6 +71,31 @@ struct CombineParams {
     int num_q_heads;
 };
 
+// The rotary KV append (rope_append.cu). q, k, v rows are contiguous heads of
+// head_dim columns, the given number of elements apart from token to token.
+struct RopeParams {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int64_t *positions;
+    const float *cos_sin;      // [max_positions][rot]: cos of the rot/2 angles, then sin
+    int64_t max_positions;
+    int rot;
+    bool inter;                // pairs (2i, 2i + 1) instead of (i, i + rot/2)
+    const int64_t *slot_mapping;
+    int64_t num_tokens;
+    int Hq, Hkv, page_size, lg_page;
+    int64_t num_pages;
+    __nv_bfloat16 *q_out;
+    void *k_cache, *v_cache;   // bf16, or e4m3 bytes
+    uint8_t *k_scale, *v_scale;   // e4m3 cache: [pages][Hkv][page_size / min(16, page_size)], exponent + 127
+    uint32_t *dev_err;
+};
+
+// Scale exponents that the 8-bit cache's writer produces: a subnormal byte under
+// the smallest is still a normal fp32 number, 448 under the largest still finite.
+constexpr int kQ8MinExp = -117;
+constexpr int kQ8MaxExp = 119;
+
 // early: launch with programmatic dependent launch (see launch_pdl)
 // tkn / tvn: maps over k_new / v_new (used when p.fused)
 // to: map over out, boxes of 64 columns x 1 head x 32 rows (used when p.out_tma)
@@ -91,6 +117,7 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
                                   int64_t num_tokens, int num_kv_heads, int head_dim,
                                   int page_size, int64_t num_pages, void *k_cache, void *v_cache,
                                   uint32_t *dev_err, int num_sms, cudaStream_t s);
+cudaError_t launch_rope_append(const RopeParams &p, int head_dim, bool q8, int num_sms, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,
                                     int32_t length_threshold, int32_t *out3, cudaStream_t s);
 

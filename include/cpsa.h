@@ -72,6 +72,7 @@ extern "C" {
 #define CPSA_DEV_SEQ_GT_TABLE 0x10u       /* seq_len > max_blocks_per_req * page_size: request skipped */
 #define CPSA_DEV_SPLITS_CLAMPED 0x20u     /* info: partials did not fit the workspace, one KV split used */
 #define CPSA_DEV_WAIT_TIMEOUT 0x40u       /* an on-chip wait hit its limit; outputs of this call invalid */
+#define CPSA_DEV_POSITION_OUT_OF_RANGE 0x100u  /* position >= max_positions: token skipped whole */
 #define CPSA_DEV_PLAN_OVERFLOW 0x80u      /* a self-planned chunk-kernel run held more pieces than it can keep */
 
 /*
@@ -91,6 +92,77 @@ int cpp_kv_cache_write(const void *k, const void *v, const int64_t *slot_mapping
                        int64_t num_tokens, int num_kv_heads, int head_dim, int page_size,
                        int64_t num_pages, void *k_cache, void *v_cache, uint32_t *dev_err,
                        void *stream);
+
+/*
+ * The rotary KV append: rotate the new tokens' q and k by their positions, write
+ * the rotated q to q_out and append k and v to the cache, in one kernel. It takes
+ * the place of cpp_kv_cache_write where the model rotates (rotary position
+ * embedding); cpp_chunked_prefill_attn then takes q_out and the caches.
+ * (The pages have no counterpart; it exists for library users.)
+ *
+ * q, k, v: token t's heads are contiguous, head_dim columns each, from element
+ * t * q_stride (k_stride, v_stride) of the base pointer on: slices of one fused
+ * projection's output, or contiguous tensors (stride = heads * head_dim). Strides
+ * are in elements, multiples of 8, at least heads * head_dim.
+ * Rotation of the first rotary_dim columns of every q and k head, in fp32:
+ *   pair (a, b) -> (a c - b s, b c + a s),  c = cos_sin[pos][i],
+ *   s = cos_sin[pos][rotary_dim / 2 + i],   i = 0 .. rotary_dim / 2 - 1,
+ * each product and sum rounded on its own; pair i is columns (i, i +
+ * rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0. Columns from
+ * rotary_dim on, and v, pass through. cos_sin: fp32 [max_positions][rotary_dim],
+ * 16-byte aligned (any scaling of the angles is the table's).
+ * rotary_dim: a multiple of 16 up to head_dim; 0 rotates nothing (positions and
+ * cos_sin are not read, may be NULL, and every token counts as having a valid
+ * position). num_q_heads = 0: k and v alone (q, q_out may be NULL).
+ * q_out: [num_tokens][num_q_heads][head_dim] bf16, contiguous; it may be q itself
+ * when q is contiguous (any other overlap of inputs and outputs is unspecified).
+ * positions, slot_mapping: int64 [num_tokens]. A token with a negative position is
+ * padding and skipped whole (its row of q_out is left as it was); a position >=
+ * max_positions sets CPSA_DEV_POSITION_OUT_OF_RANGE and the token is skipped
+ * whole. Otherwise q is rotated, and k and v are written by the rules of
+ * cpp_kv_cache_write: slot < 0 skips them, a slot past the cache sets
+ * CPSA_DEV_SLOT_OUT_OF_RANGE and skips them, duplicate slots leave an unspecified
+ * one of the writers' values. page_size: a power of two up to 2^20.
+ */
+int cpp_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                            int64_t max_positions, int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                            int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                            int64_t num_pages, void *q_out, void *k_cache, void *v_cache, uint32_t *dev_err,
+                            void *stream);
+
+/*
+ * cpp_rope_kv_cache_write into an 8-bit cache.
+ *
+ * k_cache, v_cache: e4m3 bytes [num_pages][num_kv_heads][page_size][head_dim];
+ * k_scale, v_scale: one byte per block of SB = min(16, page_size) places,
+ * [num_pages][num_kv_heads][page_size / SB]; a place holds byte * 2^(scale - 127).
+ * page_size: a power of two in [8, 256].
+ *
+ * Tokens that are neighbours in the call, with ascending slots inside one block,
+ * form a run. need = the smallest x with amax <= 448 * 2^x over the run's finite
+ * values (k after its rotation, not rounded before), within [-117, 119]. A run
+ * that holds the block's first place starts the block over: its exponent x = need,
+ * and what the block's other places held before has no meaning any more (their
+ * bytes are left as they are). Any other run takes x = max(need, the block's
+ * exponent); where that is larger, the block's other bytes are rounded to the new
+ * scale (nearest even: exact but for values that become subnormal). The run's
+ * values are rounded to nearest even under 2^x; magnitudes above 448 * 2^119
+ * saturate, infinities and NaN become NaN and take no part in amax. So a block is
+ * filled from its first place on, by any number of calls, and calls that rewrite
+ * places in its middle only ever raise its exponent.
+ * Tokens of one block that are not neighbours in the call, or not in ascending
+ * order, leave that block with an unspecified mix of their values and scales
+ * (other blocks are not affected). The same holds for duplicate slots.
+ * Everything else is cpp_rope_kv_cache_write's.
+ */
+int cpp_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                               int64_t max_positions, int rotary_dim, int interleaved,
+                               const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads,
+                               int num_kv_heads, int head_dim, int page_size, int64_t num_pages, void *q_out,
+                               void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale,
+                               uint32_t *dev_err, void *stream);
 
 /*
  * Workspace for cpp_chunked_prefill_attn, in bytes.
