@@ -10,6 +10,8 @@ this package is its Python binding plus host-side orchestration:
   cpp_chunked_prefill_attn  causal attention of prefill chunks and decode rows
   cpp_chunked_prefill_attn_write_kv
                             the KV write fused into that attention call
+  cpp_chunked_prefill_attn_q8
+                            the attention over the 8-bit cache
   cpp_split_microbatch      balanced micro-batch split point
   cpp_plan_chunk_sizes      dynamic chunk planner (quadratic latency model)
   OnlineChunker             online chunk-size controller (windowed refit of f(C, H))
@@ -20,7 +22,7 @@ this package is its Python binding plus host-side orchestration:
 from ._lib import (  # noqa: F401
     CpsaError, load, cpp_kv_cache_write, cpp_rope_kv_cache_write, cpp_rope_kv_cache_write_q8,
     cpp_attn_workspace_bytes, cpp_attn_workspace_min_bytes,
-    cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
+    cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_q8, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
     cpp_noalloc_scratch_address,
     cpp_chunked_prefill_attn_write_kv,
     cpp_split_microbatch, cpp_read_device_error, cpp_get_device_error, cpp_plan_chunk_sizes,

@@ -64,6 +64,8 @@ def load():
     lib.cpp_chunked_prefill_attn.argtypes = [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_int, _c_int,
                                              _c_int, _c_int, _c_int, _c_i64, _c_f, _c_int, _c_p, _c_p, _c_size,
                                              _c_p, _c_p]
+    lib.cpp_chunked_prefill_attn_q8.restype = _c_int
+    lib.cpp_chunked_prefill_attn_q8.argtypes = [_c_p] * 2 + lib.cpp_chunked_prefill_attn.argtypes
     lib.cpp_chunked_prefill_attn_events.restype = _c_int
     lib.cpp_chunked_prefill_attn_events.argtypes = lib.cpp_chunked_prefill_attn.argtypes + [_c_p]
     lib.cpp_chunked_prefill_attn_write_kv.restype = _c_int
@@ -292,6 +294,27 @@ def cpp_chunked_prefill_attn(q, k_cache, v_cache, query_lens, seq_lens, block_ta
         _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
         _dev(dev_err, torch.int32, "dev_err"), _stream_ptr(stream))
     _check(st, "cpp_chunked_prefill_attn")
+
+
+def cpp_chunked_prefill_attn_q8(q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table, out,
+                                workspace, dev_err, scale=0.0, max_kv_splits=8, stream=None):
+    """cpp_chunked_prefill_attn over an 8-bit cache: caches [pages, Hkv, P, d] torch.float8_e4m3fn (or uint8),
+    k_scale, v_scale [pages, Hkv, P / min(16, P)] torch.float8_e8m0fnu (or uint8), as cpp_rope_kv_cache_write_q8
+    fills them; the rest as for cpp_chunked_prefill_attn."""
+    what = "cpp_chunked_prefill_attn_q8"
+    T, Hq, d = q.shape
+    B = query_lens.shape[0]
+    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale)
+    pages, Hkv, P, d2 = k_cache.shape
+    if out.shape != q.shape or d2 != d or seq_lens.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise CpsaError(f"{what}: inconsistent shapes")
+    args = (_dev(q, torch.bfloat16, "q"), *caches, _dev(query_lens, torch.int32, "query_lens"),
+            _dev(seq_lens, torch.int32, "seq_lens"), _dev(block_table, torch.int32, "block_table"), B, T,
+            block_table.shape[1], Hq, Hkv, d, P, pages, float(scale), int(max_kv_splits),
+            _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+            _dev(dev_err, torch.int32, "dev_err"))
+    _same_device(what, q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table, out, workspace, dev_err)
+    _check(load().cpp_chunked_prefill_attn_q8(*args, _stream_ptr(stream)), what)
 
 
 def cpp_chunked_prefill_attn_events(q, k_cache, v_cache, query_lens, seq_lens, block_table, out, workspace,

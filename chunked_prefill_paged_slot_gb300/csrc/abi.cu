@@ -165,7 +165,8 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
               void *v_cache, const int32_t *query_lens, const int32_t *seq_lens, const int32_t *block_table,
               int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads, int num_kv_heads,
               int head_dim, int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
-              void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events);
+              void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events,
+              const uint8_t *k_scale = nullptr, const uint8_t *v_scale = nullptr);
 
 int check_attn_shape(int num_reqs, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                      int max_kv_splits)
@@ -350,6 +351,21 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
                                            workspace_bytes, dev_err, stream, nullptr);
 }
 
+int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
+                                const int32_t *block_table, int num_reqs, int64_t num_tokens, int max_blocks_per_req,
+                                int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                float scale, int max_kv_splits, void *out, void *workspace, size_t workspace_bytes,
+                                uint32_t *dev_err, void *stream)
+{
+    if (num_tokens > 0 && (!k_scale || !v_scale))
+        return CPSA_ERR_NULL_ARG;
+    return attn_impl(q, nullptr, nullptr, nullptr, const_cast<void *>(k_cache), const_cast<void *>(v_cache),
+                     query_lens, seq_lens, block_table, num_reqs, num_tokens, max_blocks_per_req, num_q_heads,
+                     num_kv_heads, head_dim, page_size, num_pages, scale, max_kv_splits, out, workspace,
+                     workspace_bytes, dev_err, stream, nullptr, k_scale, v_scale);
+}
+
 int cpp_chunked_prefill_attn_events(const void *q, const void *k_cache, const void *v_cache,
                                     const int32_t *query_lens, const int32_t *seq_lens, const int32_t *block_table,
                                     int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads,
@@ -401,15 +417,17 @@ int cpp_chunked_prefill_attn_write_kv_events(const void *q, const void *k, const
 
 namespace {
 
-// The attention call; k_new != nullptr fuses the KV write (k_new, v_new,
+// The attention call; k_scale != nullptr: over the 8-bit cache; k_new != nullptr fuses the KV write (k_new, v_new,
 // slot_mapping non-null then).
 int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t *slot_mapping, void *k_cache,
               void *v_cache, const int32_t *query_lens, const int32_t *seq_lens, const int32_t *block_table,
               int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads, int num_kv_heads,
               int head_dim, int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
-              void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events)
+              void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events,
+              const uint8_t *k_scale, const uint8_t *v_scale)
 {
     const bool fused = k_new != nullptr;
+    const bool q8 = k_scale != nullptr;   // the cache is e4m3 bytes with scales
     cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
     if (events)
         for (int i = 0; i < 5; ++i)
@@ -502,7 +520,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     // compute their runs themselves, and it is the call's first kernel.
     const bool single_prefill = num_reqs == 1 && num_tokens >= 2;
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
-    const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid);
+    const bool self_plan = !q8 && single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid);
     mark(0, s);
     if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
         return CPSA_ERR_CUDA;
@@ -533,6 +551,13 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     ac.k_cache_w = k_cache;
     ac.v_cache_w = v_cache;
 
+    if (q8) {
+        const Q8Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
+                        __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};
+        return launch_attn_q8_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) == cudaSuccess
+                   ? CPSA_OK
+                   : CPSA_ERR_CUDA;
+    }
     const uint64_t D = (uint64_t)head_dim;
     const uint64_t rows_kv = (uint64_t)num_pages * (uint64_t)num_kv_heads;
     CUtensorMap tq, tk, tv, tkd, tvd;

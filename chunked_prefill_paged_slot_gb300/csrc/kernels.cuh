@@ -35,6 +35,13 @@ struct AttnCommon {
     void *k_cache_w, *v_cache_w;       // bf16 [pages][Hkv][P][D], written
 };
 
+// The 8-bit cache: e4m3 bytes [pages][Hkv][P][D] and scale bytes (exponent + 127)
+// [pages][Hkv][P / SB], SB = 2^lg_sb = min(16, P).
+struct Q8Cache {
+    const uint8_t *k, *v, *ks, *vs;
+    int lg_page, lg_sb;
+};
+
 struct ChunkParams : AttnCommon {
     const PrefillItem *pitems;
     const int32_t *run_first;   // CTA c processes pieces [run_first[c], run_first[c + 1])
@@ -117,6 +124,8 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
                                   int64_t num_tokens, int num_kv_heads, int head_dim,
                                   int page_size, int64_t num_pages, void *k_cache, void *v_cache,
                                   uint32_t *dev_err, int num_sms, cudaStream_t s);
+cudaError_t launch_attn_q8_rows(const AttnCommon &p, const Q8Cache &c, const void *q, int head_dim, int num_reqs,
+                                int num_tokens, cudaStream_t s, bool early);
 cudaError_t launch_rope_append(const RopeParams &p, int head_dim, bool q8, int num_sms, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,
                                     int32_t length_threshold, int32_t *out3, cudaStream_t s);

@@ -231,6 +231,25 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
                              size_t workspace_bytes, uint32_t *dev_err, void *stream);
 
 /*
+ * cpp_chunked_prefill_attn over an 8-bit cache, the one that
+ * cpp_rope_kv_cache_write_q8 fills: k_cache, v_cache e4m3 bytes
+ * [num_pages][num_kv_heads][page_size][head_dim], k_scale, v_scale bytes
+ * [num_pages][num_kv_heads][page_size / min(16, page_size)], a place holding byte *
+ * 2^(scale - 127). Places behind a sequence's end, and the scales of blocks that
+ * hold none of its places, may hold anything. A NaN key makes the rows that see
+ * it NaN, a NaN value their column (and it may do so for that column of earlier
+ * rows of the same chunk). (The pages have no counterpart.)
+ * Every other argument, the workspace (same size functions), the device flags,
+ * the splits and CUDA graph capture are cpp_chunked_prefill_attn's.
+ */
+int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
+                                const int32_t *block_table, int num_reqs, int64_t num_tokens,
+                                int max_blocks_per_req, int num_q_heads, int num_kv_heads, int head_dim,
+                                int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
+                                void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream);
+
+/*
  * cpp_chunked_prefill_attn with timing marks: when `events` is not NULL it
  * points to 5 cudaEvent_t handles (any may be NULL) recorded on `stream`:
  * [0] before the plan kernel (when one runs), [1] before the chunk kernel, [2] after it,
