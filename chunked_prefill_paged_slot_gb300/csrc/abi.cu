@@ -127,6 +127,33 @@ int decode_heads_per_item(int num_kv_heads)
     return num_kv_heads % 8 == 0 ? 8 : (num_kv_heads % 4 == 0 ? 4 : 1);
 }
 
+// The 8-bit caches' decode items: the most heads of 8, 4, 2, 1 that divide the count.
+int q8_decode_heads(int num_kv_heads)
+{
+    return num_kv_heads % 8 == 0 ? 8 : (num_kv_heads % 4 == 0 ? 4 : (num_kv_heads % 2 == 0 ? 2 : 1));
+}
+
+// View of an 8-bit cache [pages][Hkv][P][D] for its decode kernel, innermost
+// dimension first: D bytes, P rows, Hkv heads, pages; boxes of `rows` rows of
+// `heads` heads, rows swizzled over their own D bytes.
+bool make_map_q8(CUtensorMap *m, const void *base, int head_dim, int page_size, int num_kv_heads, int64_t num_pages,
+                 uint32_t rows, uint32_t heads)
+{
+    auto enc = encode_fn();
+    if (!enc)
+        return false;
+    const uint64_t head_bytes = (uint64_t)head_dim * (uint64_t)page_size;
+    cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)page_size, (cuuint64_t)num_kv_heads,
+                          (cuuint64_t)num_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)head_dim, head_bytes, head_bytes * (uint64_t)num_kv_heads};
+    cuuint32_t box[4] = {(cuuint32_t)head_dim, rows, heads, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int nq_for_group(int group) { return (group % 2 == 0) ? 2 : 1; }
 
 // Every attention call gets its own nonzero epoch: the merge counters it leaves
@@ -498,7 +525,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.group = group;
     pp.nq = nq;
     pp.max_splits = max_kv_splits;
-    const int dec_heads = decode_heads_per_item(num_kv_heads);
+    const int dec_heads = q8 ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
     pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
     pp.fused = fused ? 1 : 0;
@@ -554,9 +581,31 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     if (q8) {
         const Q8Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                         __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};
-        return launch_attn_q8_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) == cudaSuccess
-                   ? CPSA_OK
-                   : CPSA_ERR_CUDA;
+        if (!single_decode &&
+            launch_attn_q8_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) != cudaSuccess)
+            return CPSA_ERR_CUDA;
+        if (!single_prefill) {
+            CUtensorMap tk, tv;
+            const uint32_t rows = (uint32_t)decode_q8_box_rows(page_size, dec_heads);
+            if (!make_map_q8(&tk, k_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||
+                !make_map_q8(&tv, v_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads))
+                return CPSA_ERR_CUDA;
+            DecodeParams dp;
+            static_cast<AttnCommon &>(dp) = ac;
+            dp.ditems = ditems;
+            dp.q = q;
+            dp.k_cache_ptr = k_cache;
+            dp.v_cache_ptr = v_cache;
+            const int grid_d = (int)(L.max_ditems < sms ? L.max_ditems : sms);
+            if (launch_decode_q8(dp, c, tk, tv, head_dim, dec_heads, grid_d, s, early) != cudaSuccess)
+                return CPSA_ERR_CUDA;
+            if (cap > 0) {
+                CombineParams cb{counts, citems, part_o, part_ml, out, num_q_heads};
+                if (launch_combine(cb, head_dim, 4 * sms, s, early) != cudaSuccess)
+                    return CPSA_ERR_CUDA;
+            }
+        }
+        return CPSA_OK;
     }
     const uint64_t D = (uint64_t)head_dim;
     const uint64_t rows_kv = (uint64_t)num_pages * (uint64_t)num_kv_heads;

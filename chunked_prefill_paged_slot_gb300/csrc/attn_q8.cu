@@ -32,7 +32,7 @@ __device__ __forceinline__ void q8_widen4(uint32_t w, float (&f)[4])
 
 constexpr int kPlainWarps = 8;
 
-// One CTA per (new token, q head); warp w takes every eighth key, a lane D/32
+// Chunks (query_len >= 2): one CTA per (new token, q head); warp w takes every eighth key, a lane D/32
 // columns; the warps' (max, sum, O) meet in shared memory.
 template <int D>
 __global__ void __launch_bounds__(32 * kPlainWarps)
@@ -52,7 +52,7 @@ attn_q8_row_kernel(const AttnCommon p, const Q8Cache c, const __nv_bfloat16 *q, 
         if (p.cu_q[mid] <= t) lo = mid; else hi = mid - 1;
     }
     const int r = lo, s = p.seq_lens[r], ql = p.query_lens[r];
-    if (t < p.cu_q[r] || t - p.cu_q[r] >= ql || s < ql || (int64_t)s > (int64_t)p.max_blocks * p.page_size)
+    if (ql < 2 || t < p.cu_q[r] || t - p.cu_q[r] >= ql || s < ql || (int64_t)s > (int64_t)p.max_blocks * p.page_size)
         return;
     const int last = s - ql + (t - p.cu_q[r]);
     float qv[CPL], o[CPL], m = -INFINITY, l = 0.f;

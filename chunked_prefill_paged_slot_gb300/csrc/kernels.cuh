@@ -126,6 +126,12 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
                                   uint32_t *dev_err, int num_sms, cudaStream_t s);
 cudaError_t launch_attn_q8_rows(const AttnCommon &p, const Q8Cache &c, const void *q, int head_dim, int num_reqs,
                                 int num_tokens, cudaStream_t s, bool early);
+// decode rows over the 8-bit cache, heads_per_item (8, 4, 2 or 1) kv heads per item;
+// tk / tv: [D][P][Hkv][pages] views of the caches in boxes of decode_q8_box_rows rows
+// x heads_per_item heads (see abi.cu: make_map_q8)
+cudaError_t launch_decode_q8(const DecodeParams &p, const Q8Cache &c, const CUtensorMap &tk, const CUtensorMap &tv,
+                             int head_dim, int heads_per_item, int grid, cudaStream_t s, bool early);
+int decode_q8_box_rows(int page_size, int heads_per_item);
 cudaError_t launch_rope_append(const RopeParams &p, int head_dim, bool q8, int num_sms, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,
                                     int32_t length_threshold, int32_t *out3, cudaStream_t s);

@@ -1,0 +1,67 @@
+// q8.cuh -- device helpers of the 8-bit cache's readers: scale bytes, powers of two,
+// e4m3 and bf16 to f16.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace cpsa {
+
+// The exponent a scale byte stands for (0 and 255, which the writer never stores, as
+// their neighbours: every exponent is that of a normal fp32 number).
+__device__ __forceinline__ int q8_exp(uint32_t byte) { return min(max((int)byte, 1), 254) - 127; }
+
+// 2^x, -126 <= x <= 127
+__device__ __forceinline__ float exp2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// Two e4m3 bytes (the low or the high half of w) as an f16 pair; exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Largest finite magnitude of eight bf16 numbers.
+__device__ __forceinline__ float bf16x8_amax(const uint4 &v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float((w[i] << 16) & 0x7fffffffu), b = __uint_as_float(w[i] & 0x7fff0000u);
+        m = fmaxf(m, a < INFINITY ? a : 0.f);   // false for NaN
+        m = fmaxf(m, b < INFINITY ? b : 0.f);
+    }
+    return m;
+}
+
+// Exponent x with amax * 2^-x in [2^14, 2^15) (where the range of exp2i allows it).
+__device__ __forceinline__ int q_exponent(float amax)
+{
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127 - 14;
+    return amax > 0.f ? max(e, -126) : 0;
+}
+
+// A bf16 pair times f, as an f16 pair.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f)
+{
+    return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
+
+}  // namespace cpsa
