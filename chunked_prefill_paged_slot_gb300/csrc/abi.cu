@@ -170,11 +170,11 @@ uint32_t next_epoch()
 }
 
 // Whether a batch of one prefill request of num_tokens tokens can skip the plan
-// kernel: every chunk-kernel run must fit its pieces in kSelfPlanCap. A run of R
+// kernel: every chunk-kernel run must fit its pieces in cap. A run of R
 // tiles holds at most (R - 2) / L + 2 pieces, L the shortest unit; that ratio is
 // largest with no history (L = 1, R = R0, every unit as short as it gets) and
 // stays below R0 + 3 for any history (the units grow as fast as the run).
-bool self_plan_fits(int64_t num_tokens, int units_per_qtile, int grid)
+bool self_plan_fits(int64_t num_tokens, int units_per_qtile, int grid, int cap)
 {
     // the most pieces a run can hold is in the no-history case (the shortest
     // units): a run of r0 positions meets at most r0 / (1 + kUnitCostTiles) + 2 units
@@ -185,7 +185,7 @@ bool self_plan_fits(int64_t num_tokens, int units_per_qtile, int grid)
     int64_t r0 = (w0 + grid - 1) / grid;
     if (r0 < kMinRunTiles)
         r0 = kMinRunTiles;
-    return r0 / (1 + kUnitCostTiles) + 3 <= kSelfPlanCap;
+    return r0 / (1 + kUnitCostTiles) + 3 <= cap;
 }
 
 int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t *slot_mapping, void *k_cache,
@@ -547,7 +547,8 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     // compute their runs themselves, and it is the call's first kernel.
     const bool single_prefill = num_reqs == 1 && num_tokens >= 2;
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
-    const bool self_plan = !q8 && single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid);
+    const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
+                                                            q8 ? kSelfPlanCapQ8 : kSelfPlanCap);
     mark(0, s);
     if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
         return CPSA_ERR_CUDA;
@@ -578,11 +579,36 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     ac.k_cache_w = k_cache;
     ac.v_cache_w = v_cache;
 
+    const uint64_t D = (uint64_t)head_dim;
+    ChunkParams cp;
+    static_cast<AttnCommon &>(cp) = ac;
+    cp.pitems = pitems;
+    cp.run_first = run_first;
+    cp.flags = flags;
+    cp.epoch = next_epoch();
+    cp.self_plan = self_plan ? 1 : 0;
+    cp.num_tokens = (int)num_tokens;
+    // cuts need two pieces' partial rows per run (see the chunk kernel's self plan)
+    const bool partials_fit = cap >= (int64_t)2 * pp.chunk_grid * kTileM * nq;
+    cp.split_ok = max_kv_splits > 1 && partials_fit ? 1 : 0;
+    cp.split_clamped = max_kv_splits > 1 && !partials_fit ? 1 : 0;
+    // out, [T][Hq][D], in boxes of 64 columns x 1 head x 32 rows: the chunk
+    // kernel's TMA stores of whole units' rows (head_dim 128 without the KV
+    // write, whose cache writer holds the staging buffer) and of merged rows at
+    // the end of a run; without the map the rows are stored directly
+    CUtensorMap to{};
+    cp.out_tma = head_dim == 128 && aligned16(out) &&
+                         make_map(&to, out, D, (uint64_t)num_q_heads, (uint64_t)num_tokens, D * 2,
+                                  D * 2 * num_q_heads, 64, 1, 32)
+                     ? 1
+                     : 0;
     if (q8) {
         const Q8Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                         __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};
+        cp.q = q;
+        cp.q8 = c;
         if (!single_decode &&
-            launch_attn_q8_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) != cudaSuccess)
+            launch_chunk_q8(cp, to, head_dim, nq, pp.chunk_grid, s, early && !self_plan) != cudaSuccess)
             return CPSA_ERR_CUDA;
         if (!single_prefill) {
             CUtensorMap tk, tv;
@@ -607,7 +633,6 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
         }
         return CPSA_OK;
     }
-    const uint64_t D = (uint64_t)head_dim;
     const uint64_t rows_kv = (uint64_t)num_pages * (uint64_t)num_kv_heads;
     CUtensorMap tq, tk, tv, tkd, tvd;
     const uint32_t pb_chunk = page_size < 128 ? page_size : 128;
@@ -639,28 +664,6 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
         return CPSA_ERR_CUDA;
     }
 
-    ChunkParams cp;
-    static_cast<AttnCommon &>(cp) = ac;
-    cp.pitems = pitems;
-    cp.run_first = run_first;
-    cp.flags = flags;
-    cp.epoch = next_epoch();
-    cp.self_plan = self_plan ? 1 : 0;
-    cp.num_tokens = (int)num_tokens;
-    // cuts need two pieces' partial rows per run (see the chunk kernel's self plan)
-    const bool partials_fit = cap >= (int64_t)2 * pp.chunk_grid * kTileM * nq;
-    cp.split_ok = max_kv_splits > 1 && partials_fit ? 1 : 0;
-    cp.split_clamped = max_kv_splits > 1 && !partials_fit ? 1 : 0;
-    // out, [T][Hq][D], in boxes of 64 columns x 1 head x 32 rows: the chunk
-    // kernel's TMA stores of whole units' rows (head_dim 128 without the KV
-    // write, whose cache writer holds the staging buffer) and of merged rows at
-    // the end of a run; without the map the rows are stored directly
-    CUtensorMap to = tq;
-    cp.out_tma = head_dim == 128 && aligned16(out) &&
-                         make_map(&to, out, D, (uint64_t)num_q_heads, (uint64_t)num_tokens, D * 2,
-                                  D * 2 * num_q_heads, 64, 1, 32)
-                     ? 1
-                     : 0;
     // V below page 128: one box per page of one kv head, both column halves
     CUtensorMap tv4 = tv;
     if (head_dim == 128 && page_size < 128 && !make_map4_halves(&tv4, v_cache, page_size, rows_kv, page_size))

@@ -444,6 +444,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
            | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
+// The same for f16 x f16 -> fp32.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major)
+{
+    return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
 // ---------------------------------------------------------------------------
 // math
 // ---------------------------------------------------------------------------

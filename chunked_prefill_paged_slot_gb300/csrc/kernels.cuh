@@ -60,6 +60,9 @@ struct ChunkParams : AttnCommon {
     int split_clamped;          // self-planned batch: splits were asked for but the partials do not fit
     int out_tma;                // head_dim 128, `out` mapped for TMA stores (whole units' rows without the KV
                                 // write, merged rows at the end of a run)
+    // over the 8-bit cache (launch_chunk_q8) only
+    const void *q;              // bf16 [T][Hq][D]
+    Q8Cache q8;
 };
 
 struct DecodeParams : AttnCommon {
@@ -112,6 +115,9 @@ cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const
                               const CUtensorMap &tv, const CUtensorMap &tkn, const CUtensorMap &tvn,
                               const CUtensorMap &to, const CUtensorMap &tv4, int head_dim, int nq, int grid,
                               cudaStream_t s, bool early);
+// the chunk kernel over the 8-bit cache (p.q, p.q8)
+cudaError_t launch_chunk_q8(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
+                            cudaStream_t s, bool early);
 cudaError_t launch_decode_attn(const DecodeParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int head_dim,
                                int grid, cudaStream_t s, bool early);
 // the grouped decode kernel: items of heads_per_item (4 or 8) kv heads; tk / tv
@@ -124,8 +130,6 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
                                   int64_t num_tokens, int num_kv_heads, int head_dim,
                                   int page_size, int64_t num_pages, void *k_cache, void *v_cache,
                                   uint32_t *dev_err, int num_sms, cudaStream_t s);
-cudaError_t launch_attn_q8_rows(const AttnCommon &p, const Q8Cache &c, const void *q, int head_dim, int num_reqs,
-                                int num_tokens, cudaStream_t s, bool early);
 // decode rows over the 8-bit cache, heads_per_item (8, 4, 2 or 1) kv heads per item;
 // tk / tv: [D][P][Hkv][pages] views of the caches in boxes of decode_q8_box_rows rows
 // x heads_per_item heads (see abi.cu: make_map_q8)

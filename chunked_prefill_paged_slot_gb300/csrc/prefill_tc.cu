@@ -48,6 +48,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "plan.cuh"
+#include "q8.cuh"
 
 namespace cpsa {
 
@@ -65,7 +66,9 @@ constexpr int kFmaExpPairsPer8 = CPSA_FMA_EXP_PAIRS_PER_8;
 constexpr int kMergeMaxOthers = 3;
 constexpr int kMergeStageBytes = kMergeMaxOthers * 32 * 128 * 2;
 
-template <int D, int NQ>
+// Over the 8-bit cache the kernel has another cast of warps (see chunk_attn_kernel)
+// and keeps a little more in shared memory, so fewer self-planned pieces.
+template <int D, int NQ, bool Q8 = false>
 struct ChunkCfg {
     static constexpr int kHalves = D / 64;             // 128-byte swizzle atoms across a row
     static constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16
@@ -76,14 +79,17 @@ struct ChunkCfg {
     static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer
     static constexpr int kBarOff = kStageOff + kTileBytes;
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
-    static constexpr int kBarBytes = 256 + kSelfPlanCap * 32;  // barriers + pieces
+    static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
+    static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
+    static constexpr int kBarBytes = 256 + kSelfPlanCap * 32;  // barriers + pieces (+ Q8Tiles)
     static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
     static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= kSlotOff + kSlots * kTileBytes,
                   "the staged merge uses the Q and K/V buffers");
-    static constexpr int kThreads = 352;
-    static constexpr int kLoadWarp = 8;
-    static constexpr int kMmaWarp = 9;
+    static constexpr int kThreads = Q8 ? 384 : 352;            // both leave 168 registers a thread
+    static constexpr int kLoadWarp = 8;                        // Q8: to kLoadWarp + kConverters - 1
+    static constexpr int kConverters = 3;
+    static constexpr int kMmaWarp = Q8 ? 11 : 9;
     static constexpr int kWriteWarp = 10;
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t s_col(int n) { return (uint32_t)n * 128u; }
@@ -100,6 +106,17 @@ struct ChunkBars {
     int abort;
     int it_begin, it_end;    // this CTA's run of pieces
 };
+// What the 8-bit cache's converters tell the softmax: per KV tile (its ordinal in the
+// CTA's run, modulo 8) the exponents of its K and V operands, per q row its own (two
+// sets, for items in turn). An entry is written again only after MMAs that come after
+// the softmax has read it: at most four K tiles are ahead of the softmax, and an
+// item's Q replaces the one before it once that one's scores are done, which may be
+// before the softmax looks at them, but not before it is done with the item before.
+struct Q8Tiles {
+    int kx[8], vx[8];
+    int8_t qe[2][256];
+};
+static_assert(sizeof(Q8Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32, "in place of the pieces it gave up");
 static_assert(sizeof(ChunkBars) <= 256, "the self-planned pieces follow the barriers at +256");
 static_assert(sizeof(PrefillItem) == 32, "piece size");
 
@@ -152,7 +169,7 @@ __device__ __forceinline__ int epoch_arrive(unsigned long long *cnt, uint32_t ep
 // self_plan_run); I is the integer type of the tile positions: 32 bits whenever
 // the request's W tiles fit (64-bit division is a long software routine on the
 // GPU, and this walk sits on every launch's critical path), 64 bits otherwise.
-template <int NQ, typename I>
+template <int NQ, int CAP, typename I>
 __device__ __forceinline__ int self_plan_walk(PrefillItem *items, int lane, int nqt, int hb, int nkv_last, int upq,
                                               int pairs, I run, bool cut)
 {
@@ -178,7 +195,7 @@ __device__ __forceinline__ int self_plan_walk(PrefillItem *items, int lane, int 
         const unsigned m = __ballot_sync(0xffffffffu, take);
         if (take) {
             const int k = n + __popc(m & below);
-            if (k < kSelfPlanCap) {
+            if (k < CAP) {
                 const int kvh = j / pairs, hp = j - kvh * pairs;
                 const I c0 = t0 / run;
                 const int np = cut ? (int)((u1 - 1) / run - c0 + 1) : 1;
@@ -215,7 +232,7 @@ __device__ __forceinline__ int self_plan_walk(PrefillItem *items, int lane, int 
 // (np >= 2): no overlap, and 2 x grid x 128 NQ rows are enough (the host checks
 // that they fit before it allows cuts). A piece of run c belongs to it, so its
 // index within its unit is c - c0. Validation as in the plan, flags raised by
-// CTA 0. Writes up to kSelfPlanCap pieces; returns their number (warp-uniform).
+// CTA 0. Writes up to CAP pieces; returns their number (warp-uniform).
 // Everything the self plan reads from the kernel's parameters, passed by value:
 // the plan lives out of line (so that its registers do not weigh on the softmax
 // and MMA loops, which sit at the register cap), and a reference to the
@@ -226,7 +243,7 @@ struct SelfPlanArgs {
     int num_tokens, max_blocks, page_size, group, num_kv_heads, fused, split_ok, split_clamped;
 };
 
-template <int NQ>
+template <int NQ, int CAP>
 __device__ __noinline__ int self_plan_run(const SelfPlanArgs a, PrefillItem *items, int lane)
 {
     const int q = __ldg(a.query_lens), s = __ldg(a.seq_lens);
@@ -258,12 +275,12 @@ __device__ __noinline__ int self_plan_run(const SelfPlanArgs a, PrefillItem *ite
     const long long run = max((W + grid - 1) / grid, (long long)kMinRunTiles);
     const bool cut = a.split_ok && !(shortest >= run && nkv_last + kUnitCostTiles <= run + kCutCostTiles);
     int n = W + run < 0x7fffffffll
-                ? self_plan_walk<NQ, int>(items, lane, nqt, hb, nkv_last, upq, pairs, (int)run, cut)
-                : self_plan_walk<NQ, long long>(items, lane, nqt, hb, nkv_last, upq, pairs, run, cut);
-    if (n > kSelfPlanCap) {
+                ? self_plan_walk<NQ, CAP, int>(items, lane, nqt, hb, nkv_last, upq, pairs, (int)run, cut)
+                : self_plan_walk<NQ, CAP, long long>(items, lane, nqt, hb, nkv_last, upq, pairs, run, cut);
+    if (n > CAP) {
         if (lane == 0)
             set_dev_error(a.dev_err, CPSA_DEV_PLAN_OVERFLOW);
-        n = kSelfPlanCap;
+        n = CAP;
     }
     return n;
 }
@@ -384,15 +401,16 @@ __device__ __forceinline__ float merge_weights(const float2 *pml, int piece, int
 // (this warp's 4 KB of the cache writer's buffer, free at the end of a run) and
 // every row valid, the merged rows leave by TMA stores through the `out` map,
 // 64 columns at a time; otherwise each lane stores its row.
-template <int D, int NQ>
+// own_f: this piece's O stands for own_f times it (1 over a bf16 cache).
+template <int D, int NQ, bool Q8>
 __device__ __noinline__ void merge_split_row(const ChunkParams &p, uint32_t tO, const float2 *pml, const uint4 *ph,
                                              int piece, int npieces, int wg, int row, int lane, float m_use, float l,
                                              bool valid_row, int64_t out_off, uint4 *stage, uint8_t *ostage,
-                                             const CUtensorMap *tm_o, int h, int t_row0)
+                                             const CUtensorMap *tm_o, int h, int t_row0, float own_f)
 {
     float wq[kMergeMaxOthers + 1];
     const float inv_L = merge_weights<NQ>(pml, piece, npieces, wg, row, m_use, l, wq);
-    const float inv_own = l > 0.f ? 1.f / l : 0.f;
+    const float inv_own = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
     const bool staged_out = ostage != nullptr && __all_sync(0xffffffffu, valid_row);
     if (stage != nullptr) {
 #pragma unroll
@@ -487,12 +505,12 @@ __device__ __noinline__ void merge_split_row(const ChunkParams &p, uint32_t tO, 
 // valid rows directly. Out of line: compiled into the self-planned kernel's
 // loop, the same code measured slower on one-request chunks with the KV write
 // fused, which never take it.
-template <int D>
-__device__ __noinline__ void store_unit_rows_staged(uint32_t tO, float l, bool valid_row, uint8_t *stg,
+template <int D, bool Q8>
+__device__ __noinline__ void store_unit_rows_staged(uint32_t tO, float l, float own_f, bool valid_row, uint8_t *stg,
                                                     const CUtensorMap *tm_o, __nv_bfloat16 *out, int64_t t_row,
                                                     int h, int num_q_heads, int lane)
 {
-    const float inv_l = l > 0.f ? 1.f / l : 0.f;
+    const float inv_l = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
     const bool staged = __all_sync(0xffffffffu, valid_row);
 #pragma unroll
     for (int c2 = 0; c2 < D / 64; ++c2) {
@@ -543,10 +561,10 @@ __device__ __noinline__ void store_unit_rows_staged(uint32_t tO, float l, bool v
 // The same merge for units of more than kMergeMaxOthers + 1 pieces (long KV
 // ranges against short runs), every partial straight from L2; the same weights,
 // order and rounding as merge_split_row.
-template <int D, int NQ>
+template <int D, int NQ, bool Q8>
 __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t tO, const float2 *pml, const uint4 *ph,
                                                  int piece, int npieces, int wg, int row, float m_use, float l,
-                                                 bool valid_row, int64_t out_off)
+                                                 bool valid_row, int64_t out_off, float own_f)
 {
     float M = m_use;
     for (int q = 0; q < npieces; ++q)
@@ -559,7 +577,7 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
         L += ex2_approx(ml.x - Mref) * ml.y;
     }
     const float inv_L = L > 0.f ? 1.f / L : 0.f;
-    const float inv_own = l > 0.f ? 1.f / l : 0.f;
+    const float inv_own = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
@@ -597,16 +615,223 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
     }
 }
 
+// ---------------------------------------------------------------------------
+// The 8-bit cache's converters: three warps turn e4m3 tiles into the f16 operands of
+// the tensor cores, in the slots and the swizzle that the TMA producer would fill.
+//
+// A byte becomes f16 exactly; a block's scale 2^x then enters relative to a common
+// exponent X, as one f16 multiplication by 2^(x - X + kQ8Lift): 448 * 2^7 still fits
+// f16, so all of a byte's bits are kept for blocks down to 2^-22 under the common one.
+// For K, X is the tile's largest exponent (scores below that are 2^-31 of the tile's
+// largest possible). For V, X is the largest of the piece's tiles so far; the softmax
+// warps rescale O when it rises, as they do for the running maximum. Both are told
+// with the K tile, so the softmax knows its V tile's before that is converted.
+// Q rows go to f16 under a power of two that puts their largest element in
+// [2^14, 2^15). Rows behind the last key, and of pages outside the cache, are zero.
+//
+// D / 16 threads take a row, 16 bytes each, and the warps every third group of rows;
+// while a tile is converted the registers are refilled, row by row, with the next
+// one's (K_t, V_t, K_t+1, ...), so a tile's loads have a whole tile's time to arrive. Pages are looked up two tiles
+// ahead, scale bytes one.
+// ---------------------------------------------------------------------------
+constexpr int kQ8Lift = 7;
+
+// 2^e as an f16 pair, e <= 7 (0 below f16's smallest)
+__device__ __forceinline__ uint32_t f16x2_pow2(int e)
+{
+    const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u);
+    return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Byte offset of 16-byte chunk ch (8 f16 columns) of a row in a [half][128 rows][128 B]
+// tile under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t f16_chunk_off(int row, int ch)
+{
+    return (uint32_t)((ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+                                           const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
+                                           int lane)
+{
+    using C = ChunkCfg<D, NQ, true>;
+    constexpr int LPR = D / 16;          // threads per row
+    constexpr int RPW = 32 / LPR;        // rows per warp and pass
+    constexpr int STEP = RPW * C::kConverters;
+    constexpr int NP = (128 + STEP - 1) / STEP;   // passes per tile; the last one is not every warp's
+    volatile int *abort = &bars->abort;
+    const int c = lane % LPR, r0 = cw * RPW + lane / LPR;
+    const int lg_page = p.q8.lg_page, lg_sb = p.q8.lg_sb, pmask = p.page_size - 1;
+    uint32_t q_uses = 0, slot_it = 0, tile = 0;
+    for (int it = it_begin; it < it_end && !__any_sync(0xffffffffu, *abort != 0); ++it) {
+        const PrefillItem w = items[it];
+        const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
+        const int s_len = p.seq_lens[w.r];
+        const int q_len = p.query_lens[w.r];
+        const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
+        // lane l: the page of the eight keys from kt * 128 + 8 (l & 15) on, -1 for none
+        auto page_of = [&](int kt) -> int {
+            const int key = kt * 128 + 8 * (lane & 15);
+            int pg = -1;
+            if (kt < w.kt1 && key < s_len) {
+                pg = __ldg(bt_row + (key >> lg_page));
+                if (pg < 0 || pg >= p.num_pages) {
+                    set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                    pg = -1;
+                }
+            }
+            return pg;
+        };
+        // their scale bytes, K's in the low half
+        auto scales_of = [&](int kt, int pg) -> uint32_t {
+            if (pg < 0)
+                return 0u;
+            const int key = kt * 128 + 8 * (lane & 15);
+            const int64_t at = (((int64_t)pg * p.num_kv_heads + kvh) << (lg_page - lg_sb)) + ((key & pmask) >> lg_sb);
+            return (uint32_t)__ldg(p.q8.ks + at) | (uint32_t)__ldg(p.q8.vs + at) << 16;
+        };
+        // this thread's 16 bytes of pass i of K or V tile kt, whose pages are pgs
+        auto load = [&](const uint8_t *base, int kt, int pgs, int i) -> uint4 {
+            const int row = r0 + STEP * i, key = kt * 128 + row;
+            const int pg = __shfl_sync(0xffffffffu, pgs, (row >> 3) & 15);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < 128 && pg >= 0 && key < s_len)
+                v = __ldg(reinterpret_cast<const uint4 *>(
+                    base + ((((int64_t)pg * p.num_kv_heads + kvh) << lg_page) + (key & pmask)) * D + 16 * c));
+            return v;
+        };
+        int pg0 = page_of(w.kt0), pg1 = page_of(w.kt0 + 1);
+        uint32_t sc0 = scales_of(w.kt0, pg0);
+        uint4 buf[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) buf[i] = load(p.q8.k, w.kt0, pg0, i);
+
+        // Q, head by head: rows of this thread's columns 16 c .. 16 c + 15
+        if (q_uses > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (q_uses - 1) & 1, abort)))
+            break;
+        int8_t *qe = q8t->qe[q_uses & 1];
+        ++q_uses;
+        const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
+#pragma unroll 1
+        for (int n = 0; n < NQ; ++n) {
+            const int h = kvh * p.group + hp * NQ + n;
+            uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
+#pragma unroll 2
+            for (int i = 0; i < NP; ++i) {
+                const int row = r0 + STEP * i;
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (row < 128 && w.i0 + row < q_len) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
+                    a = __ldg(src);
+                    b = __ldg(src + 1);
+                }
+                float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int e = q_exponent(m);
+                const float f = exp2i(-e);
+                if (row >= 128)
+                    continue;
+                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
+                    make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
+                               bf16x2_to_f16x2(a.w, f));
+                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
+                    make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
+                               bf16x2_to_f16x2(b.w, f));
+                if (c == 0)
+                    qe[n * 128 + row] = (int8_t)e;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars->q_full);
+
+        int X = -126;
+        bool ok = true;
+        for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
+            const int pg2 = page_of(kt + 2);
+            const uint32_t sc1 = scales_of(kt + 1, pg1);
+            // exponents of this tile's groups of eight keys, and the common ones
+            const int kxl = q8_exp(sc0 & 0xffu), vxl = q8_exp(sc0 >> 16);
+            const int KX = __reduce_max_sync(0xffffffffu, pg0 >= 0 ? kxl : -126);
+            X = max(X, __reduce_max_sync(0xffffffffu, pg0 >= 0 ? vxl : -126));
+            const uint32_t fk = f16x2_pow2(min(kxl - KX, 0) + kQ8Lift), fv = f16x2_pow2(min(vxl - X, 0) + kQ8Lift);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slot = slot_it % C::kSlots;
+                if (slot_it >= (uint32_t)C::kSlots &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1, abort))) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *dst = smem + C::kSlotOff + slot * C::kTileBytes;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int row = r0 + STEP * i;
+                    const uint32_t f = __shfl_sync(0xffffffffu, kv == 0 ? fk : fv, (row >> 3) & 15);
+                    const uint32_t x[4] = {buf[i].x, buf[i].y, buf[i].z, buf[i].w};
+                    // the next tile's row takes the place of this one
+                    buf[i] = kv == 0 ? load(p.q8.v, kt, pg0, i) : load(p.q8.k, kt + 1, pg1, i);
+                    if (row >= 128)
+                        continue;
+                    uint32_t y[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
+                        y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
+                    }
+                    // the two stores in an order that keeps eight threads of a row on different banks
+                    const int first = (D == 128 && c >= 4) ? 1 : 0;
+                    const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + first)) = first ? hi : lo;
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1 - first)) = first ? lo : hi;
+                }
+                if (kv == 0 && cw == 0 && lane == 0) {
+                    q8t->kx[tile & 7] = KX;
+                    q8t->vx[tile & 7] = X;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars->slot_full[slot]);
+                ++slot_it;
+            }
+            pg0 = pg1;
+            pg1 = pg2;
+            sc0 = sc1;
+        }
+        if (!ok)
+            break;
+    }
+}
+
 // SELF: a batch of one prefill request, planned by the kernel itself (pieces in
 // shared memory); else the plan kernel's lists in the workspace.
-template <int D, int NQ, bool SELF>
-__global__ void __launch_bounds__(352, 1)
+// Q8: over the 8-bit cache. The CTA is then 384 threads: warps 0..7 softmax, 8..10
+// converters (Q and the K/V tiles, through registers, in place of the TMA producer; 10
+// the self plan first), 11 the tcgen05 issuer. Operands are f16 instead of bf16 (see
+// q8_convert); the factors that this leaves out (per q row, K tile and piece) are
+// powers of two and go into the softmax's scale and the final 1 / l. (A fourth
+// converter warp would bring the CTA to 13 warps and every thread to 152 registers;
+// moving registers between groups of four warps instead spilled over 2 KB a thread.)
+template <int D, int NQ, bool SELF, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 384 : 352, 1)
 chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                   const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_v4)
 {
-    using C = ChunkCfg<D, NQ>;
+    using C = ChunkCfg<D, NQ, Q8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
@@ -614,7 +839,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     if (threadIdx.x == 0) {
         // a K or V tile is filled by the producer's issuer lanes, one arrival each
         const uint32_t issuers = (uint32_t)(128 / (p.page_size < 128 ? p.page_size : 128)) * C::kHalves;
-        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_full, Q8 ? C::kConverters : 1);
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->tail, issuers);
         mbar_init(&bars->drain, 1);
@@ -624,7 +849,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             mbar_init(&bars->o_done[n], 1);
         }
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(&bars->slot_full[s], issuers);
+            mbar_init(&bars->slot_full[s], Q8 ? (uint32_t)C::kConverters : issuers);
             mbar_init(&bars->slot_empty[s], 1);
         }
         mbar_init(&bars->stage, 1);
@@ -633,14 +858,16 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         fence_barrier_init();
     }
     if (warp == C::kLoadWarp && lane == 0) {
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
+        if (!Q8) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
         if (D == 128 && p.out_tma)
             tma_prefetch_desc(&tm_o);
-        if (D == 128 && p.page_size < 128)
+        if (!Q8 && D == 128 && p.page_size < 128)
             tma_prefetch_desc(&tm_v4);
-        if (p.fused) {
+        if (!Q8 && p.fused) {
             tma_prefetch_desc(&tm_kn);
             tma_prefetch_desc(&tm_vn);
         }
@@ -661,7 +888,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         if (warp == C::kWriteWarp) {
             const SelfPlanArgs a{p.query_lens, p.seq_lens, p.dev_err, p.num_tokens, p.max_blocks, p.page_size,
                                  p.group, p.num_kv_heads, p.fused, p.split_ok, p.split_clamped};
-            const int n = self_plan_run<NQ>(a, s_items, lane);
+            const int n = self_plan_run<NQ, C::kPlanCap>(a, s_items, lane);
             if (lane == 0) {
                 bars->it_begin = 0;
                 bars->it_end = n;
@@ -682,7 +909,11 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     // first row of a request in q / out (a self-planned batch has one request)
     auto row0 = [&](int r) -> int { return SELF ? 0 : p.cu_q[r]; };
 
-    if (warp == C::kLoadWarp) {
+    Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
+    if (Q8 && warp >= C::kLoadWarp && warp < C::kLoadWarp + C::kConverters) {
+        if constexpr (Q8)
+            q8_convert<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, SELF, warp - C::kLoadWarp, lane);
+    } else if (!Q8 && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ producer
         const int PB = p.page_size < 128 ? p.page_size : 128;   // rows per TMA box
         const int NB = 128 / PB;                                 // boxes per tile
@@ -825,7 +1056,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         // ------------------------------------------------------------ cache writer
         // Independent of the attention pipeline: it reads the new rows itself,
         // one K or V tile at a time, through its own buffer and barrier.
-        if (p.fused) {
+        if (!Q8 && p.fused) {
             uint8_t *stage = smem + C::kStageOff;
             uint32_t stage_uses = 0;
             bool ok = true;
@@ -927,8 +1158,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         // The whole warp walks the loop; every MMA and commit is issued by one
         // lane from an elect.sync branch. Waits are polled by all lanes and their
         // verdicts combined, so the warp stays converged.
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
+        constexpr uint32_t idesc_qk = Q8 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
+        constexpr uint32_t idesc_pv = Q8 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
         const uint32_t q_addr = smem_u32(smem + C::kQOff);
         const uint32_t slot_addr = smem_u32(smem + C::kSlotOff);
         uint32_t q_uses = 0, slot_it = 0, p_uses[2] = {0, 0};
@@ -957,7 +1188,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         // at page 8). Otherwise [half][128 rows][128 B].
         const int pg = p.page_size < 128 ? p.page_size : 128;
         const int lg_pg = __ffs(pg) - 1;
-        const bool v_pages = D == 128 && pg < 128;
+        const bool v_pages = !Q8 && D == 128 && pg < 128;
         auto issue_pv = [&](int n, int slot, bool acc, bool pm) {
 #pragma unroll
             for (int kk = 0; kk < 128 / 16; ++kk) {
@@ -1056,7 +1287,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         const uint32_t tS = tmem + lane_base + C::s_col(wg);
         const uint32_t tO = tmem + lane_base + C::o_col(wg);
         const float sl2 = p.scale_log2;
-        uint32_t s_uses = 0, o_base = 0;
+        uint32_t s_uses = 0, o_base = 0;   // s_uses: also the ordinal of the next tile
         for (int it = it_begin; it < it_end && !*abort; ++it) {
             const PrefillItem w = items[it];
             const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
@@ -1072,6 +1303,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const int limit_hist = p.fused ? hist - 1 : limit;
             const int n = w.kt1 - w.kt0;
             float m_use = -INFINITY, l = 0.f;
+            float q_sl2 = sl2;       // Q8: with the q row's exponent
+            int vx = 0;              // Q8: O stands for O * 2^(vx - kQ8Lift)
             bool ok = true;
             for (int t = 0; t < n; ++t) {
                 const int kt = w.kt0 + t;
@@ -1080,6 +1313,18 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 const int lim = from_new ? limit : limit_hist;
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], s_uses & 1, abort))))
                     break;
+                float tsl2 = sl2, xs = 1.f;
+                if constexpr (Q8) {
+                    const volatile Q8Tiles *qt = q8t;
+                    if (t == 0)
+                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]);
+                    // never 0 or infinite: a masked score times it stays -inf, a zero one 0
+                    tsl2 = fminf(fmaxf(q_sl2 * exp2i(qt->kx[s_uses & 7] - kQ8Lift), 1.2e-38f), 3.0e38f);
+                    const int x = qt->vx[s_uses & 7];
+                    if (t > 0)
+                        xs = exp2i(max(vx - x, -126));
+                    vx = x;
+                }
                 ++s_uses;
                 tc_fence_after_sync();
                 // the S row straight from TMEM: four loads, one wait
@@ -1106,16 +1351,20 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         for (int c = 0; c < 4; ++c) mc[c] = fmax3(mc[c], SV(x + c), SV(x + 4 + c));
                     mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
                 }
-                const float m_tile = mx * sl2;
-                const bool need = m_tile > m_use + 8.f;
+                const float m_tile = mx * tsl2;
+                bool need = m_tile > m_use + 8.f;
                 float alpha = 1.f;
                 if (need) {
                     alpha = ex2_approx(m_use - m_tile);   // m_use = -inf gives 0
                     l *= alpha;
                     m_use = m_tile;
                 }
+                if constexpr (Q8) {
+                    alpha *= xs;                          // O under the tile's value exponent
+                    need = need || xs != 1.f;
+                }
                 const float mref = m_use == -INFINITY ? 0.f : m_use;
-                const uint64_t sl2x2 = f2_pack(sl2, sl2);
+                const uint64_t sl2x2 = f2_pack(tsl2, tsl2);
                 const uint64_t nref2 = f2_pack(-mref, -mref);
                 uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -1136,7 +1385,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         }
                         const uint64_t p2 = f2_pack(a, b);
                         sum2 = f2_add(sum2, p2);
-                        pk[x] = pack_bf16x2(a, b);
+                        pk[x] = Q8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
                     }
                     tmem_st32(tS + 32 * hh, pk);
                 }
@@ -1177,6 +1426,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const bool valid_row = i < q_len;
             const int64_t t_row = (int64_t)row0(w.r) + i;
             const int npieces = w.piece_np >> 16;
+            float own_f = 1.f;
+            if constexpr (Q8)
+                own_f = exp2i(max(vx - kQ8Lift, -126));
             if (npieces > 1) {
                 // A piece of a split unit. Every warp (32 rows) decides on its own:
                 // at the end of its CTA's run, if every other piece has left its
@@ -1210,7 +1462,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 seen = __shfl_sync(0xffffffffu, seen, 0);
                 bool merge = seen == npieces - 1;
                 if (!merge) {
-                    const float inv_own = l > 0.f ? 1.f / l : 0.f;
+                    const float inv_own = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
                     uint4 *dst = ph + (int64_t)(piece * NQ + wg) * (D / 8) * 128 + row;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
@@ -1247,15 +1499,15 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         // the merged rows through the writer's buffer once the writer is done with it
                         const bool ostaged = staged && p.out_tma &&
                                              (!p.fused || __all_sync(0xffffffffu, mbar_wait(&bars->writer_done, 0, abort)));
-                        merge_split_row<D, NQ>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
+                        merge_split_row<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
                                                out_off,
                                                staged ? reinterpret_cast<uint4 *>(smem + (wg * 4 + sub) * kMergeStageBytes)
                                                       : nullptr,
                                                ostaged ? smem + C::kStageOff + (wg * 4 + sub) * 4096 : nullptr, &tm_o, h,
-                                               (int)(t_row - lane));
+                                               (int)(t_row - lane), own_f);
                     } else {
-                        merge_split_row_any<D, NQ>(p, tO, pml, ph, piece, npieces, wg, row, m_use, l, valid_row,
-                                                   out_off);
+                        merge_split_row_any<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, m_use, l, valid_row,
+                                                       out_off, own_f);
                     }
                     // Every other piece has counted in, so no one else touches the
                     // counter in this call: the merging warp clears it. A later call
@@ -1274,7 +1526,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // its valid rows directly. (Planned batches hold many units per
                 // run; the self-planned kernel, with few, stores directly: staging
                 // measured slower there.)
-                const float inv_l = l > 0.f ? 1.f / l : 0.f;
+                const float inv_l = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
                 // with the KV write, once the cache writer has released its buffer
                 const bool writer_idle =
                     !p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0);
@@ -1329,10 +1581,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 }
             } else if (SELF && D == 128 && p.out_tma &&
                        (!p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0))) {
-                store_unit_rows_staged<D>(tO, l, valid_row, smem + C::kStageOff + (wg * 4 + sub) * 4096, &tm_o,
+                store_unit_rows_staged<D, Q8>(tO, l, own_f, valid_row, smem + C::kStageOff + (wg * 4 + sub) * 4096, &tm_o,
                                           reinterpret_cast<__nv_bfloat16 *>(p.out), t_row, h, p.num_q_heads, lane);
             } else {
-                const float inv_l = l > 0.f ? 1.f / l : 0.f;
+                const float inv_l = (l > 0.f ? 1.f / l : 0.f) * (Q8 ? own_f : 1.f);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[32];
@@ -1376,7 +1628,7 @@ cudaError_t launch_chunk_t(const ChunkParams &p, const CUtensorMap &tq, const CU
 {
     using C = ChunkCfg<D, NQ>;
     static std::atomic<uint64_t> done_self{0}, done_plan{0};
-    auto k = p.self_plan ? chunk_attn_kernel<D, NQ, true> : chunk_attn_kernel<D, NQ, false>;
+    auto k = p.self_plan ? chunk_attn_kernel<D, NQ, true, false> : chunk_attn_kernel<D, NQ, false, false>;
     return launch_with_smem(p.self_plan ? done_self : done_plan, reinterpret_cast<const void *>(k), C::kSmemBytes,
                             [&] {
                                 return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, tq,
@@ -1384,7 +1636,28 @@ cudaError_t launch_chunk_t(const ChunkParams &p, const CUtensorMap &tq, const CU
                             });
 }
 
+template <int D, int NQ>
+cudaError_t launch_chunk_q8_t(const ChunkParams &p, const CUtensorMap &to, int grid, cudaStream_t s, bool early)
+{
+    using C = ChunkCfg<D, NQ, true>;
+    static std::atomic<uint64_t> done_self{0}, done_plan{0};
+    auto k = p.self_plan ? chunk_attn_kernel<D, NQ, true, true> : chunk_attn_kernel<D, NQ, false, true>;
+    return launch_with_smem(p.self_plan ? done_self : done_plan, reinterpret_cast<const void *>(k), C::kSmemBytes,
+                            [&] {
+                                return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, to,
+                                                  to, to, to, to, to, to);
+                            });
+}
+
 }  // namespace
+
+cudaError_t launch_chunk_q8(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
+                            cudaStream_t s, bool early)
+{
+    if (head_dim == 128)
+        return nq == 2 ? launch_chunk_q8_t<128, 2>(p, to, grid, s, early) : launch_chunk_q8_t<128, 1>(p, to, grid, s, early);
+    return nq == 2 ? launch_chunk_q8_t<64, 2>(p, to, grid, s, early) : launch_chunk_q8_t<64, 1>(p, to, grid, s, early);
+}
 
 cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                               const CUtensorMap &tv, const CUtensorMap &tkn, const CUtensorMap &tvn,
