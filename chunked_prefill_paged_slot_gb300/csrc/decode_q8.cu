@@ -67,13 +67,6 @@ struct Q8DecBars {
     int abort;
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
 __device__ __forceinline__ uint2 lds64(uint32_t a)
 {
     uint2 v;

@@ -66,6 +66,8 @@ constexpr int kFmaExpPairsPer8 = CPSA_FMA_EXP_PAIRS_PER_8;
 constexpr int kMergeMaxOthers = 3;
 constexpr int kMergeStageBytes = kMergeMaxOthers * 32 * 128 * 2;
 
+constexpr int kQ8Stages = 4;   // e4m3 tiles on their way (see q8_convert)
+
 // Over the 8-bit cache the kernel has another cast of warps (see chunk_attn_kernel)
 // and keeps a little more in shared memory, so fewer self-planned pieces.
 template <int D, int NQ, bool Q8 = false>
@@ -73,19 +75,19 @@ struct ChunkCfg {
     static constexpr int kHalves = D / 64;             // 128-byte swizzle atoms across a row
     static constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16
     static constexpr int kTileBytes = kHalves * kHalfBytes;
-    static constexpr int kSlots = D == 128 ? 4 : 8;
+    static constexpr int kSlots = D == 128 ? (Q8 ? 3 : 4) : 8;
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = NQ * kTileBytes;
-    static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer
-    static constexpr int kBarOff = kStageOff + kTileBytes;
+    static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer (Q8: e4m3 tiles)
+    static constexpr int kBarOff = kStageOff + (Q8 ? kQ8Stages * 128 * D : kTileBytes);
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
     static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
     static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
     static constexpr int kBarBytes = 256 + kSelfPlanCap * 32;  // barriers + pieces (+ Q8Tiles)
     static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
-    static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= kSlotOff + kSlots * kTileBytes,
-                  "the staged merge uses the Q and K/V buffers");
+    static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= (Q8 ? kBarOff : kStageOff),
+                  "the staged merge uses the Q and K/V buffers (Q8: and the e4m3 tiles')");
     static constexpr int kThreads = Q8 ? 384 : 352;            // both leave 168 registers a thread
     static constexpr int kLoadWarp = 8;                        // Q8: to kLoadWarp + kConverters - 1
     static constexpr int kConverters = 3;
@@ -115,6 +117,7 @@ struct ChunkBars {
 struct Q8Tiles {
     int kx[8], vx[8];
     int8_t qe[2][256];
+    uint64_t full[3][kQ8Stages];   // per converter warp: its rows of an e4m3 tile have landed
 };
 static_assert(sizeof(Q8Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32, "in place of the pieces it gave up");
 static_assert(sizeof(ChunkBars) <= 256, "the self-planned pieces follow the barriers at +256");
@@ -616,6 +619,9 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 }
 
 // ---------------------------------------------------------------------------
+// The first group of eight rows of converter warp cw's share of a tile (16 groups).
+__host__ __device__ constexpr int q8_first_group(int cw) { return cw == 0 ? 0 : 1 + 5 * cw; }
+
 // The 8-bit cache's converters: three warps turn e4m3 tiles into the f16 operands of
 // the tensor cores, in the slots and the swizzle that the TMA producer would fill.
 //
@@ -629,10 +635,16 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 // Q rows go to f16 under a power of two that puts their largest element in
 // [2^14, 2^15). Rows behind the last key, and of pages outside the cache, are zero.
 //
-// D / 16 threads take a row, 16 bytes each, and the warps every third group of rows;
-// while a tile is converted the registers are refilled, row by row, with the next
-// one's (K_t, V_t, K_t+1, ...), so a tile's loads have a whole tile's time to arrive. Pages are looked up two tiles
-// ahead, scale bytes one.
+// The e4m3 rows come by bulk copies kQ8Stages half-tiles (K_t, V_t, K_t+1, ...) ahead. A
+// warp owns 48 or 40 consecutive rows of every tile and copies, waits for and converts
+// them alone: the warps meet only at the slots' barriers. A copy is all its rows that
+// share a page (contiguous for a head). Pages are looked up three tiles ahead, scale
+// bytes two. Per 16 bytes a thread spends one load, four extractions, eight
+// conversions, eight multiplications and two stores; a 512-token chunk at history 32256
+// (32/8 heads, D 128) takes @@MEAS@@
+// (Taking the rows straight from global memory into registers cost 10.6k clocks a tile,
+// mostly addresses; bulk copies of eight rows each, one after the other from their
+// lanes, and per-thread selects between the two stores 7.0k.)
 // ---------------------------------------------------------------------------
 constexpr int kQ8Lift = 7;
 
@@ -663,138 +675,196 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                                            int lane)
 {
     using C = ChunkCfg<D, NQ, true>;
-    constexpr int LPR = D / 16;          // threads per row
-    constexpr int RPW = 32 / LPR;        // rows per warp and pass
-    constexpr int STEP = RPW * C::kConverters;
-    constexpr int NP = (128 + STEP - 1) / STEP;   // passes per tile; the last one is not every warp's
+    constexpr int NC = C::kConverters;
+    constexpr int RPW = 512 / D;         // rows per warp and pass: 4 or 8
+    constexpr int NP = 8 / RPW;          // passes per group of eight rows
+    constexpr uint32_t kGroupBytes = 8 * D;
     volatile int *abort = &bars->abort;
-    const int c = lane % LPR, r0 = cw * RPW + lane / LPR;
+    // this thread's row within a pass and its 16 columns 16 c ..: eight threads in a row
+    // (of the warp) read 128 consecutive bytes, or the opposite halves of two rows, and
+    // store to eight different 16-byte banks of the swizzled tile
+    const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;
+    const int c = D == 128 ? (lane & 3) + 4 * ((r0 & 1) ^ (lane >> 4)) : lane & 3;
+    const int g0 = q8_first_group(cw), g1 = q8_first_group(cw + 1);
     const int lg_page = p.q8.lg_page, lg_sb = p.q8.lg_sb, pmask = p.page_size - 1;
-    uint32_t q_uses = 0, slot_it = 0, tile = 0;
+    // lane l stands for the group of rows 8 l ..; the first of a page, or of the warp's
+    // share, copies all that follow in the same page and share
+    const bool copier = lane >= g0 && lane < g1 && (lane == g0 || ((8 * lane) & pmask) == 0);
+    const uint32_t copy_bytes =
+        (uint32_t)(min(g1, ((8 * lane | pmask) + 1) >> 3) - lane) * kGroupBytes;
+    uint8_t *stages = smem + C::kStageOff;
+    // swizzled offsets of this thread's two f16 chunks in pass q of a group
+    uint32_t off0[NP], off1[NP];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        off0[q] = f16_chunk_off(r0 + RPW * q, 2 * c);
+        off1[q] = f16_chunk_off(r0 + RPW * q, 2 * c + 1);
+    }
+    uint32_t q_uses = 0, slot_it = 0, tile = 0, issued = 0;   // issued, slot_it: half-tiles
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    };
     for (int it = it_begin; it < it_end && !__any_sync(0xffffffffu, *abort != 0); ++it) {
         const PrefillItem w = items[it];
         const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
         const int s_len = p.seq_lens[w.r];
         const int q_len = p.query_lens[w.r];
         const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
-        // lane l: the page of the eight keys from kt * 128 + 8 (l & 15) on, -1 for none
+        const int key_l = 8 * (lane & 15);
+        // lane l: the page of its group in tile kt as it stands in the table, -1 where there is none
         auto page_of = [&](int kt) -> int {
-            const int key = kt * 128 + 8 * (lane & 15);
-            int pg = -1;
-            if (kt < w.kt1 && key < s_len) {
-                pg = __ldg(bt_row + (key >> lg_page));
-                if (pg < 0 || pg >= p.num_pages) {
-                    set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                    pg = -1;
-                }
+            const int key = kt * 128 + key_l;
+            return kt < w.kt1 && key < s_len ? ldg_here(bt_row + (key >> lg_page)) : -1;
+        };
+        auto checked = [&](int kt, int pg) -> int {
+            if (kt < w.kt1 && kt * 128 + key_l < s_len && (pg < 0 || pg >= p.num_pages)) {
+                set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                return -1;
             }
             return pg;
         };
-        // their scale bytes, K's in the low half
-        auto scales_of = [&](int kt, int pg) -> uint32_t {
+        auto scales_of = [&](int kt, int pg) -> uint32_t {    // K's in the low half
             if (pg < 0)
                 return 0u;
-            const int key = kt * 128 + 8 * (lane & 15);
+            const int key = kt * 128 + key_l;
             const int64_t at = (((int64_t)pg * p.num_kv_heads + kvh) << (lg_page - lg_sb)) + ((key & pmask) >> lg_sb);
-            return (uint32_t)__ldg(p.q8.ks + at) | (uint32_t)__ldg(p.q8.vs + at) << 16;
+            return ldg_here(p.q8.ks + at) | ldg_here(p.q8.vs + at) << 16;
         };
-        // this thread's 16 bytes of pass i of K or V tile kt, whose pages are pgs
-        auto load = [&](const uint8_t *base, int kt, int pgs, int i) -> uint4 {
-            const int row = r0 + STEP * i, key = kt * 128 + row;
-            const int pg = __shfl_sync(0xffffffffu, pgs, (row >> 3) & 15);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < 128 && pg >= 0 && key < s_len)
-                v = __ldg(reinterpret_cast<const uint4 *>(
-                    base + ((((int64_t)pg * p.num_kv_heads + kvh) << lg_page) + (key & pmask)) * D + 16 * c));
-            return v;
-        };
-        int pg0 = page_of(w.kt0), pg1 = page_of(w.kt0 + 1);
-        uint32_t sc0 = scales_of(w.kt0, pg0);
-        uint4 buf[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) buf[i] = load(p.q8.k, w.kt0, pg0, i);
-
-        // Q, head by head: rows of this thread's columns 16 c .. 16 c + 15
-        if (q_uses > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (q_uses - 1) & 1, abort)))
-            break;
-        int8_t *qe = q8t->qe[q_uses & 1];
-        ++q_uses;
-        const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
-#pragma unroll 1
-        for (int n = 0; n < NQ; ++n) {
-            const int h = kvh * p.group + hp * NQ + n;
-            uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
-#pragma unroll 2
-            for (int i = 0; i < NP; ++i) {
-                const int row = r0 + STEP * i;
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (row < 128 && w.i0 + row < q_len) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
-                    a = __ldg(src);
-                    b = __ldg(src + 1);
+        // this warp's rows of K and V tile kt, pages pg, into the next two stages (kQ8Stages is
+        // even); each lane announces its own copy's bytes right before it issues it
+        auto issue = [&](int kt, int pg) {
+            const int st = issued % kQ8Stages;
+            if (copier) {
+                uint64_t *bar = &q8t->full[cw][st];    // V's is the next
+                if (pg >= 0) {
+                    const int64_t row = (((int64_t)pg * p.num_kv_heads + kvh) << lg_page) + ((kt * 128 + key_l) & pmask);
+                    uint8_t *dst = stages + st * (128 * D) + lane * kGroupBytes;
+                    mbar_arrive_expect_tx(bar, copy_bytes);
+                    bulk_load(dst, p.q8.k + row * D, copy_bytes, bar);
+                    mbar_arrive_expect_tx(bar + 1, copy_bytes);
+                    bulk_load(dst + 128 * D, p.q8.v + row * D, copy_bytes, bar + 1);
+                } else {
+                    mbar_arrive(bar);
+                    mbar_arrive(bar + 1);
                 }
-                float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int e = q_exponent(m);
-                const float f = exp2i(-e);
-                if (row >= 128)
-                    continue;
-                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
-                    make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
-                               bf16x2_to_f16x2(a.w, f));
-                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
-                    make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
-                               bf16x2_to_f16x2(b.w, f));
-                if (c == 0)
-                    qe[n * 128 + row] = (int8_t)e;
             }
+            issued += 2;
+        };
+        int pg0 = page_of(w.kt0), pg1 = page_of(w.kt0 + 1), pg2 = page_of(w.kt0 + 2);
+        pg0 = checked(w.kt0, pg0);
+        issue(w.kt0, pg0);
+        pg1 = checked(w.kt0 + 1, pg1);
+        if (w.kt0 + 1 < w.kt1)
+            issue(w.kt0 + 1, pg1);
+        uint32_t sc0 = scales_of(w.kt0, pg0), sc1 = scales_of(w.kt0 + 1, pg1);
+
+        // Q, head by head: rows r of this thread's columns 16 c .. 16 c + 15
+        bool ok = q_uses == 0 || wait(&bars->q_empty, (q_uses - 1) & 1);
+        if (ok) {
+            int8_t *qe = q8t->qe[q_uses & 1];
+            ++q_uses;
+            const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
+#pragma unroll 1
+            for (int n = 0; n < NQ; ++n) {
+                const int h = kvh * p.group + hp * NQ + n;
+                uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
+#pragma unroll 4
+                for (int r8 = cw * RPW; r8 < 128; r8 += NC * RPW) {
+                    const int row = r8 + r0;
+                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                    if (w.i0 + row < q_len) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
+                        a = __ldg(src);
+                        b = __ldg(src + 1);
+                    }
+                    float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
+#pragma unroll
+                    for (int o = 1; o <= 2; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    if (D == 128)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    const int e = q_exponent(m);
+                    const float f = exp2i(-e);
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
+                        make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
+                                   bf16x2_to_f16x2(a.w, f));
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
+                        make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
+                                   bf16x2_to_f16x2(b.w, f));
+                    if (c == 0)
+                        qe[n * 128 + row] = (int8_t)e;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars->q_full);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&bars->q_full);
 
         int X = -126;
-        bool ok = true;
         for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
-            const int pg2 = page_of(kt + 2);
-            const uint32_t sc1 = scales_of(kt + 1, pg1);
+            const int pg3 = page_of(kt + 3);
+            pg2 = checked(kt + 2, pg2);
+            const uint32_t sc2 = scales_of(kt + 2, pg2);
             // exponents of this tile's groups of eight keys, and the common ones
             const int kxl = q8_exp(sc0 & 0xffu), vxl = q8_exp(sc0 >> 16);
             const int KX = __reduce_max_sync(0xffffffffu, pg0 >= 0 ? kxl : -126);
             X = max(X, __reduce_max_sync(0xffffffffu, pg0 >= 0 ? vxl : -126));
             const uint32_t fk = f16x2_pow2(min(kxl - KX, 0) + kQ8Lift), fv = f16x2_pow2(min(vxl - X, 0) + kQ8Lift);
-#pragma unroll
+            const uint32_t there = __ballot_sync(0xffffffffu, pg0 >= 0);
+            const int nlive = s_len - kt * 128;
+            const bool whole = nlive >= 128 && (there & 0xffffu) == 0xffffu;
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
+                const int st = slot_it % kQ8Stages;
                 const int slot = slot_it % C::kSlots;
-                if (slot_it >= (uint32_t)C::kSlots &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1, abort))) {
-                    ok = false;
+                const uint32_t fl = kv == 0 ? fk : fv;
+                ok = wait(&q8t->full[cw][st], (slot_it / kQ8Stages) & 1);
+                if (ok && slot_it >= (uint32_t)C::kSlots)
+                    ok = wait(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1);
+                if (!ok)
                     break;
-                }
-                uint8_t *dst = smem + C::kSlotOff + slot * C::kTileBytes;
+                const uint32_t src = smem_u32(stages) + st * (128 * D) + r0 * D + 16 * c;
+                const uint32_t dst = smem_u32(smem + C::kSlotOff) + slot * C::kTileBytes;
+                // three groups at a time, all their loads first: a load cannot pass an earlier
+                // store by itself, and a lone warp hides latency only behind its own
+                // instructions (a group at a time 890 clocks a half-tile of six groups on an
+                // otherwise idle SM, three 560, six no better; unrolled further, the straight-line
+                // code runs at the rate of instruction fetch)
+#pragma unroll 1
+                for (int ga = g0; ga < g1; ga += 3) {
+                    uint4 v[3][NP];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int row = r0 + STEP * i;
-                    const uint32_t f = __shfl_sync(0xffffffffu, kv == 0 ? fk : fv, (row >> 3) & 15);
-                    const uint32_t x[4] = {buf[i].x, buf[i].y, buf[i].z, buf[i].w};
-                    // the next tile's row takes the place of this one
-                    buf[i] = kv == 0 ? load(p.q8.v, kt, pg0, i) : load(p.q8.k, kt + 1, pg1, i);
-                    if (row >= 128)
-                        continue;
-                    uint32_t y[8];
+                    for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
-                        y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
+                        for (int q = 0; q < NP; ++q)
+                            v[i][q] = lds128(src + min(ga + i, g1 - 1) * kGroupBytes + q * RPW * D);
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+#pragma unroll
+                            for (int q = 0; q < NP; ++q)
+                                if (8 * (ga + i) + RPW * q + r0 >= nlive || !((there >> (ga + i)) & 1u))
+                                    v[i][q] = make_uint4(0, 0, 0, 0);
                     }
-                    // the two stores in an order that keeps eight threads of a row on different banks
-                    const int first = (D == 128 && c >= 4) ? 1 : 0;
-                    const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + first)) = first ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1 - first)) = first ? lo : hi;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t f = __shfl_sync(0xffffffffu, fl, (ga + i) & 15);
+                        if (ga + i >= g1)
+                            break;
+#pragma unroll
+                        for (int q = 0; q < NP; ++q) {
+                            const uint32_t x[4] = {v[i][q].x, v[i][q].y, v[i][q].z, v[i][q].w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
+                                y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
+                            }
+                            sts128(dst + (ga + i) * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
+                            sts128(dst + (ga + i) * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
+                        }
+                    }
                 }
                 if (kv == 0 && cw == 0 && lane == 0) {
                     q8t->kx[tile & 7] = KX;
@@ -806,13 +876,32 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                     mbar_arrive(&bars->slot_full[slot]);
                 ++slot_it;
             }
+            // both stages are read: the tile after the next
+            if (ok && kt + 2 < w.kt1)
+                issue(kt + 2, pg2);
             pg0 = pg1;
             pg1 = pg2;
+            pg2 = pg3;
             sc0 = sc1;
+            sc1 = sc2;
         }
-        if (!ok)
+        if (!ok) {
+            // given up on a wait: let the copies in flight land before the CTA can end
+            const uint64_t t0 = global_timer_ns();
+            for (; slot_it < issued; ++slot_it)
+                while (!mbar_try_wait(&q8t->full[cw][slot_it % kQ8Stages], (slot_it / kQ8Stages) & 1) &&
+                       global_timer_ns() - t0 < 100000000ull) {
+                }
             break;
+        }
     }
+}
+
+// Rows leave through the staging buffer by TMA; not with Q8, whose e4m3 tiles take its place.
+template <bool Q8>
+__device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
+{
+    return !Q8 && p.out_tma;
 }
 
 // SELF: a batch of one prefill request, planned by the kernel itself (pieces in
@@ -852,6 +941,15 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             mbar_init(&bars->slot_full[s], Q8 ? (uint32_t)C::kConverters : issuers);
             mbar_init(&bars->slot_empty[s], 1);
         }
+        if (Q8) {
+            Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
+            for (int x = 0; x < C::kConverters; ++x) {
+                // one arrival per copy: the pages that the warp's rows of a tile lie in
+                const int a = 8 * q8_first_group(x), b = 8 * q8_first_group(x + 1) - 1;
+                const int page = p.page_size < 128 ? p.page_size : 128;
+                for (int s = 0; s < kQ8Stages; ++s) mbar_init(&q8t->full[x][s], (uint32_t)(b / page - a / page + 1));
+            }
+        }
         mbar_init(&bars->stage, 1);
         mbar_init(&bars->writer_done, 1);
         bars->abort = 0;
@@ -863,7 +961,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        if (D == 128 && p.out_tma)
+        if (D == 128 && rows_by_tma<Q8>(p))
             tma_prefetch_desc(&tm_o);
         if (!Q8 && D == 128 && p.page_size < 128)
             tma_prefetch_desc(&tm_v4);
@@ -1497,7 +1595,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                             staged = NQ == 1 || __all_sync(0xffffffffu, mbar_wait(&bars->o_done[NQ - 1 - wg],
                                                                                   (o_base - 1) & 1, abort));
                         // the merged rows through the writer's buffer once the writer is done with it
-                        const bool ostaged = staged && p.out_tma &&
+                        const bool ostaged = staged && rows_by_tma<Q8>(p) &&
                                              (!p.fused || __all_sync(0xffffffffu, mbar_wait(&bars->writer_done, 0, abort)));
                         merge_split_row<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
                                                out_off,
@@ -1530,7 +1628,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // with the KV write, once the cache writer has released its buffer
                 const bool writer_idle =
                     !p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0);
-                const bool staged = p.out_tma && writer_idle && __all_sync(0xffffffffu, valid_row);
+                const bool staged = rows_by_tma<Q8>(p) && writer_idle && __all_sync(0xffffffffu, valid_row);
                 uint8_t *stg = smem + C::kStageOff + (wg * 4 + sub) * 4096;
 #pragma unroll
                 for (int c2 = 0; c2 < D / 64; ++c2) {
@@ -1579,7 +1677,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         }
                     }
                 }
-            } else if (SELF && D == 128 && p.out_tma &&
+            } else if (SELF && D == 128 && rows_by_tma<Q8>(p) &&
                        (!p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0))) {
                 store_unit_rows_staged<D, Q8>(tO, l, own_f, valid_row, smem + C::kStageOff + (wg * 4 + sub) * 4096, &tm_o,
                                           reinterpret_cast<__nv_bfloat16 *>(p.out), t_row, h, p.num_q_heads, lane);
@@ -1606,7 +1704,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     }
 
     // the softmax warps' output stores are complete before the CTA ends
-    if (D == 128 && warp / 4 < NQ && lane == 0 && p.out_tma)
+    if (D == 128 && warp / 4 < NQ && lane == 0 && rows_by_tma<Q8>(p))
         bulk_wait_group0();
     if (threadIdx.x == 0 && bars->abort)
         set_dev_error(p.dev_err, CPSA_DEV_WAIT_TIMEOUT);
