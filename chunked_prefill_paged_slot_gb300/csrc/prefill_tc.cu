@@ -723,12 +723,16 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
             }
             return pg;
         };
-        auto scales_of = [&](int kt, int pg) -> uint32_t {    // K's in the low half
-            if (pg < 0)
-                return 0u;
-            const int key = kt * 128 + key_l;
-            const int64_t at = (((int64_t)pg * p.num_kv_heads + kvh) << (lg_page - lg_sb)) + ((key & pmask) >> lg_sb);
-            return ldg_here(p.q8.ks + at) | ldg_here(p.q8.vs + at) << 16;
+        // its scale bytes there (two registers, not combined: that would wait for the loads)
+        auto scales_of = [&](int kt, int pg, uint32_t &ks, uint32_t &vs) {
+            ks = vs = 0u;
+            if (pg >= 0) {
+                const int key = kt * 128 + key_l;
+                const int64_t at =
+                    (((int64_t)pg * p.num_kv_heads + kvh) << (lg_page - lg_sb)) + ((key & pmask) >> lg_sb);
+                ks = ldg_here(p.q8.ks + at);
+                vs = ldg_here(p.q8.vs + at);
+            }
         };
         // this warp's rows of K and V tile kt, pages pg, into the next two stages (kQ8Stages is
         // even); each lane announces its own copy's bytes right before it issues it
@@ -756,7 +760,9 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         pg1 = checked(w.kt0 + 1, pg1);
         if (w.kt0 + 1 < w.kt1)
             issue(w.kt0 + 1, pg1);
-        uint32_t sc0 = scales_of(w.kt0, pg0), sc1 = scales_of(w.kt0 + 1, pg1);
+        uint32_t ks0, vs0, ks1, vs1, ks2, vs2;
+        scales_of(w.kt0, pg0, ks0, vs0);
+        scales_of(w.kt0 + 1, pg1, ks1, vs1);
 
         // Q, head by head: rows r of this thread's columns 16 c .. 16 c + 15
         bool ok = q_uses == 0 || wait(&bars->q_empty, (q_uses - 1) & 1);
@@ -805,9 +811,9 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
             const int pg3 = page_of(kt + 3);
             pg2 = checked(kt + 2, pg2);
-            const uint32_t sc2 = scales_of(kt + 2, pg2);
+            scales_of(kt + 2, pg2, ks2, vs2);
             // exponents of this tile's groups of eight keys, and the common ones
-            const int kxl = q8_exp(sc0 & 0xffu), vxl = q8_exp(sc0 >> 16);
+            const int kxl = q8_exp(ks0), vxl = q8_exp(vs0);
             const int KX = __reduce_max_sync(0xffffffffu, pg0 >= 0 ? kxl : -126);
             X = max(X, __reduce_max_sync(0xffffffffu, pg0 >= 0 ? vxl : -126));
             const uint32_t fk = f16x2_pow2(min(kxl - KX, 0) + kQ8Lift), fv = f16x2_pow2(min(vxl - X, 0) + kQ8Lift);
@@ -882,8 +888,10 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
             pg0 = pg1;
             pg1 = pg2;
             pg2 = pg3;
-            sc0 = sc1;
-            sc1 = sc2;
+            ks0 = ks1;
+            vs0 = vs1;
+            ks1 = ks2;
+            vs1 = vs2;
         }
         if (!ok) {
             // given up on a wait: let the copies in flight land before the CTA can end
