@@ -88,10 +88,10 @@ struct ChunkCfg {
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
     static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= (Q8 ? kBarOff : kStageOff),
                   "the staged merge uses the Q and K/V buffers (Q8: and the e4m3 tiles')");
-    static constexpr int kThreads = Q8 ? 384 : 352;            // both leave 168 registers a thread
+    static constexpr int kThreads = Q8 ? 512 : 352;
     static constexpr int kLoadWarp = 8;                        // Q8: to kLoadWarp + kConverters - 1
-    static constexpr int kConverters = 3;
-    static constexpr int kMmaWarp = Q8 ? 11 : 9;
+    static constexpr int kConverters = 4;
+    static constexpr int kMmaWarp = Q8 ? 12 : 9;
     static constexpr int kWriteWarp = 10;
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t s_col(int n) { return (uint32_t)n * 128u; }
@@ -117,7 +117,7 @@ struct ChunkBars {
 struct Q8Tiles {
     int kx[8], vx[8];
     int8_t qe[2][256];
-    uint64_t full[3][kQ8Stages];   // per converter warp: its rows of an e4m3 tile have landed
+    uint64_t full[4][kQ8Stages];   // per converter warp: its rows of an e4m3 tile have landed
 };
 static_assert(sizeof(Q8Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32, "in place of the pieces it gave up");
 static_assert(sizeof(ChunkBars) <= 256, "the self-planned pieces follow the barriers at +256");
@@ -620,9 +620,9 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 
 // ---------------------------------------------------------------------------
 // The first group of eight rows of converter warp cw's share of a tile (16 groups).
-__host__ __device__ constexpr int q8_first_group(int cw) { return cw == 0 ? 0 : 1 + 5 * cw; }
+__host__ __device__ constexpr int q8_first_group(int cw) { return 4 * cw; }
 
-// The 8-bit cache's converters: three warps turn e4m3 tiles into the f16 operands of
+// The 8-bit cache's converters: four warps turn e4m3 tiles into the f16 operands of
 // the tensor cores, in the slots and the swizzle that the TMA producer would fill.
 //
 // A byte becomes f16 exactly; a block's scale 2^x then enters relative to a common
@@ -636,8 +636,8 @@ __host__ __device__ constexpr int q8_first_group(int cw) { return cw == 0 ? 0 : 
 // [2^14, 2^15). Rows behind the last key, and of pages outside the cache, are zero.
 //
 // The e4m3 rows come by bulk copies kQ8Stages half-tiles (K_t, V_t, K_t+1, ...) ahead. A
-// warp owns 48 or 40 consecutive rows of every tile and copies, waits for and converts
-// them alone: the warps meet only at the slots' barriers. A copy is all its rows that
+// warp owns 32 consecutive rows of every tile and copies, waits for and converts them
+// alone: the warps meet only at the slots' barriers. A copy is all its rows that
 // share a page (contiguous for a head). Pages are looked up three tiles ahead, scale
 // bytes two. Per 16 bytes a thread spends one load, four extractions, eight
 // conversions, eight multiplications and two stores; a 512-token chunk at history 32256
@@ -685,7 +685,8 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
     // store to eight different 16-byte banks of the swizzled tile
     const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;
     const int c = D == 128 ? (lane & 3) + 4 * ((r0 & 1) ^ (lane >> 4)) : lane & 3;
-    const int g0 = q8_first_group(cw), g1 = q8_first_group(cw + 1);
+    constexpr int kGroups = 16 / NC;     // groups of eight rows per warp
+    const int g0 = q8_first_group(cw), g1 = g0 + kGroups;
     const int lg_page = p.q8.lg_page, lg_sb = p.q8.lg_sb, pmask = p.page_size - 1;
     // lane l stands for the group of rows 8 l ..; the first of a page, or of the warp's
     // share, copies all that follow in the same page and share
@@ -832,44 +833,36 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                     break;
                 const uint32_t src = smem_u32(stages) + st * (128 * D) + r0 * D + 16 * c;
                 const uint32_t dst = smem_u32(smem + C::kSlotOff) + slot * C::kTileBytes;
-                // three groups at a time, all their loads first: a load cannot pass an earlier
-                // store by itself, and a lone warp hides latency only behind its own
-                // instructions (a group at a time 890 clocks a half-tile of six groups on an
-                // otherwise idle SM, three 560, six no better; unrolled further, the straight-line
-                // code runs at the rate of instruction fetch)
-#pragma unroll 1
-                for (int ga = g0; ga < g1; ga += 3) {
-                    uint4 v[3][NP];
+                // all loads first: a load cannot pass an earlier store by itself, and a lone warp
+                // hides latency only behind its own instructions (six groups one by one took
+                // 890 clocks on an otherwise idle SM, three at a time 560)
+                uint4 v[kGroups][NP];
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
+                for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) v[i][q] = lds128(src + (g0 + i) * kGroupBytes + q * RPW * D);
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < kGroups; ++i)
 #pragma unroll
                         for (int q = 0; q < NP; ++q)
-                            v[i][q] = lds128(src + min(ga + i, g1 - 1) * kGroupBytes + q * RPW * D);
-                    if (!whole) {
+                            if (8 * (g0 + i) + RPW * q + r0 >= nlive || !((there >> (g0 + i)) & 1u))
+                                v[i][q] = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                        for (int i = 0; i < 3; ++i)
+                for (int i = 0; i < kGroups; ++i) {
+                    const uint32_t f = __shfl_sync(0xffffffffu, fl, g0 + i);
 #pragma unroll
-                            for (int q = 0; q < NP; ++q)
-                                if (8 * (ga + i) + RPW * q + r0 >= nlive || !((there >> (ga + i)) & 1u))
-                                    v[i][q] = make_uint4(0, 0, 0, 0);
-                    }
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t x[4] = {v[i][q].x, v[i][q].y, v[i][q].z, v[i][q].w};
+                        uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint32_t f = __shfl_sync(0xffffffffu, fl, (ga + i) & 15);
-                        if (ga + i >= g1)
-                            break;
-#pragma unroll
-                        for (int q = 0; q < NP; ++q) {
-                            const uint32_t x[4] = {v[i][q].x, v[i][q].y, v[i][q].z, v[i][q].w};
-                            uint32_t y[8];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
-                                y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
-                            }
-                            sts128(dst + (ga + i) * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
-                            sts128(dst + (ga + i) * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
+                        for (int j = 0; j < 4; ++j) {
+                            y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
+                            y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
                         }
+                        sts128(dst + (g0 + i) * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
+                        sts128(dst + (g0 + i) * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
                     }
                 }
                 if (kv == 0 && cw == 0 && lane == 0) {
@@ -905,6 +898,10 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
     }
 }
 
+// The 8-bit chunk kernel's registers: every warp of a group of four calls the same one.
+__device__ __forceinline__ void regs_keep_96() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+__device__ __forceinline__ void regs_take_160() { asm volatile("setmaxnreg.inc.sync.aligned.u32 160;"); }
+
 // Rows leave through the staging buffer by TMA; not with Q8, whose e4m3 tiles take its place.
 template <bool Q8>
 __device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
@@ -914,15 +911,18 @@ __device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
 
 // SELF: a batch of one prefill request, planned by the kernel itself (pieces in
 // shared memory); else the plan kernel's lists in the workspace.
-// Q8: over the 8-bit cache. The CTA is then 384 threads: warps 0..7 softmax, 8..10
+// Q8: over the 8-bit cache. The CTA is then 512 threads: warps 0..7 softmax, 8..11
 // converters (Q and the K/V tiles, through registers, in place of the TMA producer; 10
-// the self plan first), 11 the tcgen05 issuer. Operands are f16 instead of bf16 (see
-// q8_convert); the factors that this leaves out (per q row, K tile and piece) are
-// powers of two and go into the softmax's scale and the final 1 / l. (A fourth
-// converter warp would bring the CTA to 13 warps and every thread to 152 registers;
-// moving registers between groups of four warps instead spilled over 2 KB a thread.)
+// the self plan first), 12 the tcgen05 issuer, 13..15 only there because registers move
+// by groups of four warps: of the 128 a thread that the block starts with, the softmax
+// groups take 160 and the others keep 96 (256 x 160 + 256 x 96 = 512 x 128). Operands
+// are f16 instead of bf16 (see q8_convert); the factors that this leaves out (per q row,
+// K tile and piece) are powers of two and go into the softmax's scale and the final
+// 1 / l. Measured on 512 tokens at history 32256 (32/8 heads, D 128): three converter
+// warps in 384 threads of 168 registers 254 us, four this way 239 us, four in 416
+// threads (128 registers, 0.6 KB of spills) 468 us.
 template <int D, int NQ, bool SELF, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 384 : 352, 1)
+__global__ void __launch_bounds__(Q8 ? 512 : 352, 1)
 chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
@@ -1017,8 +1017,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
 
     Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
     if (Q8 && warp >= C::kLoadWarp && warp < C::kLoadWarp + C::kConverters) {
-        if constexpr (Q8)
+        if constexpr (Q8) {
+            regs_keep_96();
             q8_convert<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, SELF, warp - C::kLoadWarp, lane);
+        }
     } else if (!Q8 && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ producer
         const int PB = p.page_size < 128 ? p.page_size : 128;   // rows per TMA box
@@ -1264,6 +1266,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         // The whole warp walks the loop; every MMA and commit is issued by one
         // lane from an elect.sync branch. Waits are polled by all lanes and their
         // verdicts combined, so the warp stays converged.
+        if constexpr (Q8)
+            regs_keep_96();
         constexpr uint32_t idesc_qk = Q8 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
         constexpr uint32_t idesc_pv = Q8 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
         const uint32_t q_addr = smem_u32(smem + C::kQOff);
@@ -1386,6 +1390,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         __syncwarp();
     } else if (warp / 4 < NQ) {
         // ------------------------------------------------------------ softmax
+        if constexpr (Q8)
+            regs_take_160();
         const int wg = warp / 4;
         const int sub = warp & 3;
         const int row = sub * 32 + lane;
@@ -1709,6 +1715,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 }
             }
         }
+    } else {
+        if constexpr (Q8)
+            regs_keep_96();
     }
 
     // the softmax warps' output stores are complete before the CTA ends
