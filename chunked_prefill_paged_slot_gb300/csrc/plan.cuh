@@ -60,7 +60,7 @@ constexpr int kMergeCounters = 2 * 4;          // per split unit: q heads (<= 2)
 // A batch of one prefill request skips the plan kernel: every chunk-kernel CTA
 // computes its own run's pieces (at most this many, kept in shared memory).
 constexpr int kSelfPlanCap = 56;
-constexpr int kSelfPlanCapQ8 = 34;   // over the 8-bit cache
+constexpr int kSelfPlanCapQ8 = 30;   // over the 8-bit cache
 
 // A prefill piece: KV tiles [kt0, kt1) of the unit (request r, query tile at
 // row i0, kv head kvh, head pair hp); piece `piece` of `npieces` of that unit.

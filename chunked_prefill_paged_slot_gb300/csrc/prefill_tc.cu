@@ -93,6 +93,7 @@ struct ChunkCfg {
     static constexpr int kConverters = 4;
     static constexpr int kMmaWarp = Q8 ? 12 : 9;
     static constexpr int kWriteWarp = 10;
+    static constexpr int kQ8LoadWarp = 13;
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t s_col(int n) { return (uint32_t)n * 128u; }
     __host__ __device__ static constexpr uint32_t o_col(int n) { return 256u + (uint32_t)n * D; }
@@ -108,16 +109,23 @@ struct ChunkBars {
     int abort;
     int it_begin, it_end;    // this CTA's run of pieces
 };
-// What the 8-bit cache's converters tell the softmax: per KV tile (its ordinal in the
-// CTA's run, modulo 8) the exponents of its K and V operands, per q row its own (two
-// sets, for items in turn). An entry is written again only after MMAs that come after
-// the softmax has read it: at most four K tiles are ahead of the softmax, and an
-// item's Q replaces the one before it once that one's scores are done, which may be
-// before the softmax looks at them, but not before it is done with the item before.
+// What the 8-bit cache's loader and converters tell the others: per KV tile (its ordinal
+// in the CTA's run, modulo 8) the exponents of its K and V operands for the softmax, and
+// (modulo 4) what the converters need; per q row its exponent (two sets, for items in
+// turn). An entry is written again only after MMAs that come after its last reader is
+// done: the loader is at most two tiles ahead of the converters, and they at most four K
+// tiles ahead of the softmax; an item's Q replaces the one before it once that one's
+// scores are done, which may be before the softmax looks at them, but not before it is
+// done with the item before.
 struct Q8Tiles {
     int kx[8], vx[8];
     int8_t qe[2][256];
-    uint64_t full[4][kQ8Stages];   // per converter warp: its rows of an e4m3 tile have landed
+    uint64_t full[kQ8Stages], empty[kQ8Stages];   // e4m3 half-tiles: landed, converted
+    struct {
+        int8_t ek[16], ev[16];   // per group of eight keys: its factor's exponent
+        uint32_t there;          // bit l: group l is loaded
+        uint32_t pad[3];
+    } tile[4];
 };
 static_assert(sizeof(Q8Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32, "in place of the pieces it gave up");
 static_assert(sizeof(ChunkBars) <= 256, "the self-planned pieces follow the barriers at +256");
@@ -619,9 +627,6 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 }
 
 // ---------------------------------------------------------------------------
-// The first group of eight rows of converter warp cw's share of a tile (16 groups).
-__host__ __device__ constexpr int q8_first_group(int cw) { return 4 * cw; }
-
 // The 8-bit cache's converters: four warps turn e4m3 tiles into the f16 operands of
 // the tensor cores, in the slots and the swizzle that the TMA producer would fill.
 //
@@ -635,16 +640,19 @@ __host__ __device__ constexpr int q8_first_group(int cw) { return 4 * cw; }
 // Q rows go to f16 under a power of two that puts their largest element in
 // [2^14, 2^15). Rows behind the last key, and of pages outside the cache, are zero.
 //
-// The e4m3 rows come by bulk copies kQ8Stages half-tiles (K_t, V_t, K_t+1, ...) ahead. A
-// warp owns 32 consecutive rows of every tile and copies, waits for and converts them
-// alone: the warps meet only at the slots' barriers. A copy is all its rows that
-// share a page (contiguous for a head). Pages are looked up three tiles ahead, scale
-// bytes two. Per 16 bytes a thread spends one load, four extractions, eight
-// conversions, eight multiplications and two stores; a 512-token chunk at history 32256
-// (32/8 heads, D 128) takes @@MEAS@@
-// (Taking the rows straight from global memory into registers cost 10.6k clocks a tile,
-// mostly addresses; bulk copies of eight rows each, one after the other from their
-// lanes, and per-thread selects between the two stores 7.0k.)
+// The loader warp looks up pages and scales and brings the e4m3 rows by bulk copies,
+// all rows of a tile that share a page at once (contiguous for a head), kQ8Stages
+// half-tiles (K_t, V_t, K_t+1, ...) ahead; pages are looked up three tiles ahead, scale
+// bytes two. The converter warps take 32 consecutive rows each. Per 16 bytes a thread
+// spends one load, four extractions, eight conversions, eight multiplications and two
+// stores.
+// What it took, for 512 tokens at history 32256 (32/8 heads, D 128), where the same
+// chunk over a bf16 cache takes 176 us: rows straight from global memory into registers
+// 727 us (1700 instructions a warp and tile, mostly addresses); bulk copies of eight rows
+// from their own lanes, and selects between the two stores, 416; copies by page, chunks
+// dealt so that nothing is selected, loads ahead of stores, 264; scale bytes not combined
+// before they are used 254; a fourth converter 237; the loader's work off the converters
+// @@L@@.
 // ---------------------------------------------------------------------------
 constexpr int kQ8Lift = 7;
 
@@ -670,49 +678,26 @@ __device__ __forceinline__ uint32_t f16_chunk_off(int row, int ch)
 }
 
 template <int D, int NQ>
-__device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
-                                           const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
-                                           int lane)
+__device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+                                        const PrefillItem *items, int it_begin, int it_end, int lane)
 {
     using C = ChunkCfg<D, NQ, true>;
-    constexpr int NC = C::kConverters;
-    constexpr int RPW = 512 / D;         // rows per warp and pass: 4 or 8
-    constexpr int NP = 8 / RPW;          // passes per group of eight rows
-    constexpr uint32_t kGroupBytes = 8 * D;
     volatile int *abort = &bars->abort;
-    // this thread's row within a pass and its 16 columns 16 c ..: eight threads in a row
-    // (of the warp) read 128 consecutive bytes, or the opposite halves of two rows, and
-    // store to eight different 16-byte banks of the swizzled tile
-    const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;
-    const int c = D == 128 ? (lane & 3) + 4 * ((r0 & 1) ^ (lane >> 4)) : lane & 3;
-    constexpr int kGroups = 16 / NC;     // groups of eight rows per warp
-    const int g0 = q8_first_group(cw), g1 = g0 + kGroups;
     const int lg_page = p.q8.lg_page, lg_sb = p.q8.lg_sb, pmask = p.page_size - 1;
-    // lane l stands for the group of rows 8 l ..; the first of a page, or of the warp's
-    // share, copies all that follow in the same page and share
-    const bool copier = lane >= g0 && lane < g1 && (lane == g0 || ((8 * lane) & pmask) == 0);
-    const uint32_t copy_bytes =
-        (uint32_t)(min(g1, ((8 * lane | pmask) + 1) >> 3) - lane) * kGroupBytes;
-    uint8_t *stages = smem + C::kStageOff;
-    // swizzled offsets of this thread's two f16 chunks in pass q of a group
-    uint32_t off0[NP], off1[NP];
-#pragma unroll
-    for (int q = 0; q < NP; ++q) {
-        off0[q] = f16_chunk_off(r0 + RPW * q, 2 * c);
-        off1[q] = f16_chunk_off(r0 + RPW * q, 2 * c + 1);
-    }
-    uint32_t q_uses = 0, slot_it = 0, tile = 0, issued = 0;   // issued, slot_it: half-tiles
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-    };
-    for (int it = it_begin; it < it_end && !__any_sync(0xffffffffu, *abort != 0); ++it) {
+    // lane l stands for the group of rows 8 l .. of a tile; the first of a page copies all
+    // that follow in the page and tile
+    const int key_l = 8 * (lane & 15);
+    const bool copier = lane < 16 && (lane == 0 || (key_l & pmask) == 0);
+    const uint32_t copy_bytes = (uint32_t)(min(128, (key_l | pmask) + 1) - key_l) * D;
+    uint8_t *stages = smem + C::kStageOff + key_l * D;
+    uint32_t half = 0, tile = 0;   // half-tiles and tiles issued
+    bool ok = true;
+    for (int it = it_begin; it < it_end && ok && !__any_sync(0xffffffffu, *abort != 0); ++it) {
         const PrefillItem w = items[it];
-        const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
+        const int kvh = w.kvh_hp & 0xFFFF;
         const int s_len = p.seq_lens[w.r];
-        const int q_len = p.query_lens[w.r];
         const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
-        const int key_l = 8 * (lane & 15);
-        // lane l: the page of its group in tile kt as it stands in the table, -1 where there is none
+        // the page of this lane's group in tile kt as it stands in the table, -1 where there is none
         auto page_of = [&](int kt) -> int {
             const int key = kt * 128 + key_l;
             return kt < w.kt1 && key < s_len ? ldg_here(bt_row + (key >> lg_page)) : -1;
@@ -735,81 +720,14 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                 vs = ldg_here(p.q8.vs + at);
             }
         };
-        // this warp's rows of K and V tile kt, pages pg, into the next two stages (kQ8Stages is
-        // even); each lane announces its own copy's bytes right before it issues it
-        auto issue = [&](int kt, int pg) {
-            const int st = issued % kQ8Stages;
-            if (copier) {
-                uint64_t *bar = &q8t->full[cw][st];    // V's is the next
-                if (pg >= 0) {
-                    const int64_t row = (((int64_t)pg * p.num_kv_heads + kvh) << lg_page) + ((kt * 128 + key_l) & pmask);
-                    uint8_t *dst = stages + st * (128 * D) + lane * kGroupBytes;
-                    mbar_arrive_expect_tx(bar, copy_bytes);
-                    bulk_load(dst, p.q8.k + row * D, copy_bytes, bar);
-                    mbar_arrive_expect_tx(bar + 1, copy_bytes);
-                    bulk_load(dst + 128 * D, p.q8.v + row * D, copy_bytes, bar + 1);
-                } else {
-                    mbar_arrive(bar);
-                    mbar_arrive(bar + 1);
-                }
-            }
-            issued += 2;
-        };
         int pg0 = page_of(w.kt0), pg1 = page_of(w.kt0 + 1), pg2 = page_of(w.kt0 + 2);
-        pg0 = checked(w.kt0, pg0);
-        issue(w.kt0, pg0);
-        pg1 = checked(w.kt0 + 1, pg1);
-        if (w.kt0 + 1 < w.kt1)
-            issue(w.kt0 + 1, pg1);
         uint32_t ks0, vs0, ks1, vs1, ks2, vs2;
+        pg0 = checked(w.kt0, pg0);
         scales_of(w.kt0, pg0, ks0, vs0);
+        pg1 = checked(w.kt0 + 1, pg1);
         scales_of(w.kt0 + 1, pg1, ks1, vs1);
-
-        // Q, head by head: rows r of this thread's columns 16 c .. 16 c + 15
-        bool ok = q_uses == 0 || wait(&bars->q_empty, (q_uses - 1) & 1);
-        if (ok) {
-            int8_t *qe = q8t->qe[q_uses & 1];
-            ++q_uses;
-            const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
-#pragma unroll 1
-            for (int n = 0; n < NQ; ++n) {
-                const int h = kvh * p.group + hp * NQ + n;
-                uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
-#pragma unroll 4
-                for (int r8 = cw * RPW; r8 < 128; r8 += NC * RPW) {
-                    const int row = r8 + r0;
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    if (w.i0 + row < q_len) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
-                        a = __ldg(src);
-                        b = __ldg(src + 1);
-                    }
-                    float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
-#pragma unroll
-                    for (int o = 1; o <= 2; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    if (D == 128)
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    const int e = q_exponent(m);
-                    const float f = exp2i(-e);
-                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
-                        make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
-                                   bf16x2_to_f16x2(a.w, f));
-                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
-                        make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
-                                   bf16x2_to_f16x2(b.w, f));
-                    if (c == 0)
-                        qe[n * 128 + row] = (int8_t)e;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars->q_full);
-        }
-
         int X = -126;
-        for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++tile) {
             const int pg3 = page_of(kt + 3);
             pg2 = checked(kt + 2, pg2);
             scales_of(kt + 2, pg2, ks2, vs2);
@@ -817,22 +735,160 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
             const int kxl = q8_exp(ks0), vxl = q8_exp(vs0);
             const int KX = __reduce_max_sync(0xffffffffu, pg0 >= 0 ? kxl : -126);
             X = max(X, __reduce_max_sync(0xffffffffu, pg0 >= 0 ? vxl : -126));
-            const uint32_t fk = f16x2_pow2(min(kxl - KX, 0) + kQ8Lift), fv = f16x2_pow2(min(vxl - X, 0) + kQ8Lift);
-            const uint32_t there = __ballot_sync(0xffffffffu, pg0 >= 0);
+            const uint32_t there = __ballot_sync(0xffffffffu, pg0 >= 0) & 0xffffu;
+            const int64_t row = (((int64_t)pg0 * p.num_kv_heads + kvh) << lg_page) + ((kt * 128 + key_l) & pmask);
+            for (int kv = 0; kv < 2; ++kv, ++half) {
+                const int st = half % kQ8Stages;
+                if (half >= (uint32_t)kQ8Stages &&
+                    !__all_sync(0xffffffffu, mbar_wait(&q8t->empty[st], ((half / kQ8Stages) - 1) & 1, abort))) {
+                    ok = false;
+                    break;
+                }
+                if (kv == 0) {
+                    // after the wait: the tile four before, whose entry this is, is converted
+                    auto &e = q8t->tile[tile & 3];
+                    if (lane < 16) {
+                        e.ek[lane] = (int8_t)(max(kxl - KX, -100) + kQ8Lift);
+                        e.ev[lane] = (int8_t)(max(vxl - X, -100) + kQ8Lift);
+                    }
+                    if (lane == 16) {
+                        e.there = there;
+                        q8t->kx[tile & 7] = KX;
+                        q8t->vx[tile & 7] = X;
+                    }
+                    __syncwarp();
+                }
+                // each lane announces its own copy's bytes right before it issues it
+                if (copier) {
+                    if (pg0 >= 0) {
+                        mbar_arrive_expect_tx(&q8t->full[st], copy_bytes);
+                        bulk_load(stages + st * (128 * D), (kv == 0 ? p.q8.k : p.q8.v) + row * D, copy_bytes,
+                                  &q8t->full[st]);
+                    } else {
+                        mbar_arrive(&q8t->full[st]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok)
+                break;
+            pg0 = pg1;
+            pg1 = pg2;
+            pg2 = pg3;
+            ks0 = ks1;
+            vs0 = vs1;
+            ks1 = ks2;
+            vs1 = vs2;
+        }
+    }
+    if (!ok || __any_sync(0xffffffffu, *abort != 0)) {
+        // given up on a wait: let the copies in flight land before the CTA can end (a
+        // half-tile's phase completes once, and only its converters' reads let it go on)
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t h = half > (uint32_t)kQ8Stages ? half - kQ8Stages : 0; h < half; ++h)
+            while (!mbar_try_wait(&q8t->full[h % kQ8Stages], (h / kQ8Stages) & 1) &&
+                   global_timer_ns() - t0 < 100000000ull) {
+            }
+    }
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+                                           const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
+                                           int lane)
+{
+    using C = ChunkCfg<D, NQ, true>;
+    constexpr int kGroups = 16 / C::kConverters;   // groups of eight rows per warp
+    constexpr int RPW = 512 / D;                   // rows per warp and pass: 4 or 8
+    constexpr int NP = 8 / RPW;                    // passes per group
+    constexpr uint32_t kGroupBytes = 8 * D;
+    volatile int *abort = &bars->abort;
+    // this thread's row within a pass and its 16 columns 16 c ..: eight threads in a row
+    // (of the warp) read 128 consecutive bytes, or the opposite halves of two rows, and
+    // store to eight different 16-byte banks of the swizzled tile
+    const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;
+    const int c = D == 128 ? (lane & 3) + 4 * ((r0 & 1) ^ (lane >> 4)) : lane & 3;
+    const int g0 = cw * kGroups;
+    const uint32_t src0 = smem_u32(smem + C::kStageOff) + g0 * kGroupBytes + r0 * D + 16 * c;
+    const uint32_t dst0 = smem_u32(smem + C::kSlotOff) + g0 * 1024;
+    // swizzled offsets of this thread's two f16 chunks in pass q of a group
+    uint32_t off0[NP], off1[NP];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        off0[q] = f16_chunk_off(r0 + RPW * q, 2 * c);
+        off1[q] = f16_chunk_off(r0 + RPW * q, 2 * c + 1);
+    }
+    uint32_t q_uses = 0, half = 0, tile = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+    };
+    bool ok = true;
+    for (int it = it_begin; it < it_end && ok && !__any_sync(0xffffffffu, *abort != 0); ++it) {
+        const PrefillItem w = items[it];
+        const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
+        const int s_len = p.seq_lens[w.r];
+        const int q_len = p.query_lens[w.r];
+        // Q, head by head: rows r of this thread's columns 16 c .. 16 c + 15
+        if (q_uses > 0 && !wait(&bars->q_empty, (q_uses - 1) & 1))
+            break;
+        int8_t *qe = q8t->qe[q_uses & 1];
+        ++q_uses;
+        const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
+#pragma unroll 1
+        for (int n = 0; n < NQ; ++n) {
+            const int h = kvh * p.group + hp * NQ + n;
+            uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
+#pragma unroll 4
+            for (int r8 = cw * RPW; r8 < 128; r8 += C::kConverters * RPW) {
+                const int row = r8 + r0;
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (w.i0 + row < q_len) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
+                    a = __ldg(src);
+                    b = __ldg(src + 1);
+                }
+                float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
+#pragma unroll
+                for (int o = 1; o <= 2; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (D == 128)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                const int e = q_exponent(m);
+                const float f = exp2i(-e);
+                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
+                    make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
+                               bf16x2_to_f16x2(a.w, f));
+                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
+                    make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
+                               bf16x2_to_f16x2(b.w, f));
+                if (c == 0)
+                    qe[n * 128 + row] = (int8_t)e;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bars->q_full);
+
+        for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
             const int nlive = s_len - kt * 128;
-            const bool whole = nlive >= 128 && (there & 0xffffu) == 0xffffu;
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
-                const int st = slot_it % kQ8Stages;
-                const int slot = slot_it % C::kSlots;
-                const uint32_t fl = kv == 0 ? fk : fv;
-                ok = wait(&q8t->full[cw][st], (slot_it / kQ8Stages) & 1);
-                if (ok && slot_it >= (uint32_t)C::kSlots)
-                    ok = wait(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1);
+                const int st = half % kQ8Stages;
+                const int slot = half % C::kSlots;
+                ok = wait(&q8t->full[st], (half / kQ8Stages) & 1);
                 if (!ok)
                     break;
-                const uint32_t src = smem_u32(stages) + st * (128 * D) + r0 * D + 16 * c;
-                const uint32_t dst = smem_u32(smem + C::kSlotOff) + slot * C::kTileBytes;
+                const auto &e = q8t->tile[tile & 3];
+                const uint32_t there = e.there;
+                const uint32_t fl = f16x2_pow2((kv == 0 ? e.ek : e.ev)[lane & 15]);
+                if (half >= (uint32_t)C::kSlots) {
+                    ok = wait(&bars->slot_empty[slot], ((half / C::kSlots) - 1) & 1);
+                    if (!ok)
+                        break;
+                }
+                const uint32_t src = src0 + st * (128 * D);
+                const uint32_t dst = dst0 + slot * C::kTileBytes;
                 // all loads first: a load cannot pass an earlier store by itself, and a lone warp
                 // hides latency only behind its own instructions (six groups one by one took
                 // 890 clocks on an otherwise idle SM, three at a time 560)
@@ -840,8 +896,8 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) v[i][q] = lds128(src + (g0 + i) * kGroupBytes + q * RPW * D);
-                if (!whole) {
+                    for (int q = 0; q < NP; ++q) v[i][q] = lds128(src + i * kGroupBytes + q * RPW * D);
+                if (nlive < 128 || there != 0xffffu) {
 #pragma unroll
                     for (int i = 0; i < kGroups; ++i)
 #pragma unroll
@@ -861,39 +917,18 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                             y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
                             y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
                         }
-                        sts128(dst + (g0 + i) * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
-                        sts128(dst + (g0 + i) * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
+                        sts128(dst + i * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
+                        sts128(dst + i * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
                     }
-                }
-                if (kv == 0 && cw == 0 && lane == 0) {
-                    q8t->kx[tile & 7] = KX;
-                    q8t->vx[tile & 7] = X;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
                     mbar_arrive(&bars->slot_full[slot]);
-                ++slot_it;
-            }
-            // both stages are read: the tile after the next
-            if (ok && kt + 2 < w.kt1)
-                issue(kt + 2, pg2);
-            pg0 = pg1;
-            pg1 = pg2;
-            pg2 = pg3;
-            ks0 = ks1;
-            vs0 = vs1;
-            ks1 = ks2;
-            vs1 = vs2;
-        }
-        if (!ok) {
-            // given up on a wait: let the copies in flight land before the CTA can end
-            const uint64_t t0 = global_timer_ns();
-            for (; slot_it < issued; ++slot_it)
-                while (!mbar_try_wait(&q8t->full[cw][slot_it % kQ8Stages], (slot_it / kQ8Stages) & 1) &&
-                       global_timer_ns() - t0 < 100000000ull) {
+                    mbar_arrive(&q8t->empty[st]);
                 }
-            break;
+                ++half;
+            }
         }
     }
 }
@@ -913,13 +948,13 @@ __device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
 // shared memory); else the plan kernel's lists in the workspace.
 // Q8: over the 8-bit cache. The CTA is then 512 threads: warps 0..7 softmax, 8..11
 // converters (Q and the K/V tiles, through registers, in place of the TMA producer; 10
-// the self plan first), 12 the tcgen05 issuer, 13..15 only there because registers move
-// by groups of four warps: of the 128 a thread that the block starts with, the softmax
+// the self plan first), 12 the tcgen05 issuer, 13 the e4m3 loader, 14 and 15 only there
+// because registers move by groups of four warps: of the 128 a thread that the block starts with, the softmax
 // groups take 160 and the others keep 96 (256 x 160 + 256 x 96 = 512 x 128). Operands
 // are f16 instead of bf16 (see q8_convert); the factors that this leaves out (per q row,
 // K tile and piece) are powers of two and go into the softmax's scale and the final
 // 1 / l. Measured on 512 tokens at history 32256 (32/8 heads, D 128): three converter
-// warps in 384 threads of 168 registers 254 us, four this way 239 us, four in 416
+// warps in 384 threads of 168 registers 254 us, four this way 237 us, four in 416
 // threads (128 registers, 0.6 KB of spills) 468 us.
 template <int D, int NQ, bool SELF, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 512 : 352, 1)
@@ -951,11 +986,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         }
         if (Q8) {
             Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
-            for (int x = 0; x < C::kConverters; ++x) {
-                // one arrival per copy: the pages that the warp's rows of a tile lie in
-                const int a = 8 * q8_first_group(x), b = 8 * q8_first_group(x + 1) - 1;
-                const int page = p.page_size < 128 ? p.page_size : 128;
-                for (int s = 0; s < kQ8Stages; ++s) mbar_init(&q8t->full[x][s], (uint32_t)(b / page - a / page + 1));
+            for (int s = 0; s < kQ8Stages; ++s) {
+                mbar_init(&q8t->full[s], (uint32_t)(128 / (p.page_size < 128 ? p.page_size : 128)));   // one per copy
+                mbar_init(&q8t->empty[s], C::kConverters);
             }
         }
         mbar_init(&bars->stage, 1);
@@ -1716,8 +1749,11 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             }
         }
     } else {
-        if constexpr (Q8)
+        if constexpr (Q8) {
             regs_keep_96();
+            if (warp == C::kQ8LoadWarp)
+                q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+        }
     }
 
     // the softmax warps' output stores are complete before the CTA ends
