@@ -66,7 +66,7 @@ constexpr int kFmaExpPairsPer8 = CPSA_FMA_EXP_PAIRS_PER_8;
 constexpr int kMergeMaxOthers = 3;
 constexpr int kMergeStageBytes = kMergeMaxOthers * 32 * 128 * 2;
 
-constexpr int kQ8Stages = 4;   // e4m3 tiles on their way (see q8_convert)
+constexpr int kQ8Stages = 2;   // e4m3 tiles on their way (see q8_convert)
 
 // Over the 8-bit cache the kernel has another cast of warps (see chunk_attn_kernel)
 // and keeps a little more in shared memory, so fewer self-planned pieces.
@@ -79,14 +79,15 @@ struct ChunkCfg {
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = NQ * kTileBytes;
     static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer (Q8: e4m3 tiles)
-    static constexpr int kBarOff = kStageOff + (Q8 ? kQ8Stages * 128 * D : kTileBytes);
+    static constexpr int kQ8StageOff = kStageOff + kTileBytes;         // Q8: e4m3 tiles
+    static constexpr int kBarOff = kStageOff + kTileBytes + (Q8 ? kQ8Stages * 128 * D : 0);
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
     static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
     static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
     static constexpr int kBarBytes = 256 + kSelfPlanCap * 32;  // barriers + pieces (+ Q8Tiles)
     static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
-    static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= (Q8 ? kBarOff : kStageOff),
+    static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= kSlotOff + 4 * kTileBytes,
                   "the staged merge uses the Q and K/V buffers (Q8: and the e4m3 tiles')");
     static constexpr int kThreads = Q8 ? 512 : 352;
     static constexpr int kLoadWarp = 8;                        // Q8: to kLoadWarp + kConverters - 1
@@ -689,7 +690,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
     const int key_l = 8 * (lane & 15);
     const bool copier = lane < 16 && (lane == 0 || (key_l & pmask) == 0);
     const uint32_t copy_bytes = (uint32_t)(min(128, (key_l | pmask) + 1) - key_l) * D;
-    uint8_t *stages = smem + C::kStageOff + key_l * D;
+    uint8_t *stages = smem + C::kQ8StageOff + key_l * D;
     uint32_t half = 0, tile = 0;   // half-tiles and tiles issued
     bool ok = true;
     for (int it = it_begin; it < it_end && ok && !__any_sync(0xffffffffu, *abort != 0); ++it) {
@@ -809,7 +810,7 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
     const int r0 = D == 128 ? (lane >> 2) & 3 : lane >> 2;
     const int c = D == 128 ? (lane & 3) + 4 * ((r0 & 1) ^ (lane >> 4)) : lane & 3;
     const int g0 = cw * kGroups;
-    const uint32_t src0 = smem_u32(smem + C::kStageOff) + g0 * kGroupBytes + r0 * D + 16 * c;
+    const uint32_t src0 = smem_u32(smem + C::kQ8StageOff) + g0 * kGroupBytes + r0 * D + 16 * c;
     const uint32_t dst0 = smem_u32(smem + C::kSlotOff) + g0 * 1024;
     // swizzled offsets of this thread's two f16 chunks in pass q of a group
     uint32_t off0[NP], off1[NP];
@@ -828,52 +829,65 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
         const int s_len = p.seq_lens[w.r];
         const int q_len = p.query_lens[w.r];
-        // Q, head by head: rows r of this thread's columns 16 c .. 16 c + 15
-        if (q_uses > 0 && !wait(&bars->q_empty, (q_uses - 1) & 1))
-            break;
-        int8_t *qe = q8t->qe[q_uses & 1];
-        ++q_uses;
-        const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
+        // Q, head by head: a warp's rows of every STEP, this thread's columns 16 c .. 16 c + 15;
+        // the first loads are on their way before the wait for the buffer
+        auto convert_q = [&]() -> bool {
+            constexpr int STEP = C::kConverters * RPW, BATCH = 4;   // 128 / STEP: 8 or 4 rows a thread and head
+            int8_t *qe = q8t->qe[q_uses & 1];
+            const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
 #pragma unroll 1
-        for (int n = 0; n < NQ; ++n) {
-            const int h = kvh * p.group + hp * NQ + n;
-            uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
-#pragma unroll 4
-            for (int r8 = cw * RPW; r8 < 128; r8 += C::kConverters * RPW) {
-                const int row = r8 + r0;
-                uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                if (w.i0 + row < q_len) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(p.q) + ((t0 + row) * p.num_q_heads + h) * D + 16 * c);
-                    a = __ldg(src);
-                    b = __ldg(src + 1);
-                }
-                float m = fmaxf(bf16x8_amax(a), bf16x8_amax(b));
+            for (int x = 0; x < NQ * (128 / STEP / BATCH); ++x) {
+                const int n = x / (128 / STEP / BATCH), rb = x % (128 / STEP / BATCH) * (BATCH * STEP) + cw * RPW + r0;
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                           (t0 * p.num_q_heads + kvh * p.group + hp * NQ + n) * D + 16 * c;
+                uint8_t *dst = smem + C::kQOff + n * C::kTileBytes;
+                uint4 a[BATCH], b[BATCH];
 #pragma unroll
-                for (int o = 1; o <= 2; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (D == 128)
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const int e = q_exponent(m);
-                const float f = exp2i(-e);
-                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
-                    make_uint4(bf16x2_to_f16x2(a.x, f), bf16x2_to_f16x2(a.y, f), bf16x2_to_f16x2(a.z, f),
-                               bf16x2_to_f16x2(a.w, f));
-                *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
-                    make_uint4(bf16x2_to_f16x2(b.x, f), bf16x2_to_f16x2(b.y, f), bf16x2_to_f16x2(b.z, f),
-                               bf16x2_to_f16x2(b.w, f));
-                if (c == 0)
-                    qe[n * 128 + row] = (int8_t)e;
+                for (int i = 0; i < BATCH; ++i) {
+                    const int row = rb + STEP * i;
+                    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+                    if (w.i0 + row < q_len) {
+                        const uint4 *at = reinterpret_cast<const uint4 *>(src + (int64_t)row * p.num_q_heads * D);
+                        a[i] = ldg_here(at);
+                        b[i] = ldg_here(at + 1);
+                    }
+                }
+                if (x == 0 && q_uses > 0 && !wait(&bars->q_empty, (q_uses - 1) & 1))
+                    return false;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int row = rb + STEP * i;
+                    float m = fmaxf(bf16x8_amax(a[i]), bf16x8_amax(b[i]));
+#pragma unroll
+                    for (int o = 1; o <= 2; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    if (D == 128)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    const int e = q_exponent(m);
+                    const float f = exp2i(-e);
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c)) =
+                        make_uint4(bf16x2_to_f16x2(a[i].x, f), bf16x2_to_f16x2(a[i].y, f),
+                                   bf16x2_to_f16x2(a[i].z, f), bf16x2_to_f16x2(a[i].w, f));
+                    *reinterpret_cast<uint4 *>(dst + f16_chunk_off(row, 2 * c + 1)) =
+                        make_uint4(bf16x2_to_f16x2(b[i].x, f), bf16x2_to_f16x2(b[i].y, f),
+                                   bf16x2_to_f16x2(b[i].z, f), bf16x2_to_f16x2(b[i].w, f));
+                    if (c == 0)
+                        qe[n * 128 + row] = (int8_t)e;
+                }
             }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&bars->q_full);
-
+            ++q_uses;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars->q_full);
+            return true;
+        };
         for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
             const int nlive = s_len - kt * 128;
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
+                // Q after the first K tile, whose slot frees earlier than Q's buffer
+                if (kt == w.kt0 && kv == 1 && !(ok = convert_q()))
+                    break;
                 const int st = half % kQ8Stages;
                 const int slot = half % C::kSlots;
                 ok = wait(&q8t->full[st], (half / kQ8Stages) & 1);
@@ -941,7 +955,7 @@ __device__ __forceinline__ void regs_take_160() { asm volatile("setmaxnreg.inc.s
 template <bool Q8>
 __device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
 {
-    return !Q8 && p.out_tma;
+    return p.out_tma;
 }
 
 // SELF: a batch of one prefill request, planned by the kernel itself (pieces in
@@ -1642,7 +1656,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                             staged = NQ == 1 || __all_sync(0xffffffffu, mbar_wait(&bars->o_done[NQ - 1 - wg],
                                                                                   (o_base - 1) & 1, abort));
                         // the merged rows through the writer's buffer once the writer is done with it
-                        const bool ostaged = staged && rows_by_tma<Q8>(p) &&
+                        const bool ostaged = !Q8 && staged && rows_by_tma<Q8>(p) &&
                                              (!p.fused || __all_sync(0xffffffffu, mbar_wait(&bars->writer_done, 0, abort)));
                         merge_split_row<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
                                                out_off,
