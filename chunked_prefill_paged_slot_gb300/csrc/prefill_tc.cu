@@ -832,7 +832,7 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         // Q, head by head: a warp's rows of every STEP, this thread's columns 16 c .. 16 c + 15;
         // the first loads are on their way before the wait for the buffer
         auto convert_q = [&]() -> bool {
-            constexpr int STEP = C::kConverters * RPW, BATCH = 4;   // 128 / STEP: 8 or 4 rows a thread and head
+            constexpr int STEP = C::kConverters * RPW, BATCH = D == 128 ? 4 : 2;   // of the 8 or 4 rows a thread has per head
             int8_t *qe = q8t->qe[q_uses & 1];
             const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
 #pragma unroll 1
