@@ -653,7 +653,7 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 // from their own lanes, and selects between the two stores, 416; copies by page, chunks
 // dealt so that nothing is selected, loads ahead of stores, 264; scale bytes not combined
 // before they are used 254; a fourth converter 237; the loader's work off the converters
-// @@L@@.
+// 229; a group's conversion no longer unrolled 213.
 // ---------------------------------------------------------------------------
 constexpr int kQ8Lift = 7;
 
@@ -903,36 +903,34 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                 }
                 const uint32_t src = src0 + st * (128 * D);
                 const uint32_t dst = dst0 + slot * C::kTileBytes;
-                // all loads first: a load cannot pass an earlier store by itself, and a lone warp
-                // hides latency only behind its own instructions (six groups one by one took
-                // 890 clocks on an otherwise idle SM, three at a time 560)
-                uint4 v[kGroups][NP];
+                // One group at a time: with the softmax and the MMA issuer unrolled as they are,
+                // instruction fetch is what runs short. On an otherwise idle SM six groups take
+                // 890 clocks this way and 645 by twos, their loads first; in the kernel it is all
+                // four groups unrolled 227 us, by twos 214, one by one 213 (and eight fresh
+                // prompts of 2600 tokens 813, 748, 724 us).
+#pragma unroll 1
+                for (int gp = 0; gp < kGroups; ++gp) {
+                    uint4 v[NP];
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-#pragma unroll
-                    for (int q = 0; q < NP; ++q) v[i][q] = lds128(src + i * kGroupBytes + q * RPW * D);
-                if (nlive < 128 || there != 0xffffu) {
-#pragma unroll
-                    for (int i = 0; i < kGroups; ++i)
+                    for (int q = 0; q < NP; ++q) v[q] = lds128(src + gp * kGroupBytes + q * RPW * D);
+                    if (nlive < 128 || there != 0xffffu) {
 #pragma unroll
                         for (int q = 0; q < NP; ++q)
-                            if (8 * (g0 + i) + RPW * q + r0 >= nlive || !((there >> (g0 + i)) & 1u))
-                                v[i][q] = make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    const uint32_t f = __shfl_sync(0xffffffffu, fl, g0 + i);
+                            if (8 * (g0 + gp) + RPW * q + r0 >= nlive || !((there >> (g0 + gp)) & 1u))
+                                v[q] = make_uint4(0, 0, 0, 0);
+                    }
+                    const uint32_t f = __shfl_sync(0xffffffffu, fl, g0 + gp);
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
-                        const uint32_t x[4] = {v[i][q].x, v[i][q].y, v[i][q].z, v[i][q].w};
+                        const uint32_t x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
                         uint32_t y[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             y[2 * j] = f16x2_mul(e4m3_lo(x[j]), f);
                             y[2 * j + 1] = f16x2_mul(e4m3_hi(x[j]), f);
                         }
-                        sts128(dst + i * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
-                        sts128(dst + i * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
+                        sts128(dst + gp * 1024 + off0[q], make_uint4(y[0], y[1], y[2], y[3]));
+                        sts128(dst + gp * 1024 + off1[q], make_uint4(y[4], y[5], y[6], y[7]));
                     }
                 }
                 fence_proxy_async_smem();

@@ -72,18 +72,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-// Largest finite magnitude of eight bf16 numbers.
+// Largest finite magnitude of eight bf16 numbers. Magnitudes of one format order like
+// their bits, so pairs of 16-bit integer maxima do; only where an infinity or NaN turns
+// up are the finite ones sorted out one by one.
 __device__ __forceinline__ float bf16x8_amax(const uint4 &v)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float m = 0.f;
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t w = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+    uint32_t m = max(w & 0xffffu, w >> 16);
+    if (m >= 0x7f80u) {
+        const uint32_t x[4] = {v.x & k, v.y & k, v.z & k, v.w & k};
+        m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = __uint_as_float((w[i] << 16) & 0x7fffffffu), b = __uint_as_float(w[i] & 0x7fff0000u);
-        m = fmaxf(m, a < INFINITY ? a : 0.f);   // false for NaN
-        m = fmaxf(m, b < INFINITY ? b : 0.f);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = x[i] & 0xffffu, hi = x[i] >> 16;
+            m = max(m, lo < 0x7f80u ? lo : 0u);
+            m = max(m, hi < 0x7f80u ? hi : 0u);
+        }
     }
-    return m;
+    return __uint_as_float(m << 16);
 }
 
 // Exponent x with amax * 2^-x in [2^14, 2^15) (where the range of exp2i allows it).
