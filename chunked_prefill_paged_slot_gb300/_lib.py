@@ -160,72 +160,80 @@ def cpp_kv_cache_write(k, v, slot_mapping, k_cache, v_cache, dev_err, stream=Non
     _check(st, "cpp_kv_cache_write")
 
 
-def _rows(t: torch.Tensor, heads, d, name):
-    """A [T, heads, d] bf16 tensor whose heads are contiguous: its address and its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise CpsaError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise CpsaError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
-        raise CpsaError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (s[0] if t.shape[0] > 1 else heads * d)
-
-
+# The calls below check and convert in one go per tensor: a serving step's smallest calls are
+# bound by the host, and every attribute of a tensor costs it a tenth of a microsecond.
+_BF16, _I32, _I64, _F32, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.uint8
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 
 
-def _bytes(t: torch.Tensor, kinds, shape, name):
-    """A contiguous one-byte tensor of one of the types `kinds`."""
+def _where(stream, t, name):
+    """(stream handle, device) of a call: its tensors, `t` first, have to be on that device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise CpsaError(f"{name} must be a CUDA tensor")
-    if t.dtype not in kinds:
-        raise CpsaError(f"{name} must be {' or '.join(map(str, kinds))}, got {t.dtype}")
-    if t.shape != shape:
-        raise CpsaError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream, stream.device_index
+
+
+def _ptr(t: torch.Tensor, kinds, name, device):
+    """The address of a contiguous tensor of one of the types `kinds` (or of that type) on `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CpsaError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise CpsaError(f"{name} is on {t.device}, the call on cuda:{device}")
+    dt = t.dtype
+    if dt is not kinds and not (isinstance(kinds, tuple) and dt in kinds):
+        raise CpsaError(f"{name} must be {' or '.join(map(str, kinds if isinstance(kinds, tuple) else (kinds,)))}, got {dt}")
     if not t.is_contiguous():
         raise CpsaError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _q8_pointers(k_cache, v_cache, k_scale, v_scale):
-    """The four tensors of an 8-bit cache: [pages, Hkv, P, d] bytes and [pages, Hkv, P / min(16, P)] scales."""
-    if k_cache.dim() != 4:
-        raise CpsaError("k_cache must be [pages, kv heads, page size, head dim]")
-    pages, heads, page, _ = k_cache.shape
-    scales = (pages, heads, page // max(1, min(16, page)))
-    return (_bytes(k_cache, _BYTES, k_cache.shape, "k_cache"), _bytes(v_cache, _BYTES, k_cache.shape, "v_cache"),
-            _bytes(k_scale, _SCALES, scales, "k_scale"), _bytes(v_scale, _SCALES, scales, "v_scale"))
+def _rows(t: torch.Tensor, tokens, heads, d, name, device):
+    """A [tokens, heads, d] bf16 tensor whose heads are contiguous: its address and its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CpsaError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise CpsaError(f"{name} is on {t.device}, the call on cuda:{device}")
+    if t.dtype is not _BF16:
+        raise CpsaError(f"{name} must be {_BF16}, got {t.dtype}")
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+        raise CpsaError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (s[0] if tokens > 1 else heads * d)
 
 
-def _same_device(what, *tensors):
-    """Every tensor on the current device, where the kernel is launched."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise CpsaError(f"{what}: a tensor is on {t.device}, the current device is cuda:{here}")
-
-
-def _rope_args(what, q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved):
-    """The arguments that both rotary appends share, up to num_pages, and q_out's address."""
-    T, Hkv, d = k.shape
-    pages, Hkv2, P, d2 = k_cache.shape
-    Hq = 0 if q is None else q.shape[1]
-    if v.shape != k.shape or Hkv2 != Hkv or d2 != d or slot_mapping.shape != (T,) \
-            or (q is None) != (q_out is None) or (q is not None and (q.shape != (T, Hq, d) or q_out.shape != q.shape)) \
+def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cache, q_out, dev_err, interleaved, stream):
+    """Both rotary appends: `caches`(device) gives the addresses of the cache's tensors, `cache` is the k cache."""
+    if not isinstance(k, torch.Tensor) or not isinstance(cache, torch.Tensor) or k.dim() != 3 or cache.dim() != 4:
+        raise CpsaError(f"{what}: inconsistent shapes")
+    T, Hkv, d = kshape = k.shape
+    pages, Hkv2, P, d2 = cache.shape
+    if v.shape != kshape or Hkv2 != Hkv or d2 != d or slot_mapping.shape != (T,) or (q is None) != (q_out is None) \
             or (cos_sin is None) != (positions is None):
         raise CpsaError(f"{what}: inconsistent shapes")
-    if cos_sin is not None and (cos_sin.dim() != 2 or positions.shape != (T,)):
-        raise CpsaError(f"{what}: inconsistent shapes")
-    qp, qs = (0, 0) if q is None else _rows(q, Hq, d, "q")
-    kp, ks = _rows(k, Hkv, d, "k")
-    vp, vs = _rows(v, Hkv, d, "v")
-    top, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    return (qp, kp, vp, qs, ks, vs, None if positions is None else _dev(positions, torch.int64, "positions"),
-            None if cos_sin is None else _dev(cos_sin, torch.float32, "cos_sin"), top, rot, int(bool(interleaved)),
-            _dev(slot_mapping, torch.int64, "slot_mapping"), T, Hq, Hkv, d, P, pages,
-            None if q_out is None else _dev(q_out, torch.bfloat16, "q_out"))
+    handle, device = _where(stream, k, "k")
+    Hq = qp = qs = qo = top = rot = 0
+    pos = cs = None
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape:
+            raise CpsaError(f"{what}: inconsistent shapes")
+        Hq = q.shape[1]
+        qp, qs = _rows(q, T, Hq, d, "q", device)
+        qo = _ptr(q_out, _BF16, "q_out", device)
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions.shape != (T,):
+            raise CpsaError(f"{what}: inconsistent shapes")
+        top, rot = cos_sin.shape
+        pos, cs = _ptr(positions, _I64, "positions", device), _ptr(cos_sin, _F32, "cos_sin", device)
+    kp, ks = _rows(k, T, Hkv, d, "k", device)
+    vp, vs = _rows(v, T, Hkv, d, "v", device)
+    st = fn(qp, kp, vp, qs, ks, vs, pos, cs, top, rot, 1 if interleaved else 0,
+            _ptr(slot_mapping, _I64, "slot_mapping", device), T, Hq, Hkv, d, P, pages, qo, *caches(device),
+            _ptr(dev_err, _I32, "dev_err", device), handle)
+    if st != 0:
+        _check(st, what)
 
 
 def cpp_rope_kv_cache_write(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dev_err,
@@ -239,27 +247,31 @@ def cpp_rope_kv_cache_write(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
     appends k and v alone."""
     if v_cache.shape != k_cache.shape:
         raise CpsaError("cpp_rope_kv_cache_write: inconsistent shapes")
-    args = _rope_args("cpp_rope_kv_cache_write", q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err,
-                      interleaved)
-    caches = (_dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"))
-    err = _dev(dev_err, torch.int32, "dev_err")
-    _same_device("cpp_rope_kv_cache_write", q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dev_err)
-    st = load().cpp_rope_kv_cache_write(*args, *caches, err, _stream_ptr(stream))
-    _check(st, "cpp_rope_kv_cache_write")
+    _rope_call("cpp_rope_kv_cache_write", load().cpp_rope_kv_cache_write,
+               lambda dev: (_ptr(k_cache, _BF16, "k_cache", dev), _ptr(v_cache, _BF16, "v_cache", dev)),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream)
+
+
+def _q8_pointers(k_cache, v_cache, k_scale, v_scale, device):
+    """The four tensors of an 8-bit cache: [pages, Hkv, P, d] bytes and [pages, Hkv, P / min(16, P)] scales."""
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise CpsaError("k_cache must be [pages, kv heads, page size, head dim]")
+    scales = (shape[0], shape[1], shape[2] // max(1, min(16, shape[2])))
+    for t, want, name in ((v_cache, shape, "v_cache"), (k_scale, scales, "k_scale"), (v_scale, scales, "v_scale")):
+        if t.shape != want:
+            raise CpsaError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+    return (_ptr(k_cache, _BYTES, "k_cache", device), _ptr(v_cache, _BYTES, "v_cache", device),
+            _ptr(k_scale, _SCALES, "k_scale", device), _ptr(v_scale, _SCALES, "v_scale", device))
 
 
 def cpp_rope_kv_cache_write_q8(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
                                dev_err, interleaved=False, stream=None):
     """cpp_rope_kv_cache_write into an 8-bit cache: caches [pages, Hkv, P, d] torch.float8_e4m3fn (or uint8),
     k_scale, v_scale [pages, Hkv, P / min(16, P)] torch.float8_e8m0fnu (or uint8)."""
-    args = _rope_args("cpp_rope_kv_cache_write_q8", q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err,
-                      interleaved)
-    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale)
-    err = _dev(dev_err, torch.int32, "dev_err")
-    _same_device("cpp_rope_kv_cache_write_q8", q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale,
-                 v_scale, q_out, dev_err)
-    st = load().cpp_rope_kv_cache_write_q8(*args, *caches, err, _stream_ptr(stream))
-    _check(st, "cpp_rope_kv_cache_write_q8")
+    _rope_call("cpp_rope_kv_cache_write_q8", load().cpp_rope_kv_cache_write_q8,
+               lambda dev: _q8_pointers(k_cache, v_cache, k_scale, v_scale, dev),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream)
 
 
 def cpp_attn_workspace_bytes(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_kv_splits=8):
@@ -302,19 +314,21 @@ def cpp_chunked_prefill_attn_q8(q, k_cache, v_cache, k_scale, v_scale, query_len
     k_scale, v_scale [pages, Hkv, P / min(16, P)] torch.float8_e8m0fnu (or uint8), as cpp_rope_kv_cache_write_q8
     fills them; the rest as for cpp_chunked_prefill_attn."""
     what = "cpp_chunked_prefill_attn_q8"
-    T, Hq, d = q.shape
-    B = query_lens.shape[0]
-    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale)
+    handle, device = _where(stream, k_cache, "k_cache")
+    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale, device)
+    T, Hq, d = qshape = q.shape
     pages, Hkv, P, d2 = k_cache.shape
-    if out.shape != q.shape or d2 != d or seq_lens.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+    B = query_lens.shape[0]
+    table = block_table.shape
+    if out.shape != qshape or d2 != d or seq_lens.shape != (B,) or len(table) != 2 or table[0] != B:
         raise CpsaError(f"{what}: inconsistent shapes")
-    args = (_dev(q, torch.bfloat16, "q"), *caches, _dev(query_lens, torch.int32, "query_lens"),
-            _dev(seq_lens, torch.int32, "seq_lens"), _dev(block_table, torch.int32, "block_table"), B, T,
-            block_table.shape[1], Hq, Hkv, d, P, pages, float(scale), int(max_kv_splits),
-            _dev(out, torch.bfloat16, "out"), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-            _dev(dev_err, torch.int32, "dev_err"))
-    _same_device(what, q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table, out, workspace, dev_err)
-    _check(load().cpp_chunked_prefill_attn_q8(*args, _stream_ptr(stream)), what)
+    st = load().cpp_chunked_prefill_attn_q8(
+        _ptr(q, _BF16, "q", device), *caches, _ptr(query_lens, _I32, "query_lens", device),
+        _ptr(seq_lens, _I32, "seq_lens", device), _ptr(block_table, _I32, "block_table", device), B, T, table[1], Hq,
+        Hkv, d, P, pages, float(scale), int(max_kv_splits), _ptr(out, _BF16, "out", device),
+        _ptr(workspace, _U8, "workspace", device), workspace.numel(), _ptr(dev_err, _I32, "dev_err", device), handle)
+    if st != 0:
+        _check(st, what)
 
 
 def cpp_chunked_prefill_attn_events(q, k_cache, v_cache, query_lens, seq_lens, block_table, out, workspace,

@@ -24,9 +24,15 @@
 // the largest value exponent so far (O is rescaled when it rises), keep f16's 11 bits
 // down to 2^-29 of the largest: more than bf16's 8 wherever they count.
 //
+// Keys are the M rows of the scores (16 keys x 16 columns times 16 columns x 8 heads) and
+// columns those of the output (16 columns x 16 keys times 16 keys x 8 heads), heads the N
+// columns of both: eight of them fill an n tile, where as M rows they would leave half of
+// every MMA empty (that way round the kernel was bound by mma.sync: 2330 of 2850 clocks a
+// stage). The probabilities pass from one to the other by 8 x 8 transposes in registers.
+//
 // Shared memory layouts and fragments. A row of a stage is D bytes, its 16-byte
 // chunks swizzled by TMA. The k index of an mma is a free relabelling of columns
-// (scores) or keys (P V), the n index of keys or columns, so the fragments are chosen
+// (scores) or keys (P V), the m index of keys or columns, so the fragments are chosen
 // for the loads: lane (g, t) = (lane / 4, lane % 4) takes, of key kappa(g) of each
 // eight, the chunks t (and t + 4): 16-byte loads that hold four whole k steps; of V the
 // keys kappa(2t), kappa(2t + 1) of each eight, D/8 consecutive columns at chi(g), the
@@ -76,14 +82,22 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Rows of a stage are keys: the key of n index g within eight, and the column piece
-// (16 bytes of 128, 8 of 64) of n index g. Conflict-free for a 128-byte row whose
+// The transposed 8 x 8 b16 matrix whose row g, columns 2t and 2t + 1 lane (g, t) holds.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Rows of a stage are keys: the key of index g within eight, and the column piece
+// (16 bytes of 128, 8 of 64) of index g. Conflict-free for a 128-byte row whose
 // chunk c sits at c ^ (row & 7), and a 64-byte row whose chunk c sits at
 // c ^ (row / 2 & 3).
 template <int D>
@@ -243,9 +257,10 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
     }
 
     // ---------------------------------------------------------------- consumers
-    constexpr int R = HI ? 2 : 1;
+    constexpr int NH = HI ? 2 : 1;             // n tiles of eight q heads
     constexpr int KS = D / 16;                 // k steps of a score
-    constexpr int NT = D / 8;                  // n tiles of the output
+    constexpr int MT = D / 16;                 // m tiles of the output
+    constexpr int NT = D / 8;                  // a lane's consecutive columns of the output
     const int g = lane >> 2, t = lane & 3;
     const int h = warp % HG, part = warp / HG;
     const int kb0 = part * kWarpKeys;
@@ -254,18 +269,13 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
         const DecodeItem w = p.ditems[it];
         const int nst = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
         const int kvh = w.kvh * HG + h;
-        // q rows as f16 under their own power of two; k step 4 j + x of lane t covers
+        // q head g (+ 8) as f16 under its own power of two; k step 4 j + x of lane t covers
         // columns 16 (t + 4 j) + 4 x + {0, 1} and {2, 3}
-        uint32_t qa[KS][4];
-        float rf[R];
+        uint32_t qb[KS][NH][2];
+        float rf[NH][2];                       // of heads 2t, 2t + 1 (+ 8): the score's scale
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            const int row = g + 8 * rr;
-            if (rr == 1 && !HI) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) qa[k][1] = qa[k][3] = 0u;
-                continue;
-            }
+        for (int nh = 0; nh < NH; ++nh) {
+            const int row = g + 8 * nh;
             uint4 raw[KS / 2];
             float amax = 0.f;
 #pragma unroll
@@ -282,27 +292,33 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const int qe = q_exponent(amax);
-            rf[rr] = p.scale_log2 * exp2i(qe);
+            const float scale = p.scale_log2 * exp2i(qe);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) rf[nh][e] = __shfl_sync(0xffffffffu, scale, 4 * (2 * t + e));
             const float f = exp2i(-qe);
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint4 r = raw[2 * j + (x >> 1)];
-                    qa[4 * j + x][rr] = bf16x2_to_f16x2((x & 1) ? r.z : r.x, f);
-                    qa[4 * j + x][2 + rr] = bf16x2_to_f16x2((x & 1) ? r.w : r.y, f);
+                    qb[4 * j + x][nh][0] = bf16x2_to_f16x2((x & 1) ? r.z : r.x, f);
+                    qb[4 * j + x][nh][1] = bf16x2_to_f16x2((x & 1) ? r.w : r.y, f);
                 }
         }
-        float m_run[R], l_run[R];
+        float m_run[NH][2], l_run[NH][2];
 #pragma unroll
-        for (int rr = 0; rr < R; ++rr) {
-            m_run[rr] = -INFINITY;
-            l_run[rr] = 0.f;
-        }
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m_run[nh][e] = -INFINITY;
+                l_run[nh][e] = 0.f;
+            }
         int X = -126;                          // the largest value exponent so far
-        float o[NT][4];
+        float o[MT][NH][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) o[j][nh][0] = o[j][nh][1] = o[j][nh][2] = o[j][nh][3] = 0.f;
 
         for (int j = 0; j < nst; ++j) {
             const uint32_t gg = gs + j;
@@ -317,82 +333,105 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                     const int key = kb0 + 8 * r8;
                     return kt + ((((key >> lgrb) * HG + h) << lgrb) + (key & (RB - 1))) * D;
                 };
-                float s[4][4];
+                // scores, keys x heads: m tile mt holds keys 16 mt .. (rows g: r8 = 2 mt, rows
+                // g + 8: r8 = 2 mt + 1)
+                float s[2][NH][4];
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-                    const uint32_t rb = row_base(nt);
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int jj = 0; jj < D / 64; ++jj) {
-                        const uint4 v = lds128(chunk_addr<D>(rb, kappa<D>(g), t + 4 * jj));
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    for (int nh = 0; nh < NH; ++nh) s[mt][nh][0] = s[mt][nh][1] = s[mt][nh][2] = s[mt][nh][3] = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(s[nt], qa[4 * jj + k], e4m3_lo(x[k]), e4m3_hi(x[k]));
+                for (int jj = 0; jj < D / 64; ++jj) {
+                    uint32_t x[4][4];
+#pragma unroll
+                    for (int r8 = 0; r8 < 4; ++r8) {
+                        const uint4 v = lds128(chunk_addr<D>(row_base(r8), kappa<D>(g), t + 4 * jj));
+                        x[r8][0] = v.x;
+                        x[r8][1] = v.y;
+                        x[r8][2] = v.z;
+                        x[r8][3] = v.w;
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const uint32_t a[4] = {e4m3_lo(x[2 * mt][k]), e4m3_lo(x[2 * mt + 1][k]),
+                                                   e4m3_hi(x[2 * mt][k]), e4m3_hi(x[2 * mt + 1][k])};
+#pragma unroll
+                            for (int nh = 0; nh < NH; ++nh)
+                                mma_f16(s[mt][nh], a, qb[4 * jj + k][nh][0], qb[4 * jj + k][nh][1]);
+                        }
                 }
                 // the scale exponents of each eight keys
                 const uint8_t *sc = smem + C::kScaleOff + stage * 128 + h * (C::kKeys >> lgsb) + (kb0 >> lgsb);
                 float kf[4], vf[4];
                 int vx[4], Xn = X;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    kf[nt] = exp2i(q8_exp(sc[(8 * nt) >> lgsb]));
-                    vx[nt] = q8_exp(sc[64 + ((8 * nt) >> lgsb)]);
-                    if (8 * nt < nv)
-                        Xn = max(Xn, vx[nt]);
+                for (int r8 = 0; r8 < 4; ++r8) {
+                    kf[r8] = exp2i(q8_exp(sc[(8 * r8) >> lgsb]));
+                    vx[r8] = q8_exp(sc[64 + ((8 * r8) >> lgsb)]);
+                    if (8 * r8 < nv)
+                        Xn = max(Xn, vx[r8]);
                 }
                 const float xs = exp2i(max(X - Xn, -126));
                 X = Xn;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) vf[nt] = exp2i(min(max(vx[nt] - X, -100), 0) + 15);
-                uint32_t pa[2][4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) pa[k][0] = pa[k][1] = pa[k][2] = pa[k][3] = 0u;
-                float scale_o[2] = {1.f, 1.f};
+                for (int r8 = 0; r8 < 4; ++r8) vf[r8] = exp2i(min(max(vx[r8] - X, -100), 0) + 15);
+                // softmax of heads 2t, 2t + 1 (+ 8) over this lane's keys kappa(g) of each eight,
+                // then over the lanes of the other g
+                uint32_t pb[4][NH];
+                float scale_o[NH][2];
                 bool moved = false;
+                const int mykey = kappa<D>(g);
 #pragma unroll
-                for (int rr = 0; rr < R; ++rr) {
-                    float mx = -INFINITY;
+                for (int nh = 0; nh < NH; ++nh) {
+                    float pr[4][2];
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        const float f = fminf(rf[rr] * kf[nt], 3.0e38f);   // a zero score stays zero
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            s[nt][2 * rr + e] *= f;
-                            if (8 * nt + kappa<D>(2 * t + e) >= nv) s[nt][2 * rr + e] = -INFINITY;
-                            mx = fmaxf(mx, s[nt][2 * rr + e]);
+                        for (int r8 = 0; r8 < 4; ++r8) {
+                            // a zero score stays zero
+                            float v = s[r8 >> 1][nh][(r8 & 1) * 2 + e] * fminf(rf[nh][e] * kf[r8], 3.0e38f);
+                            if (8 * r8 + mykey >= nv)
+                                v = -INFINITY;
+                            pr[r8][e] = v;
+                            mx = fmaxf(mx, v);
                         }
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float m_new = fmaxf(m_run[rr], mx);
-                    const float alpha = m_new == m_run[rr] ? 1.f : ex2_approx(m_run[rr] - m_new);
-                    m_run[rr] = m_new;
-                    const float mref = m_new == -INFINITY ? 0.f : m_new;
-                    float psum = 0.f;
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float m_new = fmaxf(m_run[nh][e], mx);
+                        const float alpha = m_new == m_run[nh][e] ? 1.f : ex2_approx(m_run[nh][e] - m_new);
+                        m_run[nh][e] = m_new;
+                        const float mref = m_new == -INFINITY ? 0.f : m_new;
+                        float psum = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        const float p0 = ex2_approx(s[nt][2 * rr] - mref);
-                        const float p1 = ex2_approx(s[nt][2 * rr + 1] - mref);
-                        psum += p0 + p1;
-                        // A fragment of k step nt / 2: its first or second eight keys
-                        pa[nt >> 1][(nt & 1) * 2 + rr] = pack_f16x2(p0 * vf[nt], p1 * vf[nt]);
+                        for (int r8 = 0; r8 < 4; ++r8) {
+                            pr[r8][e] = ex2_approx(pr[r8][e] - mref);
+                            psum += pr[r8][e];
+                        }
+                        l_run[nh][e] = l_run[nh][e] * alpha + psum;
+                        scale_o[nh][e] = alpha * xs;
+                        moved = moved || scale_o[nh][e] != 1.f;
                     }
-                    l_run[rr] = l_run[rr] * alpha + psum;
-                    scale_o[rr] = alpha * xs;
-                    moved = moved || scale_o[rr] != 1.f;
+                    // keys x heads to the heads x keys of a B operand
+#pragma unroll
+                    for (int r8 = 0; r8 < 4; ++r8)
+                        pb[r8][nh] = transpose_8x8(pack_f16x2(pr[r8][0] * vf[r8], pr[r8][1] * vf[r8]));
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int j2 = 0; j2 < MT; ++j2)
 #pragma unroll
-                        for (int rr = 0; rr < R; ++rr) {
-                            o[nt][2 * rr] *= scale_o[rr];
-                            o[nt][2 * rr + 1] *= scale_o[rr];
+                        for (int nh = 0; nh < NH; ++nh) {
+                            o[j2][nh][0] *= scale_o[nh][0];
+                            o[j2][nh][1] *= scale_o[nh][1];
+                            o[j2][nh][2] *= scale_o[nh][0];
+                            o[j2][nh][3] *= scale_o[nh][1];
                         }
                 }
-                // O += P V, 16 keys at a time
+                // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     constexpr int W = D / 32;              // 32-bit words of a lane's column piece
@@ -425,10 +464,13 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                         const uint32_t b = __byte_perm(rows[0][x], rows[1][x], 0x7362);
                         const uint32_t c = __byte_perm(rows[2][x], rows[3][x], 0x5140);
                         const uint32_t d = __byte_perm(rows[2][x], rows[3][x], 0x7362);
-                        mma_f16(o[4 * x + 0], pa[k], e4m3_lo(a), e4m3_lo(c));
-                        mma_f16(o[4 * x + 1], pa[k], e4m3_hi(a), e4m3_hi(c));
-                        mma_f16(o[4 * x + 2], pa[k], e4m3_lo(b), e4m3_lo(d));
-                        mma_f16(o[4 * x + 3], pa[k], e4m3_hi(b), e4m3_hi(d));
+                        const uint32_t lo[4] = {e4m3_lo(a), e4m3_hi(a), e4m3_lo(c), e4m3_hi(c)};
+                        const uint32_t hi[4] = {e4m3_lo(b), e4m3_hi(b), e4m3_lo(d), e4m3_hi(d)};
+#pragma unroll
+                        for (int nh = 0; nh < NH; ++nh) {
+                            mma_f16(o[2 * x][nh], lo, pb[2 * k][nh], pb[2 * k + 1][nh]);
+                            mma_f16(o[2 * x + 1][nh], hi, pb[2 * k][nh], pb[2 * k + 1][nh]);
+                        }
                     }
                 }
             }
@@ -437,66 +479,71 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                 mbar_arrive(&bars->empty[stage]);
         }
         gs += nst;
-        // O_true = o * 2^(X - 15); lane (g, t): of row g (+ 8), the D/8 columns from piece
-        // chi(2t) on in o[.][0 (2)], from chi(2t + 1) on in o[.][1 (3)]
+        // O_true = o * 2^(X - 15); lane (g, t) holds, of heads 2t + e (+ 8), the D/8 columns
+        // from piece chi(g) on: column 2 j in o[j][.][e], 2 j + 1 in o[j][.][2 + e]
         const float of = exp2i(X) * exp2i(-15);
+        const int col0 = chi<D>(g) * NT;
 #pragma unroll
-        for (int rr = 0; rr < R; ++rr) {
-            l_run[rr] += __shfl_xor_sync(0xffffffffu, l_run[rr], 1);
-            l_run[rr] += __shfl_xor_sync(0xffffffffu, l_run[rr], 2);
-        }
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) l_run[nh][e] += __shfl_xor_sync(0xffffffffu, l_run[nh][e], x);
         if constexpr (C::kParts == 1) {
 #pragma unroll
-            for (int rr = 0; rr < R; ++rr) {
-                const int row = g + 8 * rr;
-                if (row >= G)
-                    continue;
-                const int hq = kvh * G + row;
-                if (w.nsplit > 1) {
-                    const int64_t pr = (int64_t)w.pbase + (int64_t)hq * w.nsplit + w.split;
+            for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 2 * t + e + 8 * nh;
+                    if (row >= G)
+                        continue;
+                    const int hq = kvh * G + row;
+                    if (w.nsplit > 1) {
+                        const int64_t pr = (int64_t)w.pbase + (int64_t)hq * w.nsplit + w.split;
 #pragma unroll
-                        for (int x = 0; x < NT / 4; ++x)
-                            *reinterpret_cast<float4 *>(p.part_o + pr * D + chi<D>(2 * t + e) * NT + 4 * x) =
-                                make_float4(o[4 * x][2 * rr + e] * of, o[4 * x + 1][2 * rr + e] * of,
-                                            o[4 * x + 2][2 * rr + e] * of, o[4 * x + 3][2 * rr + e] * of);
-                    if (t == 0)
-                        reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m_run[rr], l_run[rr]);
-                } else {
-                    const float inv = of * (l_run[rr] > 0.f ? 1.f / l_run[rr] : 0.f);   // a NaN sum leaves o NaN
-                    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) + ((int64_t)w.t * p.num_q_heads + hq) * D;
+                        for (int j = 0; j < MT; j += 2)
+                            *reinterpret_cast<float4 *>(p.part_o + pr * D + col0 + 2 * j) =
+                                make_float4(o[j][nh][e] * of, o[j][nh][2 + e] * of, o[j + 1][nh][e] * of,
+                                            o[j + 1][nh][2 + e] * of);
+                        if (g == 0)
+                            reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m_run[nh][e], l_run[nh][e]);
+                    } else {
+                        const float l = l_run[nh][e];
+                        const float inv = of * (l > 0.f ? 1.f / l : 0.f);   // a NaN sum leaves o NaN
+                        __nv_bfloat16 *dst =
+                            reinterpret_cast<__nv_bfloat16 *>(p.out) + ((int64_t)w.t * p.num_q_heads + hq) * D + col0;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int x = 0; x < NT / 8; ++x)
-                            *reinterpret_cast<uint4 *>(dst + chi<D>(2 * t + e) * NT + 8 * x) =
-                                make_uint4(pack_bf16x2(o[8 * x][2 * rr + e] * inv, o[8 * x + 1][2 * rr + e] * inv),
-                                           pack_bf16x2(o[8 * x + 2][2 * rr + e] * inv, o[8 * x + 3][2 * rr + e] * inv),
-                                           pack_bf16x2(o[8 * x + 4][2 * rr + e] * inv, o[8 * x + 5][2 * rr + e] * inv),
-                                           pack_bf16x2(o[8 * x + 6][2 * rr + e] * inv, o[8 * x + 7][2 * rr + e] * inv));
+                        for (int j = 0; j < MT; j += 4)
+                            *reinterpret_cast<uint4 *>(dst + 2 * j) =
+                                make_uint4(pack_bf16x2(o[j][nh][e] * inv, o[j][nh][2 + e] * inv),
+                                           pack_bf16x2(o[j + 1][nh][e] * inv, o[j + 1][nh][2 + e] * inv),
+                                           pack_bf16x2(o[j + 2][nh][e] * inv, o[j + 2][nh][2 + e] * inv),
+                                           pack_bf16x2(o[j + 3][nh][e] * inv, o[j + 3][nh][2 + e] * inv));
+                    }
                 }
-            }
         } else {
             // the warps of a head meet: [warp][row] max and sum, [warp][row][D] O
             float *mm = reinterpret_cast<float *>(smem + C::kMergeOff);
             float *ll = mm + 8 * C::kRows;
             float *oo = ll + 8 * C::kRows;
 #pragma unroll
-            for (int rr = 0; rr < R; ++rr) {
-                const int row = g + 8 * rr;
-                if (row >= G)
-                    continue;
-                if (t == 0) {
-                    mm[warp * C::kRows + row] = m_run[rr];
-                    ll[warp * C::kRows + row] = l_run[rr];
+            for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = 2 * t + e + 8 * nh;
+                    if (row >= G)
+                        continue;
+                    if (g == 0) {
+                        mm[warp * C::kRows + row] = m_run[nh][e];
+                        ll[warp * C::kRows + row] = l_run[nh][e];
+                    }
+                    float *dst = oo + (warp * C::kRows + row) * D + col0;
+#pragma unroll
+                    for (int j = 0; j < MT; j += 2)
+                        *reinterpret_cast<float4 *>(dst + 2 * j) =
+                            make_float4(o[j][nh][e] * of, o[j][nh][2 + e] * of, o[j + 1][nh][e] * of,
+                                        o[j + 1][nh][2 + e] * of);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-                        oo[(warp * C::kRows + row) * D + chi<D>(2 * t + e) * NT + x] = o[x][2 * rr + e] * of;
-            }
             named_bar_sync(1, 256);
             for (int e = threadIdx.x; e < HG * G * D; e += 256) {
                 const int hh = e / (G * D), row = e / D % G, d = e % D;
