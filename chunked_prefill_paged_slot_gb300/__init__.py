@@ -17,7 +17,9 @@ this package is its Python binding plus host-side orchestration:
   OnlineChunker             online chunk-size controller (windowed refit of f(C, H))
   BatchScheduler            token-budget batch builder with page allocation
   AttentionStep             one step (KV write + attention) with its workspace,
-                            on one stream or as two micro-batches on two streams
+                            on one stream or as two micro-batches on two streams,
+                            with rotary positions and over an 8-bit cache where asked
+  rope_table                cosines and sines for the rotary appends
 """
 from ._lib import (  # noqa: F401
     CpsaError, load, cpp_kv_cache_write, cpp_rope_kv_cache_write, cpp_rope_kv_cache_write_q8,
@@ -31,4 +33,4 @@ from ._lib import (  # noqa: F401
     DEV_SLOT_OUT_OF_RANGE, DEV_PAGE_OUT_OF_RANGE, DEV_SEQ_LT_QUERY, DEV_TOKENS_MISMATCH, DEV_SEQ_GT_TABLE,
     DEV_SPLITS_CLAMPED, DEV_WAIT_TIMEOUT, DEV_POSITION_OUT_OF_RANGE,
 )
-from .step import AttentionStep  # noqa: F401
+from .step import AttentionStep, rope_table  # noqa: F401

@@ -527,6 +527,13 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.max_splits = max_kv_splits;
     const int dec_heads = q8 ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
+    pp.dec_keys = dec_heads > 1 ? kDecodeKeysPerSplitGrouped : kDecodeKeysPerSplit;
+    if (q8) {
+        const int64_t items = (num_reqs < num_tokens ? num_reqs : num_tokens) * (num_kv_heads / dec_heads);
+        pp.dec_keys = 2 * items >= sms   ? kDecodeKeysPerSplitGrouped
+                      : 8 * items > sms ? kDecodeKeysPerSplitQ8Few
+                                        : kDecodeKeysPerSplitQ8Fewest;
+    }
     pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
     pp.fused = fused ? 1 : 0;
     pp.prow_capacity = cap;

@@ -55,6 +55,13 @@ constexpr int kDecodeKeysPerSplit = 4096;   // keys per decode split (multiple o
 // per-head items' count: they split every 1024 keys so that small decode batches
 // still occupy the GPU (still a function of the row's own length only).
 constexpr int kDecodeKeysPerSplitGrouped = 1024;
+// Over the 8-bit cache a row's keys per split also go by how many rows a call can hold
+// (its requests, which the host knows): every 1024 once a whole row each would occupy half
+// the SMs (128 rows of 2600 to 5200 keys: 196 us, 199 us every 256), else every 256, and
+// every 128 where even eight splits of every row leave SMs idle (one row of 777 keys:
+// 22 us a call, 35 us every 1024).
+constexpr int kDecodeKeysPerSplitQ8Few = 256;
+constexpr int kDecodeKeysPerSplitQ8Fewest = 128;
 constexpr int kMaxSplitUnits = kMaxChunkGrid;   // a split unit holds a run boundary: at most grid - 1
 constexpr int kMergeCounters = 2 * 4;          // per split unit: q heads (<= 2) x 4 softmax warps
 // A batch of one prefill request skips the plan kernel: every chunk-kernel CTA
@@ -158,6 +165,7 @@ struct PlanParams {
     int Hq, Hkv, group, nq;    // nq: q heads per chunk-kernel CTA (1 or 2)
     int max_splits;
     int dec_heads;             // kv heads per decode item: 1, or a group of 4 or 8 (the grouped decode kernel)
+    int dec_keys;              // keys per decode split (a multiple of kDecodeChunk)
     int chunk_grid;            // CTAs of the chunk kernel (stream-K runs)
     int fused;                 // KV write fused: the chunk's own keys form tiles of their own
     int64_t prow_capacity;     // partial rows that fit
