@@ -17,9 +17,12 @@
 // pairs, and the columns from rot on, which pass through). Reading and writing the
 // same bytes in one thread is what lets q_out be q itself.
 //
-// Bound by memory: 2 bytes in and 2 (or 1) out per element, and the table's row.
+// Bound by memory: 2 bytes in and 2 (or 1) out per element, and the table's row. The
+// bf16 append of a 32768-token prompt (32/8 heads, D 128, 823 MB) takes 130 us, a plain
+// copy of as many bytes 125 us; small calls are bound by latency (one token: 4 us).
 #include "common.cuh"
 #include "kernels.cuh"
+#include "q8.cuh"
 
 namespace cpsa {
 
@@ -253,11 +256,32 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
     const int lg_sb = min(4, p.lg_page);
     const int64_t w0 = window * kQ8Rows;
 
-    // slot of token t, or -1 where nothing is to be written
-    auto slot_of = [&](int64_t t, bool report) -> int64_t {
+    // The window's rows are asked for before anything is known of their slots: nearly
+    // always they are the rows to do (else they are loaded again), and the two latencies
+    // overlap.
+    uint4 v0[PASSES], v1[PASSES];
+    int c0, c1;
+    unit_cols(u, is_k ? p.rot : 0, p.inter, c0, c1);
+    const __nv_bfloat16 *src = is_k ? p.k + kvh * D : p.v + kvh * D;
+    const int64_t stride = is_k ? p.k_stride : p.v_stride;
+    auto load_rows = [&](int64_t first) {
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+            const int64_t t = first + q * RPP + rsub;
+            v0[q] = v1[q] = make_uint4(0, 0, 0, 0);
+            if (t < p.num_tokens) {
+                v0[q] = __ldcs(reinterpret_cast<const uint4 *>(src + t * stride + c0));
+                v1[q] = __ldcs(reinterpret_cast<const uint4 *>(src + t * stride + c1));
+            }
+        }
+    };
+    load_rows(w0);
+
+    // slot and position of token t, or -1 where nothing is to be written
+    auto slot_of = [&](int64_t t, bool report, int64_t &pos) -> int64_t {
+        pos = 0;
         if (t < 0 || t >= p.num_tokens)
             return -1;
-        int64_t pos;
         const int state = position_state(p, t, pos);
         const int64_t s = __ldg(p.slot_mapping + t);
         if (state != 0) {
@@ -274,16 +298,18 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
     };
     // lane l looks at token w0 + l: the window and the up to 15 tokens behind it
     // that can still belong to its last run
-    const int64_t slot = slot_of(w0 + lane, job == 0 && lane < kQ8Rows);
+    int64_t pos, pos_before;
+    const int64_t slot = slot_of(w0 + lane, job == 0 && lane < kQ8Rows, pos);
     int64_t before = __shfl_up_sync(0xffffffffu, slot, 1);
     if (lane == 0)
-        before = slot_of(w0 - 1, false);
+        before = slot_of(w0 - 1, false, pos_before);
     const bool live = slot >= 0;
     const bool joins = live && before >= 0 && (before >> lg_sb) == (slot >> lg_sb) && before < slot;
     const uint32_t lead = __ballot_sync(0xffffffffu, live && !joins);
     const uint32_t cont = __ballot_sync(0xffffffffu, joins);
     // the rows to do: runs whose first token is in the window
     uint32_t todo = lead & 0xffffu;
+    int loaded = 0;   // v0, v1 hold the rows from this one on
     while (todo) {
         // the next whole runs, at most kQ8Rows rows from the first one's start (a run is
         // at most SB <= 16 rows long, so there is always at least one)
@@ -303,36 +329,42 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
         // row i's slot in lane i; rows between runs (padding) have -1
         const int64_t rslot = __shfl_sync(0xffffffffu, slot, (base + lane) & 31);
         const bool mine = lane < rows && rslot >= 0;
-        // 1. all rows into registers, rotated, and their largest finite magnitudes
-        float x0[PASSES][8], x1[PASSES][8];
+        if (base != loaded)
+            load_rows(w0 + base);
+        loaded = base;
+        const int64_t rpos = __shfl_sync(0xffffffffu, pos, (base + lane) & 31);
+        // this lane's 16 values of pass q, rotated
+        auto values = [&](int q, float (&x0)[8], float (&x1)[8]) {
+            widen8(v0[q], x0);
+            widen8(v1[q], x1);
+            const int64_t at = __shfl_sync(0xffffffffu, rpos, q * RPP + rsub);
+            if (is_k && u < (p.rot >> 4)) {
+                float c[8], s[8];
+                load8(p.cos_sin + at * p.rot + 8 * u, c);
+                load8(p.cos_sin + at * p.rot + (p.rot >> 1) + 8 * u, s);
+                rotate_unit(x0, x1, c, s, p.inter);
+            }
+        };
+        // 1. the rows' largest finite magnitudes
         float rowmax = 0.f;
-        int c0, c1;
-        unit_cols(u, is_k ? p.rot : 0, p.inter, c0, c1);
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
             const int row = q * RPP + rsub;
-            const int64_t t = w0 + base + row;
             const bool on = __shfl_sync(0xffffffffu, (int)mine, row) != 0;
             float m = 0.f;
-            if (on) {
-                const __nv_bfloat16 *src =
-                    is_k ? p.k + t * p.k_stride + kvh * D : p.v + t * p.v_stride + kvh * D;
-                widen8(__ldcs(reinterpret_cast<const uint4 *>(src + c0)), x0[q]);
-                widen8(__ldcs(reinterpret_cast<const uint4 *>(src + c1)), x1[q]);
-                if (is_k && u < (p.rot >> 4)) {
-                    float c[8], s[8];
-                    const int64_t pos = __ldg(p.positions + t);
-                    load8(p.cos_sin + pos * p.rot + 8 * u, c);
-                    load8(p.cos_sin + pos * p.rot + (p.rot >> 1) + 8 * u, s);
-                    rotate_unit(x0[q], x1[q], c, s, p.inter);
-                }
+            if (is_k) {
+                float x0[8], x1[8];
+                values(q, x0, x1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float a = fabsf(x0[q][i]), b = fabsf(x1[q][i]);
+                    const float a = fabsf(x0[i]), b = fabsf(x1[i]);
                     m = fmaxf(m, a < INFINITY ? a : 0.f);      // false for NaN
                     m = fmaxf(m, b < INFINITY ? b : 0.f);
                 }
+            } else {
+                m = fmaxf(bf16x8_amax(v0[q]), bf16x8_amax(v1[q]));
             }
+            m = on ? m : 0.f;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             // to the lane of the row's number
@@ -407,15 +439,15 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             const float f = exp2_int(-__shfl_sync(0xffffffffu, x, row));
             uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(
                 0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(bytes + (int64_t)off * D), row));
+            float x0[8], x1[8];
+            values(q, x0, x1);
             if (!on)
                 continue;
             uint32_t b0[2], b1[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                b0[i] = e4m3x2(x0[q][4 * i] * f, x0[q][4 * i + 1] * f) |
-                        e4m3x2(x0[q][4 * i + 2] * f, x0[q][4 * i + 3] * f) << 16;
-                b1[i] = e4m3x2(x1[q][4 * i] * f, x1[q][4 * i + 1] * f) |
-                        e4m3x2(x1[q][4 * i + 2] * f, x1[q][4 * i + 3] * f) << 16;
+                b0[i] = e4m3x2(x0[4 * i] * f, x0[4 * i + 1] * f) | e4m3x2(x0[4 * i + 2] * f, x0[4 * i + 3] * f) << 16;
+                b1[i] = e4m3x2(x1[4 * i] * f, x1[4 * i + 1] * f) | e4m3x2(x1[4 * i + 2] * f, x1[4 * i + 3] * f) << 16;
             }
             *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(b0[0], b0[1]);
             *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(b1[0], b1[1]);
@@ -426,8 +458,13 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
 
 // Blocks [0, kv_blocks): one warp per (window, kv head, k or v), heads fastest (the
 // table's rows of a window are shared through L1); the rest: the q heads.
+// Five blocks an SM (102 registers): a 32768-token prompt (32/8 heads, D 128, 756 MB,
+// which a plain copy of as many bytes moves in 118 us) takes 151 us; 165 us with the 116
+// registers the compiler takes by itself, 152, 154 and 206 us with six, seven and eight
+// blocks; 181 us when the rows were asked for only once their slots were known and kept
+// rotated in registers.
 template <int D, int HPT>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_q8_kernel(const RopeParams p, int kv_blocks)
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const RopeParams p, int kv_blocks)
 {
     pdl_trigger();
     pdl_wait();
