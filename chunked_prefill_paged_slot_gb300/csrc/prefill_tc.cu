@@ -1522,7 +1522,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 }
                 const float mref = m_use == -INFINITY ? 0.f : m_use;
                 const uint64_t sl2x2 = f2_pack(tsl2, tsl2);
-                const uint64_t nref2 = f2_pack(-mref, -mref);
+                // Q8: probabilities times 2^kQ8Lift, the row sum with them (the final O / l does not
+                // change): at most 2^8 * 2^7 in f16, and whole down to 2^-21 of the largest
+                const float nref = Q8 ? (float)kQ8Lift - mref : -mref;
+                const uint64_t nref2 = f2_pack(nref, nref);
                 uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
