@@ -174,18 +174,18 @@ uint32_t next_epoch()
 // tiles holds at most (R - 2) / L + 2 pieces, L the shortest unit; that ratio is
 // largest with no history (L = 1, R = R0, every unit as short as it gets) and
 // stays below R0 + 3 for any history (the units grow as fast as the run).
-bool self_plan_fits(int64_t num_tokens, int units_per_qtile, int grid, int cap)
+bool self_plan_fits(int64_t num_tokens, int units_per_qtile, int grid, int cap, int unit_cost)
 {
     // the most pieces a run can hold is in the no-history case (the shortest
-    // units): a run of r0 positions meets at most r0 / (1 + kUnitCostTiles) + 2 units
+    // units): a run of r0 positions meets at most r0 / (1 + unit_cost) + 2 units
     // (each unit takes at least one tile and its fixed cost, plus the ones it starts
     // and ends inside); one more for safety
     const int64_t nqt = (num_tokens + kTileM - 1) / kTileM;
-    const int64_t w0 = (int64_t)units_per_qtile * (nqt * (nqt + 1) / 2 + nqt * kUnitCostTiles);
+    const int64_t w0 = (int64_t)units_per_qtile * (nqt * (nqt + 1) / 2 + nqt * unit_cost);
     int64_t r0 = (w0 + grid - 1) / grid;
     if (r0 < kMinRunTiles)
         r0 = kMinRunTiles;
-    return r0 / (1 + kUnitCostTiles) + 3 <= cap;
+    return r0 / (1 + unit_cost) + 3 <= cap;
 }
 
 int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t *slot_mapping, void *k_cache,
@@ -527,6 +527,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.max_splits = max_kv_splits;
     const int dec_heads = q8 ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
+    pp.unit_cost = q8 ? unit_cost_q8(head_dim) : kUnitCostTiles;
     pp.dec_keys = dec_heads > 1 ? kDecodeKeysPerSplitGrouped : kDecodeKeysPerSplit;
     if (q8) {
         const int64_t items = (num_reqs < num_tokens ? num_reqs : num_tokens) * (num_kv_heads / dec_heads);
@@ -555,7 +556,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     const bool single_prefill = num_reqs == 1 && num_tokens >= 2;
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
     const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
-                                                            q8 ? kSelfPlanCapQ8 : kSelfPlanCap);
+                                                            q8 ? kSelfPlanCapQ8 : kSelfPlanCap, pp.unit_cost);
     mark(0, s);
     if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
         return CPSA_ERR_CUDA;

@@ -53,7 +53,7 @@ __device__ __forceinline__ int unit_tiles(const PlanParams &p, const Req &rq, in
 }
 
 // Stream-K positions of all prefill units of one request: their KV tiles plus
-// kUnitCostTiles per unit (0 for decode / invalid / empty).
+// unit_cost per unit (0 for decode / invalid / empty).
 __device__ int prefill_tiles(const PlanParams &p, const Req &rq)
 {
     if (!rq.valid || rq.q < 2)
@@ -61,7 +61,7 @@ __device__ int prefill_tiles(const PlanParams &p, const Req &rq)
     const int units_per_qtile = p.Hkv * (p.group / p.nq);
     int tiles = 0;
     for (int qt = 0; qt * kTileM < rq.q; ++qt)
-        tiles += (unit_tiles(p, rq, qt, min(kTileM, rq.q - qt * kTileM)) + kUnitCostTiles) * units_per_qtile;
+        tiles += (unit_tiles(p, rq, qt, min(kTileM, rq.q - qt * kTileM)) + p.unit_cost) * units_per_qtile;
     return tiles;
 }
 
@@ -72,7 +72,7 @@ __device__ int longest_unit(const PlanParams &p, const Req &rq)
     if (!rq.valid || rq.q < 2)
         return 0;
     const int nqt = ceil_div(rq.q, kTileM);
-    return unit_tiles(p, rq, nqt - 1, rq.q - (nqt - 1) * kTileM) + kUnitCostTiles;
+    return unit_tiles(p, rq, nqt - 1, rq.q - (nqt - 1) * kTileM) + p.unit_cost;
 }
 
 // Positions of the request's shortest unit (its first query tile), INT_MAX for
@@ -81,7 +81,7 @@ __device__ int shortest_unit(const PlanParams &p, const Req &rq)
 {
     if (!rq.valid || rq.q < 2)
         return 0x7fffffff;
-    return unit_tiles(p, rq, 0, min(kTileM, rq.q)) + kUnitCostTiles;
+    return unit_tiles(p, rq, 0, min(kTileM, rq.q)) + p.unit_cost;
 }
 
 __device__ int decode_splits(const Req &rq, int max_splits, int dec_keys)
@@ -167,9 +167,9 @@ __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int ti
         const int nkv = a == 0 ? nkv_last : hb + qt + 1;
         // tiles of the units of query tiles nqt - 1 .. qt + 1: nkv_last, then hb + nqt - a' for a' = 1 .. a - 1
         const int before = a == 0 ? 0 : nkv_last + (a - 1) * (hb + nqt) - (a - 1) * a / 2;
-        // the unit's positions [u0, u1): kUnitCostTiles of fixed cost, then its tiles from t0
-        const int u0 = tile_off + upq * (before + a * kUnitCostTiles) + j * (nkv + kUnitCostTiles);
-        const int t0 = u0 + kUnitCostTiles, u1 = t0 + nkv;
+        // the unit's positions [u0, u1): unit_cost of fixed cost, then its tiles from t0
+        const int u0 = tile_off + upq * (before + a * p.unit_cost) + j * (nkv + p.unit_cost);
+        const int t0 = u0 + p.unit_cost, u1 = t0 + nkv;
         const int first = t0 / run;
         const int np = active ? (cut ? (u1 - 1) / run - first + 1 : 1) : 0;
         const bool split = np > 1;

@@ -46,6 +46,12 @@ constexpr int kMinRunTiles = 4;             // shortest run of KV tiles per CTA
 #define CPSA_UNIT_COST_TILES 2
 #endif
 constexpr int kUnitCostTiles = CPSA_UNIT_COST_TILES;   // a unit's fixed cost, in KV tiles (< kMinRunTiles)
+// Over the 8-bit cache a unit of 128 columns costs more to start (its Q passes through
+// registers). At 3 eight fresh prompts of 2600 tokens take 663 us and a fresh chunk of 512
+// 21 us, at 2 712 and 30 us (one prompt of 2000 tokens: 72 and 69 us); with 64 columns
+// ragged prompts take 90 us at 3, 88 at 2.
+__host__ __device__ constexpr int unit_cost_q8(int head_dim) { return head_dim == 128 ? 3 : kUnitCostTiles; }
+static_assert(unit_cost_q8(128) < kMinRunTiles, "a run must hold more than one unit's start");
 static_assert(kUnitCostTiles >= 0 && kUnitCostTiles < kMinRunTiles, "a run must hold more than one unit's start");
 constexpr int kCutCostTiles = 6;            // a run's extra item and merge when a unit is cut, in KV tiles
 constexpr int kMaxChunkGrid = 256;          // upper bound of the chunk kernel's grid (SMs)
@@ -165,6 +171,7 @@ struct PlanParams {
     int Hq, Hkv, group, nq;    // nq: q heads per chunk-kernel CTA (1 or 2)
     int max_splits;
     int dec_heads;             // kv heads per decode item: 1, or a group of 4 or 8 (the grouped decode kernel)
+    int unit_cost;             // a unit's fixed cost in KV tiles: kUnitCostTiles, or unit_cost_q8
     int dec_keys;              // keys per decode split (a multiple of kDecodeChunk)
     int chunk_grid;            // CTAs of the chunk kernel (stream-K runs)
     int fused;                 // KV write fused: the chunk's own keys form tiles of their own

@@ -181,7 +181,7 @@ __device__ __forceinline__ int epoch_arrive(unsigned long long *cnt, uint32_t ep
 // self_plan_run); I is the integer type of the tile positions: 32 bits whenever
 // the request's W tiles fit (64-bit division is a long software routine on the
 // GPU, and this walk sits on every launch's critical path), 64 bits otherwise.
-template <int NQ, int CAP, typename I>
+template <int NQ, int CAP, int UC, typename I>
 __device__ __forceinline__ int self_plan_walk(PrefillItem *items, int lane, int nqt, int hb, int nkv_last, int upq,
                                               int pairs, I run, bool cut)
 {
@@ -198,9 +198,9 @@ __device__ __forceinline__ int self_plan_walk(PrefillItem *items, int lane, int 
         const int nkv = a == 0 ? nkv_last : hb + qt + 1;
         // KV tiles of one unit column before the a-th query tile from the last
         const I before = a == 0 ? (I)0 : (I)nkv_last + (I)(a - 1) * (I)(hb + nqt) - (I)((a - 1) * a / 2);
-        // the unit's positions: kUnitCostTiles of fixed cost from u0, its tiles [t0, u1)
-        const I u0 = (I)upq * (before + (I)a * kUnitCostTiles) + (I)j * (I)(nkv + kUnitCostTiles);
-        const I t0 = u0 + kUnitCostTiles, u1 = t0 + (I)nkv;
+        // the unit's positions: UC (the plan's unit_cost) of fixed cost from u0, its tiles [t0, u1)
+        const I u0 = (I)upq * (before + (I)a * UC) + (I)j * (I)(nkv + UC);
+        const I t0 = u0 + UC, u1 = t0 + (I)nkv;
         // with cuts a run takes every piece of a unit inside it; without, whole units
         // go to the run that holds their first tile
         const bool take = active && (cut ? (u1 > lo && t0 < hi) : (t0 >= lo && t0 < hi));
@@ -255,7 +255,7 @@ struct SelfPlanArgs {
     int num_tokens, max_blocks, page_size, group, num_kv_heads, fused, split_ok, split_clamped;
 };
 
-template <int NQ, int CAP>
+template <int NQ, int CAP, int UC>
 __device__ __noinline__ int self_plan_run(const SelfPlanArgs a, PrefillItem *items, int lane)
 {
     const int q = __ldg(a.query_lens), s = __ldg(a.seq_lens);
@@ -281,14 +281,14 @@ __device__ __noinline__ int self_plan_run(const SelfPlanArgs a, PrefillItem *ite
     const int hb = (hist + kTileN - 1) / kTileN;
     const int nkv_last = a.fused ? hb + nqt : (hist + q + kTileN - 1) / kTileN;
     const long long W = (long long)upq * (nkv_last + (long long)(nqt - 1) * (hb + nqt) - (long long)(nqt - 1) * nqt / 2 +
-                                          (long long)nqt * kUnitCostTiles);
-    const int shortest = (nqt == 1 ? nkv_last : hb + 1) + kUnitCostTiles;
+                                          (long long)nqt * UC);
+    const int shortest = (nqt == 1 ? nkv_last : hb + 1) + UC;
     const long long grid = gridDim.x;
     const long long run = max((W + grid - 1) / grid, (long long)kMinRunTiles);
-    const bool cut = a.split_ok && !(shortest >= run && nkv_last + kUnitCostTiles <= run + kCutCostTiles);
+    const bool cut = a.split_ok && !(shortest >= run && nkv_last + UC <= run + kCutCostTiles);
     int n = W + run < 0x7fffffffll
-                ? self_plan_walk<NQ, CAP, int>(items, lane, nqt, hb, nkv_last, upq, pairs, (int)run, cut)
-                : self_plan_walk<NQ, CAP, long long>(items, lane, nqt, hb, nkv_last, upq, pairs, run, cut);
+                ? self_plan_walk<NQ, CAP, UC, int>(items, lane, nqt, hb, nkv_last, upq, pairs, (int)run, cut)
+                : self_plan_walk<NQ, CAP, UC, long long>(items, lane, nqt, hb, nkv_last, upq, pairs, run, cut);
     if (n > CAP) {
         if (lane == 0)
             set_dev_error(a.dev_err, CPSA_DEV_PLAN_OVERFLOW);
@@ -1039,7 +1039,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         if (warp == C::kWriteWarp) {
             const SelfPlanArgs a{p.query_lens, p.seq_lens, p.dev_err, p.num_tokens, p.max_blocks, p.page_size,
                                  p.group, p.num_kv_heads, p.fused, p.split_ok, p.split_clamped};
-            const int n = self_plan_run<NQ, C::kPlanCap>(a, s_items, lane);
+            const int n = self_plan_run<NQ, C::kPlanCap, Q8 ? unit_cost_q8(D) : kUnitCostTiles>(a, s_items, lane);
             if (lane == 0) {
                 bars->it_begin = 0;
                 bars->it_end = n;
