@@ -176,14 +176,18 @@ def _where(stream, t, name):
     return stream.cuda_stream, stream.device_index
 
 
+def _elsewhere(t, name, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return CpsaError(f"{name} must be a CUDA tensor")
+    return CpsaError(f"{name} is on {t.device}, the call on cuda:{device}")
+
+
 def _ptr(t: torch.Tensor, kinds, name, device):
     """The address of a contiguous tensor of one of the types `kinds` (or of that type) on `device`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise CpsaError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise CpsaError(f"{name} is on {t.device}, the call on cuda:{device}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise _elsewhere(t, name, device)
     dt = t.dtype
-    if dt is not kinds and not (isinstance(kinds, tuple) and dt in kinds):
+    if dt is not kinds and not (type(kinds) is tuple and dt in kinds):
         raise CpsaError(f"{name} must be {' or '.join(map(str, kinds if isinstance(kinds, tuple) else (kinds,)))}, got {dt}")
     if not t.is_contiguous():
         raise CpsaError(f"{name} must be contiguous")
@@ -192,10 +196,8 @@ def _ptr(t: torch.Tensor, kinds, name, device):
 
 def _rows(t: torch.Tensor, tokens, heads, d, name, device):
     """A [tokens, heads, d] bf16 tensor whose heads are contiguous: its address and its token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise CpsaError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise CpsaError(f"{name} is on {t.device}, the call on cuda:{device}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise _elsewhere(t, name, device)
     if t.dtype is not _BF16:
         raise CpsaError(f"{name} must be {_BF16}, got {t.dtype}")
     s = t.stride()

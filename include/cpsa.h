@@ -239,8 +239,14 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
  * hold none of its places, may hold anything. A NaN key makes the rows that see
  * it NaN, a NaN value their column (and it may do so for that column of earlier
  * rows of the same chunk). (The pages have no counterpart.)
- * Every other argument, the workspace (same size functions), the device flags,
- * the splits and CUDA graph capture are cpp_chunked_prefill_attn's.
+ * Every other argument, the workspace (same size functions), the device flags
+ * and CUDA graph capture are cpp_chunked_prefill_attn's, and so are the splits,
+ * but for the keys per split of a decode row: they also go by num_reqs (fewer rows
+ * split finer), so a decode row's last-bit rounding can depend on it.
+ * Arithmetic: stored values enter the MMAs as f16, exact up to factors of powers of
+ * two for blocks down to 2^-22 of the largest scale among the 128 keys (K) or the
+ * keys so far (V) that are multiplied together, f16 under it; q rows likewise under
+ * a power of two of their own; probabilities in f16; everything else in fp32.
  */
 int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
                                 const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
