@@ -333,12 +333,13 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             load_rows(w0 + base);
         loaded = base;
         const int64_t rpos = __shfl_sync(0xffffffffu, pos, (base + lane) & 31);
-        // this lane's 16 values of pass q, rotated
-        auto values = [&](int q, float (&x0)[8], float (&x1)[8]) {
+        // this lane's 16 values of pass q, rotated; on: its row is one to do (any other's
+        // position may be no row of the table)
+        auto values = [&](int q, bool on, float (&x0)[8], float (&x1)[8]) {
             widen8(v0[q], x0);
             widen8(v1[q], x1);
             const int64_t at = __shfl_sync(0xffffffffu, rpos, q * RPP + rsub);
-            if (is_k && u < (p.rot >> 4)) {
+            if (on && is_k && u < (p.rot >> 4)) {
                 float c[8], s[8];
                 load8(p.cos_sin + at * p.rot + 8 * u, c);
                 load8(p.cos_sin + at * p.rot + (p.rot >> 1) + 8 * u, s);
@@ -354,7 +355,7 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             float m = 0.f;
             if (is_k) {
                 float x0[8], x1[8];
-                values(q, x0, x1);
+                values(q, on, x0, x1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float a = fabsf(x0[i]), b = fabsf(x1[i]);
@@ -440,7 +441,7 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(
                 0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(bytes + (int64_t)off * D), row));
             float x0[8], x1[8];
-            values(q, x0, x1);
+            values(q, on, x0, x1);
             if (!on)
                 continue;
             uint32_t b0[2], b1[2];

@@ -279,6 +279,31 @@ def test_flags_and_skipped_tokens(cuda_lib, q8):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+def test_no_position_outside_the_table_is_looked_up(cuda_lib, q8):
+    """Positions far behind and far before the table, between tokens that are done: their rows of it are not read."""
+    runs = [(0, 2, 0), (18, 1, 1 << 40), (19, 1, -(1 << 40)), (20, 5, 1), (40, 1, (1 << 62) + 5), (41, 1, -1), (42, 3, 2)]
+    c = Case(11, 4, 2, 128, 16, 64, 128, runs, top=6)
+    q_out = bf16(c.rng, (c.T, 4, 128)).cuda()
+    before = q_out.clone()
+    q, k, v, pos, cs, slots = c.args()
+    _, w = c.live()
+    sl = np.where(w, c.slots, -1)
+    (kc, ks), (vc, vs) = q8_cache(c), q8_cache(c)
+    if q8:
+        was = [x.view(torch.uint8).cpu().numpy() for x in (vc, vs)]
+        cuda_lib.cpp_rope_kv_cache_write_q8(q, k, v, pos, cs, slots, kc, vc, ks, vs, q_out, c.err)
+        check_q8(c, wide(v), False, np.zeros((c.T, 2, 128)), vc, vs, was[0], was[1], sl)
+    else:
+        kc, vc = (bf16(c.rng, (64, 2, 16, 128)).cuda() for _ in range(2))
+        want = wide(vc)
+        cuda_lib.cpp_rope_kv_cache_write(q, k, v, pos, cs, slots, kc, vc, q_out, c.err)
+        want[sl[w] // 16, :, sl[w] % 16] = wide(v)[w]
+        assert np.array_equal(wide(vc), want)
+    c.check_q(q_out, before, False)
+    assert cuda_lib.cpp_read_device_error(c.err) == cuda_lib.DEV_POSITION_OUT_OF_RANGE
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_strided_contiguous_and_in_place_agree(cuda_lib, q8):
     c = Case(6, 14, 2, 128, 16, 64, 96, RUNS["mixed"])
     q, k, v, pos, cs, slots = c.args()
