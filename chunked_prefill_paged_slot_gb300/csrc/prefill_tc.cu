@@ -1574,8 +1574,14 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    // Q8: this warp's rows of the item before have left its staging buffer. The
+                    // staged merge at the end of a run, which takes the buffers of all warps,
+                    // comes after both heads' last P.V and so after this in every warp.
+                    if (Q8 && D == 128 && t == 0)
+                        bulk_wait_group_read0();
                     mbar_arrive(&bars->p_full[wg]);
+                }
             }
             if (!ok)
                 break;
