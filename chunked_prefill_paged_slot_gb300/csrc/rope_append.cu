@@ -18,7 +18,7 @@
 // same bytes in one thread is what lets q_out be q itself.
 //
 // Bound by memory: 2 bytes in and 2 (or 1) out per element, and the table's row. The
-// bf16 append of a 32768-token prompt (32/8 heads, D 128, 823 MB) takes 130 us, a plain
+// bf16 append of a 32768-token prompt (32/8 heads, D 128, 823 MB) takes 125 us, a plain
 // copy of as many bytes 125 us; small calls are bound by latency (one token: 4 us).
 #include "common.cuh"
 #include "kernels.cuh"
@@ -481,16 +481,19 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const R
 }
 
 // Heads per thread: one while a single wave of threads holds every unit (the
-// fewest dependent steps, which is all that counts there), else four (the table's
-// values are loaded once for them).
-constexpr int kRopeHeads = 4;
+// fewest dependent steps, which is all that counts there), else two (four beside the
+// 8-bit cache's windows, whose registers leave fewer warps to keep loads in flight): the
+// table's values are loaded once for them. A 32768-token prompt into the bf16 cache takes
+// 125 us with two and 130 with four, into the 8-bit cache 172 and 151.
+constexpr int kRopeHeads = 2, kRopeHeadsQ8 = 4;
 
 template <int D>
 cudaError_t launch_rope_t(const RopeParams &p, bool q8, int num_sms, cudaStream_t s)
 {
     const int heads = q8 ? p.Hq : p.Hq + 2 * p.Hkv;
+    const int many = q8 ? kRopeHeadsQ8 : kRopeHeads;
     const bool one = p.num_tokens * heads * (D / 16) <= (int64_t)num_sms * 1024;
-    const int64_t items = p.num_tokens * (one ? heads : (heads + kRopeHeads - 1) / kRopeHeads) * (D / 16);
+    const int64_t items = p.num_tokens * (one ? heads : (heads + many - 1) / many) * (D / 16);
     int64_t blocks = (items + kRopeThreads - 1) / kRopeThreads;
     if (blocks > (int64_t)num_sms * 64)
         blocks = (int64_t)num_sms * 64;
@@ -501,7 +504,7 @@ cudaError_t launch_rope_t(const RopeParams &p, bool q8, int num_sms, cudaStream_
     const int64_t kv_blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     if (kv_blocks + blocks > 0x7fffffff)
         return cudaErrorInvalidValue;
-    return launch_pdl(false, one ? rope_append_q8_kernel<D, 1> : rope_append_q8_kernel<D, kRopeHeads>,
+    return launch_pdl(false, one ? rope_append_q8_kernel<D, 1> : rope_append_q8_kernel<D, kRopeHeadsQ8>,
                       dim3((unsigned)(kv_blocks + blocks)), dim3(kRopeThreads), 0, s, p, (int)kv_blocks);
 }
 
