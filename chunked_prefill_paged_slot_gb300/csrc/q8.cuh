@@ -74,13 +74,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 
 // Largest finite magnitude of eight bf16 numbers. Magnitudes of one format order like
 // their bits, so pairs of 16-bit integer maxima do; only where an infinity or NaN turns
-// up are the finite ones sorted out one by one.
-__device__ __forceinline__ float bf16x8_amax(const uint4 &v)
+// up (which sets `others`) are the finite ones sorted out one by one.
+__device__ __forceinline__ float bf16x8_amax(const uint4 &v, bool &others)
 {
     const uint32_t k = 0x7fff7fffu;
     const uint32_t w = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
     uint32_t m = max(w & 0xffffu, w >> 16);
     if (m >= 0x7f80u) {
+        others = true;
         const uint32_t x[4] = {v.x & k, v.y & k, v.z & k, v.w & k};
         m = 0;
 #pragma unroll
@@ -91,6 +92,12 @@ __device__ __forceinline__ float bf16x8_amax(const uint4 &v)
         }
     }
     return __uint_as_float(m << 16);
+}
+
+__device__ __forceinline__ float bf16x8_amax(const uint4 &v)
+{
+    bool others = false;
+    return bf16x8_amax(v, others);
 }
 
 // Exponent x with amax * 2^-x in [2^14, 2^15) (where the range of exp2i allows it).

@@ -216,14 +216,17 @@ __device__ __forceinline__ int need_exponent(float a)
 
 __device__ __forceinline__ float exp2_int(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
-// Two values under their scale as e4m3 bytes: nearest even, saturating; infinities
-// become NaN like NaN itself (x * 0 + x is NaN for an infinity and x otherwise).
+// Two values under their scale as e4m3 bytes: nearest even, saturating (infinities
+// too), NaN as NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(fmaf(hi, 0.f, hi)), "f"(fmaf(lo, 0.f, lo)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+
+// An infinity as NaN; anything else as it is.
+__device__ __forceinline__ float inf_to_nan(float x) { return fmaf(x, 0.f, x); }
 
 __device__ __forceinline__ uint32_t rescale_bytes(uint32_t w, uint32_t f16x2_factor)
 {
@@ -346,8 +349,11 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
                 rotate_unit(x0, x1, c, s, p.inter);
             }
         };
-        // 1. the rows' largest finite magnitudes
+        // 1. the rows' largest finite magnitudes. Infinities, which neither count nor saturate
+        // but become NaN, are rare: whether there are any is seen from the maxima, and only
+        // then is every value looked at for itself. (A maximum passes over NaN.)
         float rowmax = 0.f;
+        bool inf = false;
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
             const int row = q * RPP + rsub;
@@ -357,13 +363,19 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
                 float x0[8], x1[8];
                 values(q, on, x0, x1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = fabsf(x0[i]), b = fabsf(x1[i]);
-                    m = fmaxf(m, a < INFINITY ? a : 0.f);      // false for NaN
-                    m = fmaxf(m, b < INFINITY ? b : 0.f);
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
+                if (m == INFINITY) {
+                    m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float a = fabsf(x0[i]), b = fabsf(x1[i]);
+                        m = fmaxf(m, a < INFINITY ? a : 0.f);      // false for NaN
+                        m = fmaxf(m, b < INFINITY ? b : 0.f);
+                    }
+                    inf = true;
                 }
             } else {
-                m = fmaxf(bf16x8_amax(v0[q]), bf16x8_amax(v1[q]));
+                m = fmaxf(bf16x8_amax(v0[q], inf), bf16x8_amax(v1[q], inf));
             }
             m = on ? m : 0.f;
 #pragma unroll
@@ -373,6 +385,7 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             if (lane / RPP == q)
                 rowmax = got;
         }
+        inf = __any_sync(0xffffffffu, inf);
         // 2. each run's maximum (rows of a run are neighbours), its old and its new scale
         const uint32_t upto = leads & (0xffffffffu >> (31 - lane));
         const int start = upto ? 31 - __clz(upto) : 0;
@@ -444,6 +457,13 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
             values(q, on, x0, x1);
             if (!on)
                 continue;
+            if (inf) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x0[i] = inf_to_nan(x0[i]);
+                    x1[i] = inf_to_nan(x1[i]);
+                }
+            }
             uint32_t b0[2], b1[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
