@@ -6,6 +6,7 @@ package imports nothing from the product: the two share no code.
 
 Parts:
   attention.c  KV write (bit copy by slot) and paged causal attention, fp64, OpenMP
+  append.py    rotation and the 8-bit cache's blocks (numpy, 64 bits), on their own
   split.py     simple and balanced micro-batch split points (pure Python integers)
   planner.py   quadratic latency model, chunk-size solver and post-processing,
                online calibration (windowed two-variable refit)
