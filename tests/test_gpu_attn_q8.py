@@ -219,6 +219,56 @@ def test_captured_and_replayed_on_another_stream(cuda_lib, hist, qlen):
     assert cuda_lib.cpp_read_device_error(err) == 0
 
 
+def test_two_graphs_that_share_a_workspace(cuda_lib):
+    """Replayed in turn: neither the work lists nor the merge counters of one disturb the other."""
+    batches = [draw(spec([3000], [300], hq=8, hkv=2, seed=1350)), draw(spec([2000, 900, 5000], [260, 1, 1], seed=1351))]
+    want = [run(cuda_lib, *x)[0] for x in batches]
+    size = max(cuda_lib.cpp_attn_workspace_bytes(len(b.spec.qlen), b.num_tokens, 8, 2, 128, 8) for b, _ in batches)
+    ws = torch.full((size,), 0xAB, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    jobs = []
+    for b, caches in batches:
+        kc, ks, vc, vs = (to_dev(x) for x in caches)
+        out = torch.zeros(b.num_tokens, 8, 128, dtype=torch.bfloat16, device="cuda")
+        args = (to_dev_bf16(b.q), kc, vc, ks, vs, to_dev(b.query_lens), to_dev(b.seq_lens), to_dev(b.block_table), out,
+                ws, err)
+        torch.cuda.synchronize()
+        cuda_lib.cpp_chunked_prefill_attn_q8(*args, stream=side)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            cuda_lib.cpp_chunked_prefill_attn_q8(*args)
+        jobs.append((g, out, args))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        g, out, _ = jobs[i]
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.double().cpu().numpy(), want[i])
+    assert cuda_lib.cpp_read_device_error(err) == 0
+
+
+def test_calls_of_another_device_are_refused(cuda_lib, monkeypatch):
+    """Tensors and streams that are not the current device's (here: a current device that is not theirs)."""
+    from chunked_prefill_paged_slot_gb300 import _lib
+    b, caches = draw(spec([20], [3], hq=2, hkv=2, seed=1360))
+    kc, ks, vc, vs = (to_dev(x) for x in caches)
+    q = to_dev_bf16(b.q)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    monkeypatch.setattr(_lib.torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(cuda_lib.CpsaError, match="the current device is cuda:1"):
+        cuda_lib.cpp_chunked_prefill_attn_q8(q, kc, vc, ks, vs, to_dev(b.query_lens), to_dev(b.seq_lens),
+                                             to_dev(b.block_table), q.clone(), kc, err, stream=s)
+    with pytest.raises(cuda_lib.CpsaError, match="the current device is cuda:1"):
+        cuda_lib.cpp_rope_kv_cache_write_q8(None, q, q, None, None, to_dev(b.slot_mapping), kc, vc, ks, vs, None, err,
+                                            stream=s)
+    monkeypatch.undo()
+    with pytest.raises(cuda_lib.CpsaError, match="q is on cuda:0, the current device is cuda:1"):
+        _lib._ptr(q, torch.bfloat16, "q", 1)
+
+
 def test_two_streams_with_their_own_workspaces(cuda_lib):
     one, two = draw(spec([3000, 100], [200, 1], seed=1400)), draw(spec([100, 4000, 5000], [150, 1, 1], seed=1401))
     want = [run(cuda_lib, *x)[0] for x in (one, two)]
