@@ -47,8 +47,8 @@ constexpr int kMinRunTiles = 4;             // shortest run of KV tiles per CTA
 #endif
 constexpr int kUnitCostTiles = CPSA_UNIT_COST_TILES;   // a unit's fixed cost, in KV tiles (< kMinRunTiles)
 // Over the 8-bit cache a unit of 128 columns costs more to start (its Q passes through
-// registers). At 3 eight fresh prompts of 2600 tokens take 663 us and a fresh chunk of 512
-// 21 us, at 2 712 and 30 us (one prompt of 2000 tokens: 72 and 69 us); with 64 columns
+// registers). At 3 eight fresh prompts of 2600 tokens take 635 us and a fresh chunk of 512
+// 21 us, at 2 703 and 30 us (one prompt of 2000 tokens: 70 and 67 us); with 64 columns
 // ragged prompts take 90 us at 3, 88 at 2.
 __host__ __device__ constexpr int unit_cost_q8(int head_dim) { return head_dim == 128 ? 3 : kUnitCostTiles; }
 static_assert(unit_cost_q8(128) < kMinRunTiles, "a run must hold more than one unit's start");

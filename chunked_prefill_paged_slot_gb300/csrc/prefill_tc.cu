@@ -738,6 +738,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
             X = max(X, __reduce_max_sync(0xffffffffu, pg0 >= 0 ? vxl : -126));
             const uint32_t there = __ballot_sync(0xffffffffu, pg0 >= 0) & 0xffffu;
             const int64_t row = (((int64_t)pg0 * p.num_kv_heads + kvh) << lg_page) + ((kt * 128 + key_l) & pmask);
+#pragma unroll 1   // instruction fetch, again: eight fresh prompts of 2600 tokens 662 -> 635 us
             for (int kv = 0; kv < 2; ++kv, ++half) {
                 const int st = half % kQ8Stages;
                 if (half >= (uint32_t)kQ8Stages &&
