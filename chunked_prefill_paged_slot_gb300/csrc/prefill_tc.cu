@@ -1470,7 +1470,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const int limit_hist = p.fused ? hist - 1 : limit;
             const int n = w.kt1 - w.kt0;
             float m_use = -INFINITY, l = 0.f;
-            float q_sl2 = sl2;       // Q8: with the q row's exponent
+            float q_sl2 = sl2;       // Q8: with the q row's exponent and the lift
             int vx = 0;              // Q8: O stands for O * 2^(vx - kQ8Lift)
             bool ok = true;
             for (int t = 0; t < n; ++t) {
@@ -1483,10 +1483,11 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 float tsl2 = sl2, xs = 1.f;
                 if constexpr (Q8) {
                     const volatile Q8Tiles *qt = q8t;
+                    // (the lift with the q row's exponent: the K tile's may be the smallest there is)
                     if (t == 0)
-                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]);
+                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]) * exp2i(-kQ8Lift);
                     // never 0 or infinite: a masked score times it stays -inf, a zero one 0
-                    tsl2 = fminf(fmaxf(q_sl2 * exp2i(qt->kx[s_uses & 7] - kQ8Lift), 1.2e-38f), 3.0e38f);
+                    tsl2 = fminf(fmaxf(q_sl2 * exp2i(qt->kx[s_uses & 7]), 1.2e-38f), 3.0e38f);
                     const int x = qt->vx[s_uses & 7];
                     if (t > 0)
                         xs = exp2i(max(vx - x, -126));
