@@ -513,17 +513,19 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                         if (g == 0)
                             reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(m_run[nh][e], l_run[nh][e]);
                     } else {
+                        // 1 / l and the power one after the other: their product may be no normal number
                         const float l = l_run[nh][e];
-                        const float inv = of * (l > 0.f ? 1.f / l : 0.f);   // a NaN sum leaves o NaN
+                        const float inv = l > 0.f ? 1.f / l : 0.f;   // a NaN sum leaves o NaN
                         __nv_bfloat16 *dst =
                             reinterpret_cast<__nv_bfloat16 *>(p.out) + ((int64_t)w.t * p.num_q_heads + hq) * D + col0;
 #pragma unroll
-                        for (int j = 0; j < MT; j += 4)
-                            *reinterpret_cast<uint4 *>(dst + 2 * j) =
-                                make_uint4(pack_bf16x2(o[j][nh][e] * inv, o[j][nh][2 + e] * inv),
-                                           pack_bf16x2(o[j + 1][nh][e] * inv, o[j + 1][nh][2 + e] * inv),
-                                           pack_bf16x2(o[j + 2][nh][e] * inv, o[j + 2][nh][2 + e] * inv),
-                                           pack_bf16x2(o[j + 3][nh][e] * inv, o[j + 3][nh][2 + e] * inv));
+                        for (int j = 0; j < MT; j += 4) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                pk[x] = pack_bf16x2(o[j + x][nh][e] * inv * of, o[j + x][nh][2 + e] * inv * of);
+                            *reinterpret_cast<uint4 *>(dst + 2 * j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        }
                     }
                 }
         } else {

@@ -958,6 +958,22 @@ __device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
     return p.out_tma;
 }
 
+// This thread's row of O times f. Out of line: rarely called, and the softmax loop's code stays as it is.
+template <int D>
+__device__ __noinline__ void scale_o_row(uint32_t tO, float f)
+{
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tO + c * 32, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
+        tmem_st32(tO + c * 32, r);
+    }
+    tmem_wait_st();
+}
+
 // SELF: a batch of one prefill request, planned by the kernel itself (pieces in
 // shared memory); else the plan kernel's lists in the workspace.
 // Q8: over the 8-bit cache. The CTA is then 512 threads: warps 0..7 softmax, 8..11
@@ -1604,8 +1620,16 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const int64_t t_row = (int64_t)row0(w.r) + i;
             const int npieces = w.piece_np >> 16;
             float own_f = 1.f;
-            if constexpr (Q8)
-                own_f = exp2i(max(vx - kQ8Lift, -126));
+            if constexpr (Q8) {
+                // O stands for O * 2^(vx - kQ8Lift). Where this and 1 / l together could leave the
+                // normal numbers and lose digits (values below 2^-44), O takes a part of it first
+                int e = vx - kQ8Lift;
+                if (e < -60) {
+                    scale_o_row<D>(tO, exp2i(-56));
+                    e += 56;
+                }
+                own_f = exp2i(e);
+            }
             if (npieces > 1) {
                 // A piece of a split unit. Every warp (32 rows) decides on its own:
                 // at the end of its CTA's run, if every other piece has left its
