@@ -223,7 +223,11 @@ __device__ __forceinline__ int need_exponent(float a)
     return max(kQ8MinExp, min(kQ8MaxExp, e));
 }
 
-__device__ __forceinline__ float exp2_int(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+// 2^x, -127 <= x <= 127 (the smallest of them a subnormal number)
+__device__ __forceinline__ float exp2_int(int x)
+{
+    return __uint_as_float(x > -127 ? (uint32_t)(x + 127) << 23 : 0x400000u);
+}
 
 // Two values under their scale as e4m3 bytes: nearest even, saturating (infinities
 // too), NaN as NaN.
@@ -430,7 +434,8 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
         if (mine) {
             x = need_exponent(runmax);
             if (kept) {
-                const int was = min((int)was_byte - 127, kQ8MaxExp);
+                // (another writer's may be above kQ8MaxExp; 255, which stands for none, as 254)
+                const int was = min((int)was_byte - 127, 127);
                 grow = max(0, x - was);
                 x = max(x, was);
             }

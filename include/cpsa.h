@@ -150,7 +150,8 @@ int cpp_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t
  * values are rounded to nearest even under 2^x; magnitudes above 448 * 2^119
  * saturate, infinities and NaN become NaN and take no part in amax. So a block is
  * filled from its first place on, by any number of calls, and calls that rewrite
- * places in its middle only ever raise its exponent.
+ * places in its middle only ever raise its exponent (whoever wrote it: scale bytes
+ * 0 to 254; 255, the mark of no scale, counts as 254).
  * Tokens of one block that are not neighbours in the call, or not in ascending
  * order, leave that block with an unspecified mix of their values and scales
  * (other blocks are not affected). The same holds for duplicate slots.
