@@ -68,16 +68,16 @@ class AttentionStep:
         """KV write of the new tokens (rotated, or into 8 bits, when the step was built so), then attention, on one
         stream. positions: int64 [T], with rope; k_scale, v_scale: the 8-bit cache's; q_rot: where the rotated q goes
         (the step's own buffer)."""
+        if (self.rope is None) != (positions is None):
+            raise _lib.CpsaError("AttentionStep.run: positions go with a step built with rope, and only with it")
+        if self.q8 != (k_scale is not None) or self.q8 != (v_scale is not None):
+            raise _lib.CpsaError("AttentionStep.run: k_scale and v_scale go with a step of an 8-bit cache, and only with it")
         ws = self.workspaces[0] if workspace is None else workspace
         if self.fused_kv_write:
             _lib.cpp_chunked_prefill_attn_write_kv(q, k, v, slot_mapping, k_cache, v_cache, query_lens, seq_lens,
                                                    block_table, out, ws, self.dev_err, scale=scale,
                                                    max_kv_splits=self.max_kv_splits, stream=stream)
             return
-        if (self.rope is None) != (positions is None):
-            raise _lib.CpsaError("AttentionStep.run: positions go with a step built with rope, and only with it")
-        if self.q8 != (k_scale is not None) or self.q8 != (v_scale is not None):
-            raise _lib.CpsaError("AttentionStep.run: k_scale and v_scale go with a step of an 8-bit cache, and only with it")
         q_in = None
         if self.rope is not None:
             q_in = q
