@@ -119,6 +119,8 @@ def load():
     lib.cpp_selftest_exp2.argtypes = [_c_p, _c_p, _c_p, _c_i64, _c_p]
     lib.cpp_selftest_wait_timeout.restype = _c_int
     lib.cpp_selftest_wait_timeout.argtypes = [_c_i64, _c_p, _c_p, _c_p]
+    lib.cpp_selftest_warp_wait.restype = _c_int
+    lib.cpp_selftest_warp_wait.argtypes = [_c_i64, _c_p, _c_p]
     lib.cpp_status_string.restype = ctypes.c_char_p
     lib.cpp_status_string.argtypes = [_c_int]
     _lib = lib
@@ -594,4 +596,12 @@ def cpp_selftest_wait_timeout(limit_ns, dev_err, stream=None):
     _check(load().cpp_selftest_wait_timeout(int(limit_ns), _dev(dev_err, torch.int32, "dev_err"),
                                             _dev(out, torch.int32, "out3"), _stream_ptr(stream)),
            "cpp_selftest_wait_timeout")
+    return out
+
+
+def cpp_selftest_warp_wait(limit_ns, device="cuda", stream=None):
+    """Runs the self-test of the warp-wide waits; returns its int32 [68] device tensor (see cpsa.h)."""
+    out = torch.full((68,), -1, dtype=torch.int32, device=device)
+    _check(load().cpp_selftest_warp_wait(int(limit_ns), _dev(out, torch.int32, "out68"), _stream_ptr(stream)),
+           "cpp_selftest_warp_wait")
     return out

@@ -745,6 +745,16 @@ int cpp_selftest_wait_timeout(int64_t limit_ns, uint32_t *dev_err, int32_t *out3
                : CPSA_ERR_CUDA;
 }
 
+int cpp_selftest_warp_wait(int64_t limit_ns, int32_t *out68, void *stream)
+{
+    if (limit_ns < 1000 || limit_ns > 100000000)
+        return CPSA_ERR_BAD_SHAPE;
+    if (!out68)
+        return CPSA_ERR_NULL_ARG;
+    return launch_warp_wait_selftest((uint64_t)limit_ns, out68, (cudaStream_t)stream) == cudaSuccess ? CPSA_OK
+                                                                                                     : CPSA_ERR_CUDA;
+}
+
 int cpp_read_device_error(uint32_t *dev_err, uint32_t *host_flags, int clear, void *stream)
 {
     if (!dev_err || !host_flags)

@@ -119,6 +119,37 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// mbar_wait of a whole warp on one barrier: one verdict for all its lanes, so that a
+// lane that gives up and one that sees the phase complete at the last moment do not
+// part before the warp's next collective (a shuffle, an mma.sync, a named barrier).
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               uint64_t limit_ns = kWaitLimitNs)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+}
+
+// Whether a role of the CTA has given up, the same for all lanes.
+__device__ __forceinline__ bool warp_aborted(volatile int *abort) { return __any_sync(0xffffffffu, *abort != 0); }
+
+// The end of a role that fills a ring of `depth` barriers by copies (its use i on
+// bars[i % depth], `uses` of them announced in full): leave only once those copies
+// have landed, for the CTA's shared memory is no longer its own when it ends.
+// A barrier's last phase completes once, and nothing announces another. Returns
+// false where limit_ns ran out first.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bars, uint32_t uses, uint32_t depth,
+                                           uint64_t limit_ns = kWaitLimitNs)
+{
+    const uint64_t t0 = global_timer_ns();
+    bool landed = true;
+    for (uint32_t i = uses > depth ? uses - depth : 0; i < uses; ++i)
+        while (!mbar_try_wait(&bars[i % depth], (i / depth) & 1))
+            if (global_timer_ns() - t0 > limit_ns) {
+                landed = false;
+                break;
+            }
+    return landed;
+}
+
 // mbar_wait for warps off the critical path: sleeps between polls so that the
 // waiting warp leaves the issue slots of its SM sub-partition to the warps that
 // share it. Same limits and result as mbar_wait.

@@ -170,7 +170,7 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
         DecodeItem w_next{};
         if (blockIdx.x < n_items)
             w_next = p.ditems[blockIdx.x];
-        for (int it = blockIdx.x; it < n_items && !stop && !*abort; it += gridDim.x) {
+        for (int it = blockIdx.x; it < n_items && !stop && !warp_aborted(abort); it += gridDim.x) {
             const DecodeItem w = w_next;
             if (it + (int)gridDim.x < n_items)
                 w_next = p.ditems[it + gridDim.x];
@@ -225,7 +225,8 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                 uint32_t s2lo, s2hi;
                 scales_of(j + 2, s2lo, s2hi);
                 const int stage = g % C::kStages;
-                if (g >= (uint32_t)C::kStages && !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort)) {
+                if (g >= (uint32_t)C::kStages &&
+                    !mbar_wait_warp(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort)) {
                     stop = true;
                     break;
                 }
@@ -258,6 +259,7 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                 __syncwarp();
             }
         }
+        mbar_drain(bars->full, g, C::kStages);
         return;
     }
 
@@ -328,7 +330,7 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
         for (int j = 0; j < nst; ++j) {
             const uint32_t gg = gs + j;
             const int stage = gg % C::kStages;
-            if (!mbar_wait(&bars->full[stage], (gg / C::kStages) & 1, abort))
+            if (!mbar_wait_warp(&bars->full[stage], (gg / C::kStages) & 1, abort))
                 break;
             const int nv = w.key1 - w.key0 - j * C::kKeys - kb0;   // this warp's valid keys (may be <= 0, or > 32)
             if (nv > 0) {

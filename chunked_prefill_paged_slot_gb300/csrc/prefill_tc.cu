@@ -693,7 +693,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
     uint8_t *stages = smem + C::kQ8StageOff + key_l * D;
     uint32_t half = 0, tile = 0;   // half-tiles and tiles issued
     bool ok = true;
-    for (int it = it_begin; it < it_end && ok && !__any_sync(0xffffffffu, *abort != 0); ++it) {
+    for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
         const PrefillItem w = items[it];
         const int kvh = w.kvh_hp & 0xFFFF;
         const int s_len = p.seq_lens[w.r];
@@ -742,7 +742,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
             for (int kv = 0; kv < 2; ++kv, ++half) {
                 const int st = half % kQ8Stages;
                 if (half >= (uint32_t)kQ8Stages &&
-                    !__all_sync(0xffffffffu, mbar_wait(&q8t->empty[st], ((half / kQ8Stages) - 1) & 1, abort))) {
+                    !mbar_wait_warp(&q8t->empty[st], ((half / kQ8Stages) - 1) & 1, abort)) {
                     ok = false;
                     break;
                 }
@@ -783,15 +783,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
             vs1 = vs2;
         }
     }
-    if (!ok || __any_sync(0xffffffffu, *abort != 0)) {
-        // given up on a wait: let the copies in flight land before the CTA can end (a
-        // half-tile's phase completes once, and only its converters' reads let it go on)
-        const uint64_t t0 = global_timer_ns();
-        for (uint32_t h = half > (uint32_t)kQ8Stages ? half - kQ8Stages : 0; h < half; ++h)
-            while (!mbar_try_wait(&q8t->full[h % kQ8Stages], (h / kQ8Stages) & 1) &&
-                   global_timer_ns() - t0 < 100000000ull) {
-            }
-    }
+    mbar_drain(q8t->full, half, kQ8Stages);
 }
 
 template <int D, int NQ>
@@ -822,10 +814,10 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
     }
     uint32_t q_uses = 0, half = 0, tile = 0;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+        return mbar_wait_warp(bar, parity, abort);
     };
     bool ok = true;
-    for (int it = it_begin; it < it_end && ok && !__any_sync(0xffffffffu, *abort != 0); ++it) {
+    for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
         const PrefillItem w = items[it];
         const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
         const int s_len = p.seq_lens[w.r];

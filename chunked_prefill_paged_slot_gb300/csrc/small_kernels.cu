@@ -334,6 +334,61 @@ __global__ void wait_selftest_kernel(uint64_t limit_ns, uint32_t *dev_err, int32
         set_dev_error(dev_err, CPSA_DEV_WAIT_TIMEOUT);
 }
 
+// Self-test of the warp-wide waits (mbar_wait_warp) and of the drain at a role's end
+// (mbar_drain). Warp 0 waits on a barrier with a limit of limit_ns for its lane 0, which
+// runs out, and the standard one for its other lanes, whose phase warp 1 completes as soon
+// as lane 0 has given up: first by mbar_wait, whose verdicts then differ from lane to
+// lane, then by mbar_wait_warp. Then it drains a ring of two barriers with three uses, the
+// last of which warp 1 completes limit_ns late, and one barrier that nothing completes.
+// out[0..31], out[32..63]: the lanes' verdicts of either wait; out[64], out[65]: whether the
+// ring's uses landed, and in how many microseconds; out[66], out[67]: the same of the last.
+__global__ void warp_wait_selftest_kernel(uint64_t limit_ns, int32_t *out)
+{
+    __shared__ __align__(8) uint64_t bar[2], ring[2], never;
+    __shared__ int gave_up[4];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[i], 1);
+            mbar_init(&ring[i], 1);
+        }
+        mbar_init(&never, 1);
+        for (int i = 0; i < 4; ++i) gave_up[i] = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        const uint64_t limit = lane == 0 ? limit_ns : kWaitLimitNs;
+        const int who = lane == 0 ? 0 : 1;
+        out[lane] = mbar_wait(&bar[0], 0, &gave_up[who], limit) ? 1 : 0;
+        __syncwarp();
+        out[32 + lane] = mbar_wait_warp(&bar[1], 0, &gave_up[2 + who], limit) ? 1 : 0;
+        __syncwarp();
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t t0 = global_timer_ns();
+            const bool landed = i == 0 ? mbar_drain(ring, 3, 2) : mbar_drain(&never, 1, 1, limit_ns);
+            const uint64_t us = (global_timer_ns() - t0) / 1000u;
+            if (lane == 0) {
+                out[64 + 2 * i] = landed ? 1 : 0;
+                out[65 + 2 * i] = (int32_t)(us < 0x7fffffffu ? us : 0x7fffffffu);
+            }
+            __syncwarp();
+        }
+    } else if (lane == 0) {
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t t0 = global_timer_ns();
+            while (*reinterpret_cast<volatile int *>(&gave_up[2 * i]) == 0 && global_timer_ns() - t0 < kWaitLimitNs / 2)
+                __nanosleep(200);
+            mbar_arrive(&bar[i]);
+        }
+        mbar_arrive(&ring[0]);
+        mbar_arrive(&ring[1]);
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < limit_ns) __nanosleep(200);
+        mbar_arrive(&ring[0]);
+    }
+}
+
 // The same split for batches of at most kSplitSmallMax requests, by one warp
 // with no shared memory: the running prefix is carried across 32-request
 // chunks, and the winning boundary carries its own prefix, so n1 needs no second
@@ -419,6 +474,12 @@ cudaError_t launch_exp2_selftest(const float *x, float *poly, float *hw, int64_t
 cudaError_t launch_wait_selftest(uint64_t limit_ns, uint32_t *dev_err, int32_t *out, cudaStream_t s)
 {
     wait_selftest_kernel<<<1, 64, 0, s>>>(limit_ns, dev_err, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_warp_wait_selftest(uint64_t limit_ns, int32_t *out, cudaStream_t s)
+{
+    warp_wait_selftest_kernel<<<1, 64, 0, s>>>(limit_ns, out);
     return cudaGetLastError();
 }
 

@@ -529,6 +529,18 @@ int cpp_selftest_exp2(const float *x, float *out_poly, float *out_hw, int64_t n,
  */
 int cpp_selftest_wait_timeout(int64_t limit_ns, uint32_t *dev_err, int32_t *out3, void *stream);
 
+/*
+ * Self-test of the same waits taken by a whole warp, and of the end of a role that
+ * issues copies. One CTA, limit_ns as above, out68 a device int32[68]. Lane 0 of a
+ * warp gives up on a barrier after limit_ns, its other lanes see the phase complete
+ * right after: out68[0..31] the lanes' verdicts of the plain wait (lane 0: 0, the
+ * others: 1), out68[32..63] those of the warp-wide wait that the kernels use (all 0).
+ * Then the drain of a ring whose last fill lands limit_ns late (out68[64]: 1, out68[65]
+ * microseconds) and of a barrier whose fill never lands (out68[66]: 0 after limit_ns,
+ * out68[67] microseconds). No copy is in flight; the kernel always ends. Stream-ordered.
+ */
+int cpp_selftest_warp_wait(int64_t limit_ns, int32_t *out68, void *stream);
+
 /* Human-readable name of a status code. */
 const char *cpp_status_string(int status);
 
