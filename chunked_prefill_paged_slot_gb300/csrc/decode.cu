@@ -143,8 +143,11 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
         const int lg = 31 - __clz(PB);
         const uint32_t box_bytes = (uint32_t)PB * C::kRowBytes;
         uint32_t g = 0, patch_uses = 0;
-        bool stop = false;
-        for (int it = blockIdx.x; it < n_items && !stop && !*abort; it += gridDim.x) {
+        // A lane that has given up a wait, at stage `last`, issues no more copies, but walks on with
+        // the warp to the end: what the lanes do together stays together, without a vote a stage
+        // (128 rows of 2600 to 5200 keys, 2 kv heads: 154 us with it, 149 without)
+        uint32_t last = 0xffffffffu;
+        for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
             const DecodeItem w = p.ditems[it];
             const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
             // the row's own key, when this item's range ends with it and the KV write is fused
@@ -165,11 +168,9 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                 for (int k = 0; k + 1 < kLookahead; ++k) pg[k] = pg[k + 1];
                 pg[kLookahead - 1] = lookup(c0 + kLookahead * kKC);
                 const int stage = g % C::kStages;
-                if (g >= (uint32_t)C::kStages &&
-                    !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort)) {
-                    stop = true;
-                    break;
-                }
+                if (g >= (uint32_t)C::kStages && g < last &&
+                    !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort))
+                    last = g;
                 const int off = (c0 + lane * PB) % p.page_size;
                 bool valid = false;
                 if (lane < NB && c0 + lane * PB < w.key1) {
@@ -183,12 +184,12 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                 uint8_t *vdst = kdst + C::kTileBytes;
                 const bool patch = knew >= c0 && knew < c0 + kKC;
                 uint64_t *bar = patch ? &bars->patch : &bars->full[stage];
-                if (lane == 0)
+                if (lane == 0 && g < last)
                     mbar_arrive_expect_tx(bar, bytes);
                 for (int j = 0; j < NB; ++j) {
                     const int pj = __shfl_sync(0xffffffffu, page, j);
                     const int oj = __shfl_sync(0xffffffffu, off, j);
-                    if (lane == 0 && ((vmask >> j) & 1u)) {
+                    if (lane == 0 && g < last && ((vmask >> j) & 1u)) {
                         // rows [oj, oj + PB) of page-head block (pj, kvh), both halves in one box
                         const int z = pj * p.num_kv_heads + w.kvh;
                         if (C::kHalves == 2) {
@@ -201,11 +202,8 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                     }
                 }
                 if (patch) {
-                    if (!mbar_wait(&bars->patch, patch_uses & 1u, abort)) {
-                        stop = true;
-                        break;
-                    }
-                    ++patch_uses;
+                    if (g < last && !mbar_wait(&bars->patch, patch_uses++ & 1u, abort))
+                        last = g;
                     // lanes 0..D/8-1: 16-byte chunks of the K row; lanes 16..16+D/8-1: of the V row
                     const int which = lane >> 4, ch = lane & 15;
                     if (ch < D / 8) {
@@ -229,10 +227,14 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                     }
                     fence_proxy_async_smem();   // the patch before later copies into this stage
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0 && g < last)
                         mbar_arrive(&bars->full[stage]);
                 }
             }
+        }
+        if (lane == 0) {
+            mbar_drain(bars->full, min(g, last), C::kStages);
+            mbar_drain(&bars->patch, patch_uses, 1);
         }
         return;   // the producer takes no part in the consumers' named barriers
     }
@@ -248,10 +250,13 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
     const int lg = 31 - __clz(p.page_size < kKC ? p.page_size : kKC);   // log2 rows per block
     uint32_t g = 0;
     // every consumer warp walks every item (no early exit on abort: the named
-    // barriers below need all four; a failed wait returns at once instead)
+    // barriers below need all four). A lane whose wait gives up goes on with the others,
+    // over whatever the stage holds: one verdict for the warp would cost a vote a stage
+    // (a row of 777 keys 39.2 us, 35.9 without), and the call is flagged. Later items are
+    // passed over.
     for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
         const DecodeItem w = p.ditems[it];
-        const int nch = (w.key1 - w.key0 + kKC - 1) / kKC;
+        const int nch = warp_aborted(abort) ? 0 : (w.key1 - w.key0 + kKC - 1) / kKC;
         // q fragments (rows >= G are zero)
         uint32_t qa[D / 16][4];
         {
@@ -283,8 +288,7 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
             if ((int)(gg % C::kGroups) != group)
                 continue;
             const int stage = gg % C::kStages;
-            if (!mbar_wait(&bars->full[stage], (gg / C::kStages) & 1, abort))
-                break;
+            mbar_wait(&bars->full[stage], (gg / C::kStages) & 1, abort);
             const int c0 = w.key0 + j * kKC;
             const int kb0 = (warp & 3) * 16;               // this warp's keys in the stage
             const int nv = min(16, w.key1 - c0 - kb0);     // valid keys of this warp (may be <= 0)
@@ -522,13 +526,13 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         }
         const uint32_t box_bytes = (uint32_t)HG * RB * D * 2;
         uint32_t g = 0, patch_uses = 0;
-        bool stop = false;
+        uint32_t last = 0xffffffffu;   // see decode_attn_kernel
         // the next item's descriptor is read one item ahead (its page lookups
         // depend on it, and they start the item's stream)
         DecodeItem w_next{};
         if (blockIdx.x < n_items)
             w_next = p.ditems[blockIdx.x];
-        for (int it = blockIdx.x; it < n_items && !stop && !*abort; it += gridDim.x) {
+        for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
             const DecodeItem w = w_next;
             if (it + (int)gridDim.x < n_items)
                 w_next = p.ditems[it + gridDim.x];
@@ -555,16 +559,14 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                 const int pg0 = __shfl_sync(0xffffffffu, cur0, j & 31);
                 const int pg1 = __shfl_sync(0xffffffffu, cur1, j & 31);
                 const int stage = g % C::kStages;
-                if (g >= (uint32_t)C::kStages &&
-                    !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort)) {
-                    stop = true;
-                    break;
-                }
+                if (g >= (uint32_t)C::kStages && g < last &&
+                    !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort))
+                    last = g;
                 uint8_t *kdst = smem + stage * C::kStageBytes;
                 uint8_t *vdst = kdst + C::kTileBytes;
                 const bool patch = knew >= c0 && knew < c0 + C::kKeys;
                 uint64_t *bar = patch ? &bars->patch : &bars->full[stage];
-                if (lane == 0) {
+                if (lane == 0 && g < last) {
                     // one lane announces the stage's bytes, then issues its copies
                     bool v0 = false, v1 = false;
                     if (c0 < w.key1) {
@@ -596,11 +598,8 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                 }
                 __syncwarp();
                 if (patch) {
-                    if (!mbar_wait(&bars->patch, patch_uses & 1u, abort)) {
-                        stop = true;
-                        break;
-                    }
-                    ++patch_uses;
+                    if (g < last && !mbar_wait(&bars->patch, patch_uses++ & 1u, abort))
+                        last = g;
                     // the new token's K and V rows of the HG heads, 16-byte chunks over the
                     // lanes: into the stage (over the cache's old bytes) and to the slot
                     const int rr = knew - c0;
@@ -624,10 +623,14 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                         set_dev_error(p.dev_err, CPSA_DEV_SLOT_OUT_OF_RANGE);
                     fence_proxy_async_smem();   // the patch before later copies into this stage
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0 && g < last)
                         mbar_arrive(&bars->full[stage]);
                 }
             }
+        }
+        if (lane == 0) {
+            mbar_drain(bars->full, min(g, last), C::kStages);
+            mbar_drain(&bars->patch, patch_uses, 1);
         }
         return;
     }
@@ -643,7 +646,8 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     uint32_t g = 0;
     for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
         const DecodeItem w = p.ditems[it];
-        const int nch = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
+        // (waits and aborts as in decode_attn_kernel)
+        const int nch = warp_aborted(abort) ? 0 : (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
         const int kvh = w.kvh * HG + h;
         uint32_t qa[D / 16][4];
         {
@@ -673,8 +677,7 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         for (int j = 0; j < nch; ++j) {
             const uint32_t gg = g + j;
             const int stage = gg % C::kStages;
-            if (!mbar_wait(&bars->full[stage], (gg / C::kStages) & 1, abort))
-                break;
+            mbar_wait(&bars->full[stage], (gg / C::kStages) & 1, abort);
             const int c0 = w.key0 + j * C::kKeys;
             const int nv = min(C::kKeys, w.key1 - c0);   // valid keys of this stage (>= 1)
             uint8_t *kst = smem + stage * C::kStageBytes;

@@ -1083,7 +1083,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         const uint32_t box_bytes = (uint32_t)PB * 128u;
         const bool v_pages = D == 128 && PB < 128;   // V tiles of the cache in page-major boxes
         uint32_t q_uses = 0, slot_it = 0, tail_uses = 0;
-        for (int it = it_begin; it < it_end && !*abort; ++it) {
+        for (int it = it_begin; it < it_end && !warp_aborted(abort); ++it) {
             const PrefillItem w = items[it];
             const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
             const int h0 = kvh * p.group + hp * NQ;
@@ -1094,7 +1094,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             // (fused KV write) from the new rows
             const int nh = p.fused ? (hist + 127) / 128 : 0x7fffffff;
             const int hist_end = p.fused ? hist : s_len;
-            if (q_uses > 0 && !mbar_wait(&bars->q_empty, (q_uses - 1) & 1, abort))
+            if (q_uses > 0 && !mbar_wait_warp(&bars->q_empty, (q_uses - 1) & 1, abort))
                 break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars->q_full, NQ * C::kTileBytes);
@@ -1143,7 +1143,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 for (int kv = 0; kv < 2 && !stop; ++kv) {
                     const int slot = slot_it % C::kSlots;
                     if (slot_it >= (uint32_t)C::kSlots &&
-                        !mbar_wait(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1, abort)) {
+                        !mbar_wait_warp(&bars->slot_empty[slot], ((slot_it / C::kSlots) - 1) & 1, abort)) {
                         stop = true;
                         break;
                     }
@@ -1181,11 +1181,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     if (fix) {
                         // value rows >= key_end must be zero: P is zero there, but the
                         // bytes may be NaN and 0 * NaN would poison the row sums.
-                        if (!mbar_wait(&bars->tail, tail_uses & 1, abort)) {
+                        if (!mbar_wait_warp(&bars->tail, tail_uses++ & 1, abort)) {
                             stop = true;
                             break;
                         }
-                        ++tail_uses;
                         const int first = key_end - key0;   // 1 .. 127
                         const int nchunks = (128 - first) * 8;   // 16-byte chunks per half
                         if (v_pages && !from_new) {
@@ -1215,6 +1214,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             if (stop)
                 break;
         }
+        mbar_drain(&bars->q_full, q_uses, 1);
+        mbar_drain(bars->slot_full, slot_it, C::kSlots);
+        mbar_drain(&bars->tail, tail_uses, 1);
     } else if (warp == C::kWriteWarp) {
         // ------------------------------------------------------------ cache writer
         // Independent of the attention pipeline: it reads the new rows itself,
@@ -1223,7 +1225,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             uint8_t *stage = smem + C::kStageOff;
             uint32_t stage_uses = 0;
             bool ok = true;
-            for (int it = it_begin; it < it_end && ok && !*abort; ++it) {
+            for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
                 const PrefillItem w = items[it];
                 const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
                 const int q_len = p.query_lens[w.r];
@@ -1336,10 +1338,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const uint32_t slot_addr = smem_u32(smem + C::kSlotOff);
             uint32_t q_uses = 0, slot_it = 0, p_uses[2] = {0, 0};
             auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-                const bool ok = mbar_wait(bar, parity, abort);
-                return __all_sync(0xffffffffu, ok);
+                return mbar_wait_warp(bar, parity, abort);
             };
-            auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
+            auto aborted = [&]() -> bool { return warp_aborted(abort); };
             auto commit = [&](uint64_t *bar) {
                 if (elect_one_sync())
                     umma_commit(bar);
@@ -1463,7 +1464,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         const uint32_t tO = tmem + lane_base + C::o_col(wg);
         const float sl2 = p.scale_log2;
         uint32_t s_uses = 0, o_base = 0;   // s_uses: also the ordinal of the next tile
-        for (int it = it_begin; it < it_end && !*abort; ++it) {
+        for (int it = it_begin; it < it_end && !warp_aborted(abort); ++it) {
             const PrefillItem w = items[it];
             const int kvh = w.kvh_hp & 0xFFFF, hp = w.kvh_hp >> 16;
             const int h = kvh * p.group + hp * NQ + wg;
@@ -1486,7 +1487,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 const bool from_new = kt >= nh;
                 const int key0 = from_new ? hist + (kt - nh) * 128 : kt * 128;
                 const int lim = from_new ? limit : limit_hist;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[wg], s_uses & 1, abort))))
+                if (!(ok = mbar_wait_warp(&bars->s_full[wg], s_uses & 1, abort)))
                     break;
                 float tsl2 = sl2, xs = 1.f;
                 if constexpr (Q8) {
@@ -1577,7 +1578,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 tmem_wait_st();
                 if (__any_sync(0xffffffffu, need) && t > 0) {
                     // O holds the sum through tile t-1: wait for that P.V, then rescale
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_done[wg], (o_base + t - 1) & 1, abort))))
+                    if (!(ok = mbar_wait_warp(&bars->o_done[wg], (o_base + t - 1) & 1, abort)))
                         break;
                     tc_fence_after_sync();
 #pragma unroll
@@ -1604,7 +1605,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             }
             if (!ok)
                 break;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_done[wg], (o_base + n - 1) & 1, abort)))
+            if (!mbar_wait_warp(&bars->o_done[wg], (o_base + n - 1) & 1, abort))
                 break;
             o_base += n;
             tc_fence_after_sync();
@@ -1687,11 +1688,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         // other head's last P.V is done: the merge stages through them
                         bool staged = false;
                         if (D == 128 && it + 1 == it_end)
-                            staged = NQ == 1 || __all_sync(0xffffffffu, mbar_wait(&bars->o_done[NQ - 1 - wg],
-                                                                                  (o_base - 1) & 1, abort));
+                            staged = NQ == 1 || mbar_wait_warp(&bars->o_done[NQ - 1 - wg], (o_base - 1) & 1, abort);
                         // the merged rows through the writer's buffer once the writer is done with it
                         const bool ostaged = !Q8 && staged && rows_by_tma<Q8>(p) &&
-                                             (!p.fused || __all_sync(0xffffffffu, mbar_wait(&bars->writer_done, 0, abort)));
+                                             (!p.fused || mbar_wait_warp(&bars->writer_done, 0, abort));
                         merge_split_row<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
                                                out_off,
                                                staged ? reinterpret_cast<uint4 *>(smem + (wg * 4 + sub) * kMergeStageBytes)
