@@ -1318,140 +1318,6 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         } else if (lane == 0) {
             mbar_arrive(&bars->writer_done);
         }
-    } else if (warp == C::kMmaWarp || (Q8 && warp > C::kMmaWarp)) {
-        // Q8: the issuer, the e4m3 loader and two idle warps give up registers as one group
-        if constexpr (Q8)
-            regs_keep_96();
-        if (Q8 && warp != C::kMmaWarp) {
-            if constexpr (Q8) {
-                if (warp == C::kQ8LoadWarp)
-                    q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
-            }
-        } else {
-            // ------------------------------------------------------------ MMA issuer
-            // The whole warp walks the loop; every MMA and commit is issued by one
-            // lane from an elect.sync branch. Waits are polled by all lanes and their
-            // verdicts combined, so the warp stays converged.
-            constexpr uint32_t idesc_qk = Q8 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
-            constexpr uint32_t idesc_pv = Q8 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
-            const uint32_t q_addr = smem_u32(smem + C::kQOff);
-            const uint32_t slot_addr = smem_u32(smem + C::kSlotOff);
-            uint32_t q_uses = 0, slot_it = 0, p_uses[2] = {0, 0};
-            auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-                return mbar_wait_warp(bar, parity, abort);
-            };
-            auto aborted = [&]() -> bool { return warp_aborted(abort); };
-            auto commit = [&](uint64_t *bar) {
-                if (elect_one_sync())
-                    umma_commit(bar);
-            };
-            auto issue_qk = [&](int n, int slot) {
-    #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t koff = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
-                    const uint64_t a = smem_desc_sw128(q_addr + n * C::kTileBytes + koff, 0, 1024);
-                    const uint64_t b = smem_desc_sw128(slot_addr + slot * C::kTileBytes + koff, 0, 1024);
-                    if (elect_one_sync())
-                        umma_ss(tmem + C::s_col(n), a, b, idesc_qk, kk > 0);
-                }
-            };
-            // V below page 128 (cache tiles) lands page-major, [page][half][P rows][128 B]:
-            // keys 16 kk .. 16 kk + 15 start at page 16 kk / P, row 16 kk % P; the
-            // column halves are P * 128 bytes apart, 8-key groups 1024 bytes (two pages
-            // at page 8). Otherwise [half][128 rows][128 B].
-            const int pg = p.page_size < 128 ? p.page_size : 128;
-            const int lg_pg = __ffs(pg) - 1;
-            const bool v_pages = !Q8 && D == 128 && pg < 128;
-            auto issue_pv = [&](int n, int slot, bool acc, bool pm) {
-    #pragma unroll
-                for (int kk = 0; kk < 128 / 16; ++kk) {
-                    const int r0 = kk * 16;
-                    const uint32_t off = pm ? (uint32_t)(((r0 >> lg_pg) << (lg_pg + 8)) + (r0 & (pg - 1)) * 128)
-                                            : (uint32_t)(r0 * 128);
-                    const uint64_t b = smem_desc_sw128(slot_addr + slot * C::kTileBytes + off,
-                                                       pm ? (uint32_t)pg * 128u : (uint32_t)C::kHalfBytes,
-                                                       pm && pg < 16 ? (uint32_t)pg * 256u : 1024u);
-                    if (elect_one_sync())
-                        umma_ts(tmem + C::o_col(n), tmem + C::s_col(n) + kk * 8, b, idesc_pv, (acc || kk > 0));
-                }
-            };
-            auto wait_slot = [&](int &slot) -> bool {
-                slot = slot_it % C::kSlots;
-                const bool ok = wait(&bars->slot_full[slot], (slot_it / C::kSlots) & 1);
-                ++slot_it;
-                tc_fence_after_sync();
-                return ok;
-            };
-            for (int it = it_begin; it < it_end && !aborted(); ++it) {
-                const PrefillItem w = items[it];
-                const int n = w.kt1 - w.kt0;
-                // tiles from nh on hold the chunk's own keys, loaded from k/v (fused KV write)
-                const int nh = v_pages && p.fused ? (p.seq_lens[w.r] - p.query_lens[w.r] + 127) / 128 : 0x7fffffff;
-                if (!wait(&bars->q_full, q_uses & 1))
-                    break;
-                ++q_uses;
-                tc_fence_after_sync();
-                int sK, sV;
-                if (!wait_slot(sK))
-                    break;
-                for (int qn = 0; qn < NQ; ++qn) {
-                    issue_qk(qn, sK);
-                    commit(&bars->s_full[qn]);
-                }
-                commit(&bars->slot_empty[sK]);
-                if (n == 1)
-                    commit(&bars->q_empty);
-                bool ok = true;
-                for (int t = 0; t < n && ok; ++t) {
-                    if (!(ok = wait_slot(sV)))
-                        break;
-                    if (!(ok = wait(&bars->p_full[0], p_uses[0] & 1)))
-                        break;
-                    ++p_uses[0];
-                    tc_fence_after_sync();
-                    const bool pm = v_pages && w.kt0 + t < nh;
-                    issue_pv(0, sV, t > 0, pm);
-                    commit(&bars->o_done[0]);
-                    const bool more = t + 1 < n;
-                    if (more) {
-                        if (!(ok = wait_slot(sK)))
-                            break;
-                        issue_qk(0, sK);
-                        commit(&bars->s_full[0]);
-                    }
-                    if (NQ == 2) {
-                        if (!(ok = wait(&bars->p_full[1], p_uses[1] & 1)))
-                            break;
-                        ++p_uses[1];
-                        tc_fence_after_sync();
-                        issue_pv(1, sV, t > 0, pm);
-                        commit(&bars->o_done[1]);
-                    }
-                    commit(&bars->slot_empty[sV]);
-                    if (more) {
-                        if (NQ == 2) {
-                            issue_qk(1, sK);
-                            commit(&bars->s_full[1]);
-                        }
-                        commit(&bars->slot_empty[sK]);
-                        if (t + 2 == n)
-                            commit(&bars->q_empty);
-                    }
-                }
-                if (!ok)
-                    break;
-            }
-            if (aborted()) {
-                // let every MMA issued so far finish before TMEM is released
-                commit(&bars->drain);
-                if (lane == 0) {
-                    uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(&bars->drain, 0) && global_timer_ns() - t0 < 100000000ull) {
-                    }
-                }
-            }
-            __syncwarp();
-        }
     } else if (warp / 4 < NQ) {
         // ------------------------------------------------------------ softmax
         if constexpr (Q8)
@@ -1795,6 +1661,144 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     }
                 }
             }
+        }
+    } else if (warp == C::kMmaWarp || (Q8 && warp > C::kMmaWarp)) {
+        // Q8: the issuer, the e4m3 loader and two idle warps give up registers as one group.
+        // Where this stands among the roles, and the loader ahead of the issuer, only moves code,
+        // but instruction fetch is what runs short: with this group before the softmax, 512 tokens
+        // at history 32256 (32/8 heads) take 216 us instead of 210, eight fresh prompts of 2600
+        // tokens 692 instead of 630.
+        if constexpr (Q8)
+            regs_keep_96();
+        if (Q8 && warp != C::kMmaWarp) {
+            if constexpr (Q8) {
+                if (warp == C::kQ8LoadWarp)
+                    q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+            }
+        } else {
+            // ------------------------------------------------------------ MMA issuer
+            // The whole warp walks the loop; every MMA and commit is issued by one
+            // lane from an elect.sync branch. Waits are polled by all lanes and their
+            // verdicts combined, so the warp stays converged.
+            constexpr uint32_t idesc_qk = Q8 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false);
+            constexpr uint32_t idesc_pv = Q8 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, true);
+            const uint32_t q_addr = smem_u32(smem + C::kQOff);
+            const uint32_t slot_addr = smem_u32(smem + C::kSlotOff);
+            uint32_t q_uses = 0, slot_it = 0, p_uses[2] = {0, 0};
+            auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+                return mbar_wait_warp(bar, parity, abort);
+            };
+            auto aborted = [&]() -> bool { return warp_aborted(abort); };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one_sync())
+                    umma_commit(bar);
+            };
+            auto issue_qk = [&](int n, int slot) {
+    #pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t koff = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
+                    const uint64_t a = smem_desc_sw128(q_addr + n * C::kTileBytes + koff, 0, 1024);
+                    const uint64_t b = smem_desc_sw128(slot_addr + slot * C::kTileBytes + koff, 0, 1024);
+                    if (elect_one_sync())
+                        umma_ss(tmem + C::s_col(n), a, b, idesc_qk, kk > 0);
+                }
+            };
+            // V below page 128 (cache tiles) lands page-major, [page][half][P rows][128 B]:
+            // keys 16 kk .. 16 kk + 15 start at page 16 kk / P, row 16 kk % P; the
+            // column halves are P * 128 bytes apart, 8-key groups 1024 bytes (two pages
+            // at page 8). Otherwise [half][128 rows][128 B].
+            const int pg = p.page_size < 128 ? p.page_size : 128;
+            const int lg_pg = __ffs(pg) - 1;
+            const bool v_pages = !Q8 && D == 128 && pg < 128;
+            auto issue_pv = [&](int n, int slot, bool acc, bool pm) {
+    #pragma unroll
+                for (int kk = 0; kk < 128 / 16; ++kk) {
+                    const int r0 = kk * 16;
+                    const uint32_t off = pm ? (uint32_t)(((r0 >> lg_pg) << (lg_pg + 8)) + (r0 & (pg - 1)) * 128)
+                                            : (uint32_t)(r0 * 128);
+                    const uint64_t b = smem_desc_sw128(slot_addr + slot * C::kTileBytes + off,
+                                                       pm ? (uint32_t)pg * 128u : (uint32_t)C::kHalfBytes,
+                                                       pm && pg < 16 ? (uint32_t)pg * 256u : 1024u);
+                    if (elect_one_sync())
+                        umma_ts(tmem + C::o_col(n), tmem + C::s_col(n) + kk * 8, b, idesc_pv, (acc || kk > 0));
+                }
+            };
+            auto wait_slot = [&](int &slot) -> bool {
+                slot = slot_it % C::kSlots;
+                const bool ok = wait(&bars->slot_full[slot], (slot_it / C::kSlots) & 1);
+                ++slot_it;
+                tc_fence_after_sync();
+                return ok;
+            };
+            for (int it = it_begin; it < it_end && !aborted(); ++it) {
+                const PrefillItem w = items[it];
+                const int n = w.kt1 - w.kt0;
+                // tiles from nh on hold the chunk's own keys, loaded from k/v (fused KV write)
+                const int nh = v_pages && p.fused ? (p.seq_lens[w.r] - p.query_lens[w.r] + 127) / 128 : 0x7fffffff;
+                if (!wait(&bars->q_full, q_uses & 1))
+                    break;
+                ++q_uses;
+                tc_fence_after_sync();
+                int sK, sV;
+                if (!wait_slot(sK))
+                    break;
+                for (int qn = 0; qn < NQ; ++qn) {
+                    issue_qk(qn, sK);
+                    commit(&bars->s_full[qn]);
+                }
+                commit(&bars->slot_empty[sK]);
+                if (n == 1)
+                    commit(&bars->q_empty);
+                bool ok = true;
+                for (int t = 0; t < n && ok; ++t) {
+                    if (!(ok = wait_slot(sV)))
+                        break;
+                    if (!(ok = wait(&bars->p_full[0], p_uses[0] & 1)))
+                        break;
+                    ++p_uses[0];
+                    tc_fence_after_sync();
+                    const bool pm = v_pages && w.kt0 + t < nh;
+                    issue_pv(0, sV, t > 0, pm);
+                    commit(&bars->o_done[0]);
+                    const bool more = t + 1 < n;
+                    if (more) {
+                        if (!(ok = wait_slot(sK)))
+                            break;
+                        issue_qk(0, sK);
+                        commit(&bars->s_full[0]);
+                    }
+                    if (NQ == 2) {
+                        if (!(ok = wait(&bars->p_full[1], p_uses[1] & 1)))
+                            break;
+                        ++p_uses[1];
+                        tc_fence_after_sync();
+                        issue_pv(1, sV, t > 0, pm);
+                        commit(&bars->o_done[1]);
+                    }
+                    commit(&bars->slot_empty[sV]);
+                    if (more) {
+                        if (NQ == 2) {
+                            issue_qk(1, sK);
+                            commit(&bars->s_full[1]);
+                        }
+                        commit(&bars->slot_empty[sK]);
+                        if (t + 2 == n)
+                            commit(&bars->q_empty);
+                    }
+                }
+                if (!ok)
+                    break;
+            }
+            if (aborted()) {
+                // let every MMA issued so far finish before TMEM is released
+                commit(&bars->drain);
+                if (lane == 0) {
+                    uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&bars->drain, 0) && global_timer_ns() - t0 < 100000000ull) {
+                    }
+                }
+            }
+            __syncwarp();
         }
     } else if constexpr (Q8) {
         regs_keep_96();   // one q head a CTA: the other softmax group is idle
