@@ -4,7 +4,6 @@
 #pragma once
 
 #include <atomic>
-#include <type_traits>
 #include <utility>
 
 #include <cuda.h>

@@ -31,7 +31,7 @@
 // stage). The probabilities pass from one to the other by 8 x 8 transposes in registers.
 //
 // Measured (32/8 heads, D 128, pages of 16): 128 rows of 2600 to 5200 keys, 1.05 GB, in
-// 168 us, 6.2 TB/s or 93 % of a plain copy's rate; the rest of a call's 195 us is the plan,
+// 170 us, 6.2 TB/s or 91 % of a plain copy's rate; the rest of a call's 195 us is the plan,
 // the empty chunk launch and the combine. Stages of 64 KB, three of them (two where the
 // merge needs room), keep 128 to 192 KB a SM in flight.
 //

@@ -47,9 +47,9 @@ constexpr int kMinRunTiles = 4;             // shortest run of KV tiles per CTA
 #endif
 constexpr int kUnitCostTiles = CPSA_UNIT_COST_TILES;   // a unit's fixed cost, in KV tiles (< kMinRunTiles)
 // Over the 8-bit cache a unit of 128 columns costs more to start (its Q passes through
-// registers). At 3 eight fresh prompts of 2600 tokens take 635 us and a fresh chunk of 512
-// 21 us, at 2 703 and 30 us (one prompt of 2000 tokens: 70 and 67 us); with 64 columns
-// ragged prompts take 90 us at 3, 88 at 2.
+// registers). At 3 eight fresh prompts of 2600 tokens (32/8 heads) take 628 us and a fresh
+// chunk of 512 19.6 us, at 2 687 and 25.7 (one prompt of 2000 tokens: 67.3 and 64.3 us);
+// with 64 columns six prompts of 1187 tokens (14/2 heads) take 86.8 us at 3, 84.1 at 2.
 __host__ __device__ constexpr int unit_cost_q8(int head_dim) { return head_dim == 128 ? 3 : kUnitCostTiles; }
 static_assert(unit_cost_q8(128) < kMinRunTiles, "a run must hold more than one unit's start");
 static_assert(kUnitCostTiles >= 0 && kUnitCostTiles < kMinRunTiles, "a run must hold more than one unit's start");
@@ -63,9 +63,10 @@ constexpr int kDecodeKeysPerSplit = 4096;   // keys per decode split (multiple o
 constexpr int kDecodeKeysPerSplitGrouped = 1024;
 // Over the 8-bit cache a row's keys per split also go by how many rows a call can hold
 // (its requests, which the host knows): every 1024 once a whole row each would occupy half
-// the SMs (128 rows of 2600 to 5200 keys: 196 us, 199 us every 256), else every 256, and
+// the SMs (128 rows of 2600 to 5200 keys: 190 us, 194 us every 256), else every 256, and
 // every 128 where even eight splits of every row leave SMs idle (one row of 777 keys:
-// 22 us a call, 35 us every 1024).
+// 14.0 us, 15.8 every 256, 32.2 every 1024; a longer row has its eight splits either way,
+// 32768 keys 140 us).
 constexpr int kDecodeKeysPerSplitQ8Few = 256;
 constexpr int kDecodeKeysPerSplitQ8Fewest = 128;
 constexpr int kMaxSplitUnits = kMaxChunkGrid;   // a split unit holds a run boundary: at most grid - 1

@@ -78,7 +78,7 @@ struct ChunkCfg {
     static constexpr int kSlots = D == 128 ? (Q8 ? 3 : 4) : 8;
     static constexpr int kQOff = 0;
     static constexpr int kSlotOff = NQ * kTileBytes;
-    static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer (Q8: e4m3 tiles)
+    static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer; rows on their way out
     static constexpr int kQ8StageOff = kStageOff + kTileBytes;         // Q8: e4m3 tiles
     static constexpr int kBarOff = kStageOff + kTileBytes + (Q8 ? kQ8Stages * 128 * D : 0);
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
@@ -653,7 +653,7 @@ __device__ __noinline__ void merge_split_row_any(const ChunkParams &p, uint32_t 
 // from their own lanes, and selects between the two stores, 416; copies by page, chunks
 // dealt so that nothing is selected, loads ahead of stores, 264; scale bytes not combined
 // before they are used 254; a fourth converter 237; the loader's work off the converters
-// 229; a group's conversion no longer unrolled 213.
+// 229; a group's conversion no longer unrolled 213 (210 as it is now).
 // ---------------------------------------------------------------------------
 constexpr int kQ8Lift = 7;
 
@@ -897,10 +897,11 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                 const uint32_t src = src0 + st * (128 * D);
                 const uint32_t dst = dst0 + slot * C::kTileBytes;
                 // One group at a time: with the softmax and the MMA issuer unrolled as they are,
-                // instruction fetch is what runs short. On an otherwise idle SM six groups take
-                // 890 clocks this way and 645 by twos, their loads first; in the kernel it is all
-                // four groups unrolled 227 us, by twos 214, one by one 213 (and eight fresh
-                // prompts of 2600 tokens 813, 748, 724 us).
+                // instruction fetch is what runs short. On an otherwise idle SM six groups (a warp's
+                // share of a tile among three converters) take 890 clocks this way and 645 by twos,
+                // their loads first; in the kernel, with four converters, all four groups unrolled
+                // took 227 us, by twos 214, one by one 213 (and eight fresh prompts of 2600 tokens
+                // 813, 748, 724 us).
 #pragma unroll 1
                 for (int gp = 0; gp < kGroups; ++gp) {
                     uint4 v[NP];
@@ -942,13 +943,6 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
 // one of these instructions, not just one alike in another branch.
 __device__ __forceinline__ void regs_keep_96() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 __device__ __forceinline__ void regs_take_160() { asm volatile("setmaxnreg.inc.sync.aligned.u32 160;"); }
-
-// Rows leave through the staging buffer by TMA; not with Q8, whose e4m3 tiles take its place.
-template <bool Q8>
-__device__ __forceinline__ bool rows_by_tma(const ChunkParams &p)
-{
-    return p.out_tma;
-}
 
 // This thread's row of O times f. Out of line: rarely called, and the softmax loop's code stays as it is.
 template <int D>
@@ -1024,7 +1018,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        if (D == 128 && rows_by_tma<Q8>(p))
+        if (D == 128 && p.out_tma)
             tma_prefetch_desc(&tm_o);
         if (!Q8 && D == 128 && p.page_size < 128)
             tma_prefetch_desc(&tm_v4);
@@ -1499,7 +1493,11 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // Partials are O / l in bf16 (m and l in fp32 beside them), column-major
                 // per (piece, head): the 8 columns 8j .. 8j + 7 of row `row` as one
                 // 16-byte unit at ((piece * NQ + wg) * D/8 + j) * 128 + row, so a warp's
-                // accesses are 512 contiguous bytes. The unit's partial rows keep
+                // accesses are 512 contiguous bytes. bf16, because three other pieces' partials
+                // of all warps then fit the Q and K/V buffers and the merge reads them from L2 in
+                // one go; it costs a second rounding of half a bf16 step (512 tokens at history
+                // 32256 over the 8-bit cache: 2.4e-3 of the norm from the 64-bit result, 1.7e-3, the
+                // output's own rounding, with whole units). The unit's partial rows keep
                 // the fp32 row pitch of the workspace (decode partials share it).
                 const int piece = w.piece_np & 0xFFFF;
                 unsigned long long *cnt = p.flags + ((int64_t)w.aux * NQ + wg) * 4 + sub;
@@ -1556,7 +1554,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (D == 128 && it + 1 == it_end)
                             staged = NQ == 1 || mbar_wait_warp(&bars->o_done[NQ - 1 - wg], (o_base - 1) & 1, abort);
                         // the merged rows through the writer's buffer once the writer is done with it
-                        const bool ostaged = !Q8 && staged && rows_by_tma<Q8>(p) &&
+                        const bool ostaged = !Q8 && staged && p.out_tma &&
                                              (!p.fused || mbar_wait_warp(&bars->writer_done, 0, abort));
                         merge_split_row<D, NQ, Q8>(p, tO, pml, ph, piece, npieces, wg, row, lane, m_use, l, valid_row,
                                                out_off,
@@ -1589,7 +1587,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // with the KV write, once the cache writer has released its buffer
                 const bool writer_idle =
                     !p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0);
-                const bool staged = rows_by_tma<Q8>(p) && writer_idle && __all_sync(0xffffffffu, valid_row);
+                const bool staged = p.out_tma && writer_idle && __all_sync(0xffffffffu, valid_row);
                 uint8_t *stg = smem + C::kStageOff + (wg * 4 + sub) * 4096;
 #pragma unroll
                 for (int c2 = 0; c2 < D / 64; ++c2) {
@@ -1638,7 +1636,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         }
                     }
                 }
-            } else if (SELF && D == 128 && rows_by_tma<Q8>(p) &&
+            } else if (SELF && D == 128 && p.out_tma &&
                        (!p.fused || __shfl_sync(0xffffffffu, lane == 0 && mbar_test_wait(&bars->writer_done, 0), 0))) {
                 store_unit_rows_staged<D, Q8>(tO, l, own_f, valid_row, smem + C::kStageOff + (wg * 4 + sub) * 4096, &tm_o,
                                           reinterpret_cast<__nv_bfloat16 *>(p.out), t_row, h, p.num_q_heads, lane);
@@ -1805,7 +1803,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     }
 
     // the softmax warps' output stores are complete before the CTA ends
-    if (D == 128 && warp / 4 < NQ && lane == 0 && rows_by_tma<Q8>(p))
+    if (D == 128 && warp / 4 < NQ && lane == 0 && p.out_tma)
         bulk_wait_group0();
     if (threadIdx.x == 0 && bars->abort)
         set_dev_error(p.dev_err, CPSA_DEV_WAIT_TIMEOUT);

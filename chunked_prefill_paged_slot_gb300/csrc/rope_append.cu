@@ -18,8 +18,9 @@
 // same bytes in one thread is what lets q_out be q itself.
 //
 // Bound by memory: 2 bytes in and 2 (or 1) out per element, and the table's row. The
-// bf16 append of a 32768-token prompt (32/8 heads, D 128, 823 MB) takes 125 us, a plain
-// copy of as many bytes 125 us; small calls are bound by latency (one token: 4 us).
+// bf16 append of a 32768-token prompt (32/8 heads, D 128, 823 MB) takes 123 us, 6.7 TB/s
+// or 99 % of a plain copy's rate; small calls are bound by latency (one token: 2 us
+// replayed among others, 11 us a call).
 #include "common.cuh"
 #include "kernels.cuh"
 #include "q8.cuh"
@@ -502,11 +503,10 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
 
 // Blocks [0, kv_blocks): one warp per (window, kv head, k or v), heads fastest (the
 // table's rows of a window are shared through L1); the rest: the q heads.
-// Five blocks an SM (102 registers): a 32768-token prompt (32/8 heads, D 128, 756 MB,
-// which a plain copy of as many bytes moves in 118 us) takes 151 us; 165 us with the 116
-// registers the compiler takes by itself, 152, 154 and 206 us with six, seven and eight
-// blocks; 181 us when the rows were asked for only once their slots were known and kept
-// rotated in registers.
+// Five blocks an SM (96 registers): a 32768-token prompt (32/8 heads, D 128, 756 MB, 111 us
+// at a plain copy's rate) takes 148 us; 161 us with the 116 registers the compiler takes by
+// itself, 159, 147, 151 and 194 us with four, six, seven and eight blocks. (181 us when the
+// rows were asked for only once their slots were known and kept rotated in registers.)
 template <int D, int HPT>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const RopeParams p, int kv_blocks)
 {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const R
 // fewest dependent steps, which is all that counts there), else two (four beside the
 // 8-bit cache's windows, whose registers leave fewer warps to keep loads in flight): the
 // table's values are loaded once for them. A 32768-token prompt into the bf16 cache takes
-// 125 us with two and 130 with four, into the 8-bit cache 172 and 151.
+// 123 us with two and 127 with four, into the 8-bit cache 161 and 148.
 constexpr int kRopeHeads = 2, kRopeHeadsQ8 = 4;
 
 template <int D>

@@ -247,7 +247,9 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
  * Arithmetic: stored values enter the MMAs as f16, exact up to factors of powers of
  * two for blocks down to 2^-22 of the largest scale among the 128 keys (K) or the
  * keys so far (V) that are multiplied together, f16 under it; q rows likewise under
- * a power of two of their own; probabilities in f16; everything else in fp32.
+ * a power of two of their own; probabilities in f16; partial results of a chunk's
+ * split units in bf16, as in cpp_chunked_prefill_attn; everything else in fp32.
+ * Scale bytes 0 and 255, which the append never stores, are read as 1 and 254.
  */
 int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
                                 const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
