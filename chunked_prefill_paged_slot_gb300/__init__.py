@@ -7,6 +7,11 @@ this package is its Python binding plus host-side orchestration:
   cpp_rope_kv_cache_write   rotary position embedding of q and k fused with that append
   cpp_rope_kv_cache_write_q8
                             the same into an 8-bit cache (e4m3, a scale per 16 tokens and head)
+  cpp_rope_kv_cache_write_q4
+                            and into a 4-bit one (e2m1 codes, a scale per 16 columns)
+  cpp_norm_rope_kv_cache_write (and _q8, _q4)
+                            the same with an RMS norm of every q and k head before the rotation
+  cpp_kv_cache_read_q4      rows of the 4-bit cache back as bf16
   cpp_chunked_prefill_attn  causal attention of prefill chunks and decode rows
   cpp_chunked_prefill_attn_write_kv
                             the KV write fused into that attention call
@@ -23,6 +28,8 @@ this package is its Python binding plus host-side orchestration:
 """
 from ._lib import (  # noqa: F401
     CpsaError, load, cpp_kv_cache_write, cpp_rope_kv_cache_write, cpp_rope_kv_cache_write_q8,
+    cpp_rope_kv_cache_write_q4, cpp_norm_rope_kv_cache_write, cpp_norm_rope_kv_cache_write_q8,
+    cpp_norm_rope_kv_cache_write_q4, cpp_kv_cache_read_q4,
     cpp_attn_workspace_bytes, cpp_attn_workspace_min_bytes,
     cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_q8, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
     cpp_noalloc_scratch_address,

@@ -56,6 +56,14 @@ def load():
                                             _c_p, _c_p, _c_p]
     lib.cpp_rope_kv_cache_write_q8.restype = _c_int
     lib.cpp_rope_kv_cache_write_q8.argtypes = lib.cpp_rope_kv_cache_write.argtypes + [_c_p, _c_p]
+    lib.cpp_rope_kv_cache_write_q4.restype = _c_int
+    lib.cpp_rope_kv_cache_write_q4.argtypes = lib.cpp_rope_kv_cache_write_q8.argtypes
+    for name in ("cpp_rope_kv_cache_write", "cpp_rope_kv_cache_write_q8", "cpp_rope_kv_cache_write_q4"):
+        plain, normed = getattr(lib, name), getattr(lib, name.replace("cpp_rope", "cpp_norm_rope"))
+        normed.restype = _c_int
+        normed.argtypes = plain.argtypes[:6] + [_c_p, _c_p, _c_f] + plain.argtypes[6:]
+    lib.cpp_kv_cache_read_q4.restype = _c_int
+    lib.cpp_kv_cache_read_q4.argtypes = [_c_p] * 5 + [_c_i64, _c_int, _c_int, _c_int, _c_i64] + [_c_p] * 4
     lib.cpp_attn_workspace_bytes.restype = _c_size
     lib.cpp_attn_workspace_bytes.argtypes = [_c_int, _c_i64, _c_int, _c_int, _c_int, _c_int]
     lib.cpp_attn_workspace_min_bytes.restype = _c_size
@@ -218,13 +226,15 @@ def _rows(t: torch.Tensor, tokens, heads, d, name, device):
     return t.data_ptr(), (s[0] if tokens > 1 else heads * d)
 
 
-def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cache, q_out, dev_err, interleaved, stream):
-    """Both rotary appends: `caches`(device) gives the addresses of the cache's tensors, `cache` is the k cache."""
+def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cache, q_out, dev_err, interleaved, stream,
+               norm=None, per_byte=1):
+    """The rotary appends: `caches`(device) gives the addresses of the cache's tensors, `cache` is the k cache; norm:
+    None, or (q_weight, k_weight, eps); per_byte: columns to an element of the cache."""
     if not isinstance(k, torch.Tensor) or not isinstance(cache, torch.Tensor) or k.dim() != 3 or cache.dim() != 4:
         raise CpsaError(f"{what}: inconsistent shapes")
     T, Hkv, d = kshape = k.shape
     pages, Hkv2, P, d2 = cache.shape
-    if v.shape != kshape or Hkv2 != Hkv or d2 != d or slot_mapping.shape != (T,) or (q is None) != (q_out is None) \
+    if v.shape != kshape or Hkv2 != Hkv or d2 * per_byte != d or slot_mapping.shape != (T,) or (q is None) != (q_out is None) \
             or (cos_sin is None) != (positions is None):
         raise CpsaError(f"{what}: inconsistent shapes")
     handle, device = _where(stream, k, "k")
@@ -243,7 +253,14 @@ def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cach
         pos, cs = _ptr(positions, _I64, "positions", device), _ptr(cos_sin, _F32, "cos_sin", device)
     kp, ks = _rows(k, T, Hkv, d, "k", device)
     vp, vs = _rows(v, T, Hkv, d, "v", device)
-    st = fn(qp, kp, vp, qs, ks, vs, pos, cs, top, rot, 1 if interleaved else 0,
+    more = ()
+    if norm is not None:
+        q_weight, k_weight, eps = norm
+        if (q_weight is None) != (q is None) or k_weight.shape != (d,) or (q_weight is not None and q_weight.shape != (d,)):
+            raise CpsaError(f"{what}: k_weight, and q_weight with q, must have shape ({d},)")
+        more = (None if q_weight is None else _ptr(q_weight, _F32, "q_weight", device),
+                _ptr(k_weight, _F32, "k_weight", device), float(eps))
+    st = fn(qp, kp, vp, qs, ks, vs, *more, pos, cs, top, rot, 1 if interleaved else 0,
             _ptr(slot_mapping, _I64, "slot_mapping", device), T, Hq, Hkv, d, P, pages, qo, *caches(device),
             _ptr(dev_err, _I32, "dev_err", device), handle)
     if st != 0:
@@ -286,6 +303,79 @@ def cpp_rope_kv_cache_write_q8(q, k, v, positions, cos_sin, slot_mapping, k_cach
     _rope_call("cpp_rope_kv_cache_write_q8", load().cpp_rope_kv_cache_write_q8,
                lambda dev: _q8_pointers(k_cache, v_cache, k_scale, v_scale, dev),
                q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream)
+
+
+# The 4-bit cache's bytes hold two codes each: torch's type of that name, or plain bytes.
+_CODES = (torch.uint8, torch.float4_e2m1fn_x2)
+
+
+def _q4_pointers(k_cache, v_cache, k_scale, v_scale, device):
+    """The four tensors of a 4-bit cache: [pages, Hkv, P, d / 2] bytes and [pages, Hkv, P, d / 16] scales."""
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise CpsaError("k_cache must be [pages, kv heads, page size, head dim / 2]")
+    scales = (shape[0], shape[1], shape[2], shape[3] // 8)
+    for t, want, name in ((v_cache, shape, "v_cache"), (k_scale, scales, "k_scale"), (v_scale, scales, "v_scale")):
+        if t.shape != want:
+            raise CpsaError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+    return (_ptr(k_cache, _CODES, "k_cache", device), _ptr(v_cache, _CODES, "v_cache", device),
+            _ptr(k_scale, _U8, "k_scale", device), _ptr(v_scale, _U8, "v_scale", device))
+
+
+def cpp_rope_kv_cache_write_q4(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
+                               dev_err, interleaved=False, stream=None):
+    """cpp_rope_kv_cache_write into a 4-bit cache: caches [pages, Hkv, P, d / 2] torch.float4_e2m1fn_x2 (or uint8), the
+    even column in a byte's low half; k_scale, v_scale [pages, Hkv, P, d / 16] uint8, one for every 16 columns of a place
+    (byte << 7 are the bits of the f16 number it stands for)."""
+    _rope_call("cpp_rope_kv_cache_write_q4", load().cpp_rope_kv_cache_write_q4,
+               lambda dev: _q4_pointers(k_cache, v_cache, k_scale, v_scale, dev),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream, per_byte=2)
+
+
+def cpp_norm_rope_kv_cache_write(q, k, v, q_weight, k_weight, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
+                                 dev_err, eps=1e-6, interleaved=False, stream=None):
+    """cpp_rope_kv_cache_write with an RMS norm of every q and k head before its rotation: x / sqrt(mean(x^2) + eps) *
+    weight, q_weight and k_weight fp32 [d] (q_weight None where q is). positions = cos_sin = None norms without rotating."""
+    if v_cache.shape != k_cache.shape:
+        raise CpsaError("cpp_norm_rope_kv_cache_write: inconsistent shapes")
+    _rope_call("cpp_norm_rope_kv_cache_write", load().cpp_norm_rope_kv_cache_write,
+               lambda dev: (_ptr(k_cache, _BF16, "k_cache", dev), _ptr(v_cache, _BF16, "v_cache", dev)),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream,
+               norm=(q_weight, k_weight, eps))
+
+
+def cpp_norm_rope_kv_cache_write_q8(q, k, v, q_weight, k_weight, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                                    k_scale, v_scale, q_out, dev_err, eps=1e-6, interleaved=False, stream=None):
+    """cpp_norm_rope_kv_cache_write into an 8-bit cache (its tensors: cpp_rope_kv_cache_write_q8)."""
+    _rope_call("cpp_norm_rope_kv_cache_write_q8", load().cpp_norm_rope_kv_cache_write_q8,
+               lambda dev: _q8_pointers(k_cache, v_cache, k_scale, v_scale, dev),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream,
+               norm=(q_weight, k_weight, eps))
+
+
+def cpp_norm_rope_kv_cache_write_q4(q, k, v, q_weight, k_weight, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                                    k_scale, v_scale, q_out, dev_err, eps=1e-6, interleaved=False, stream=None):
+    """cpp_norm_rope_kv_cache_write into a 4-bit cache (its tensors: cpp_rope_kv_cache_write_q4)."""
+    _rope_call("cpp_norm_rope_kv_cache_write_q4", load().cpp_norm_rope_kv_cache_write_q4,
+               lambda dev: _q4_pointers(k_cache, v_cache, k_scale, v_scale, dev),
+               q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream,
+               norm=(q_weight, k_weight, eps), per_byte=2)
+
+
+def cpp_kv_cache_read_q4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k, v, dev_err, stream=None):
+    """Rows of a 4-bit cache back as bf16: k, v [T, Hkv, d] bf16 take the places slot_mapping [T] int64 names (negative:
+    the token's rows are left as they were). The cache's tensors: cpp_rope_kv_cache_write_q4."""
+    handle, device = _where(stream, k_cache, "k_cache")
+    caches = _q4_pointers(k_cache, v_cache, k_scale, v_scale, device)
+    pages, Hkv, P, half = k_cache.shape
+    T, d = k.shape[0], 2 * half
+    if k.shape != (T, Hkv, d) or v.shape != k.shape or slot_mapping.shape != (T,):
+        raise CpsaError("cpp_kv_cache_read_q4: inconsistent shapes")
+    st = load().cpp_kv_cache_read_q4(*caches, _ptr(slot_mapping, _I64, "slot_mapping", device), T, Hkv, d, P, pages,
+                                     _ptr(k, _BF16, "k", device), _ptr(v, _BF16, "v", device),
+                                     _ptr(dev_err, _I32, "dev_err", device), handle)
+    if st != 0:
+        _check(st, "cpp_kv_cache_read_q4")
 
 
 def cpp_attn_workspace_bytes(num_reqs, num_tokens, num_q_heads, num_kv_heads, head_dim, max_kv_splits=8):

@@ -208,21 +208,31 @@ int check_attn_shape(int num_reqs, int64_t num_tokens, int num_q_heads, int num_
     return CPSA_OK;
 }
 
-// Both rotary KV appends: the checks, then one launch.
+// What a head norm takes; none: all empty.
+struct HeadNorm {
+    const float *q_weight, *k_weight;
+    float eps;
+};
+
+// The rotary KV appends, into a cache of `bits` (16, 8 or 4) a number, with head norms
+// where `norm` is given: the checks, then one launch.
 int rope_append_impl(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                      int64_t v_stride, const int64_t *positions, const float *cos_sin, int64_t max_positions,
                      int rotary_dim, int interleaved, const int64_t *slot_mapping, int64_t num_tokens,
                      int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages, void *q_out,
-                     void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale, bool q8, uint32_t *dev_err,
-                     void *stream)
+                     void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale, int bits, uint32_t *dev_err,
+                     void *stream, const HeadNorm *norm = nullptr)
 {
+    const bool scaled = bits < 16;
     if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX / 2 || num_q_heads < 0 || num_kv_heads <= 0 ||
         num_q_heads > 65535 || num_kv_heads > 65535 || num_pages < 0 || max_positions < 0 || rotary_dim < 0)
         return CPSA_ERR_BAD_SHAPE;
     if (head_dim != 64 && head_dim != 128)
         return CPSA_ERR_UNSUPPORTED;
-    if (!(q8 ? pow2_in(page_size, 8, 256) : pow2_in(page_size, 1, 1 << 20)))
+    if (!(scaled ? pow2_in(page_size, 8, 256) : pow2_in(page_size, 1, 1 << 20)))
         return CPSA_ERR_UNSUPPORTED;
+    if (norm && !(norm->eps > 0.f && norm->eps <= 3.4e38f))
+        return CPSA_ERR_BAD_SHAPE;
     if (rotary_dim > head_dim || rotary_dim % 16 != 0)
         return CPSA_ERR_UNSUPPORTED;
     if (num_pages > ((int64_t)1 << 62) / page_size || max_positions > ((int64_t)1 << 55))
@@ -236,11 +246,15 @@ int rope_append_impl(const void *q, const void *k, const void *v, int64_t q_stri
     if (num_tokens == 0)
         return CPSA_OK;
     if (!k || !v || !slot_mapping || !k_cache || !v_cache || !dev_err || (num_q_heads > 0 && (!q || !q_out)) ||
-        (rotary_dim > 0 && (!positions || !cos_sin)) || (q8 && (!k_scale || !v_scale)))
+        (rotary_dim > 0 && (!positions || !cos_sin)) || (scaled && (!k_scale || !v_scale)) ||
+        (norm && (!norm->k_weight || (num_q_heads > 0 && !norm->q_weight))))
         return CPSA_ERR_NULL_ARG;
+    if (bits == 4 && (!aligned16(k_scale) || !aligned16(v_scale)))   // the attention reads them by TMA
+        return CPSA_ERR_MISALIGNED;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
         (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out) || q_stride % 8 != 0)) || k_stride % 8 != 0 ||
-        v_stride % 8 != 0 || (rotary_dim > 0 && !aligned16(cos_sin)))
+        v_stride % 8 != 0 || (rotary_dim > 0 && !aligned16(cos_sin)) ||
+        (norm && (!aligned16(norm->k_weight) || (num_q_heads > 0 && !aligned16(norm->q_weight)))))
         return CPSA_ERR_MISALIGNED;
     // in place only where every row is written back to where it was read
     if (num_q_heads > 0 && q == q_out && q_stride != (int64_t)num_q_heads * head_dim)
@@ -273,7 +287,12 @@ int rope_append_impl(const void *q, const void *k, const void *v, int64_t q_stri
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.dev_err = dev_err;
-    return launch_rope_append(p, head_dim, q8, sms, (cudaStream_t)stream) == cudaSuccess ? CPSA_OK : CPSA_ERR_CUDA;
+    if (norm) {
+        p.q_weight = norm->q_weight;
+        p.k_weight = norm->k_weight;
+        p.eps = norm->eps;
+    }
+    return launch_rope_append(p, head_dim, bits, sms, (cudaStream_t)stream) == cudaSuccess ? CPSA_OK : CPSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -331,7 +350,7 @@ int cpp_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t
 {
     return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
                             interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
-                            num_pages, q_out, k_cache, v_cache, nullptr, nullptr, false, dev_err, stream);
+                            num_pages, q_out, k_cache, v_cache, nullptr, nullptr, 16, dev_err, stream);
 }
 
 int cpp_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
@@ -343,7 +362,95 @@ int cpp_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int6
 {
     return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
                             interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
-                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, true, dev_err, stream);
+                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, 8, dev_err, stream);
+}
+
+int cpp_rope_kv_cache_write_q4(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                               int64_t max_positions, int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                               int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                               int64_t num_pages, void *q_out, void *k_cache, void *v_cache, uint8_t *k_scale,
+                               uint8_t *v_scale, uint32_t *dev_err, void *stream)
+{
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, 4, dev_err, stream);
+}
+
+int cpp_norm_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                 const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                 int rotary_dim, int interleaved, const int64_t *slot_mapping, int64_t num_tokens,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                 void *q_out, void *k_cache, void *v_cache, uint32_t *dev_err, void *stream)
+{
+    const HeadNorm norm{q_weight, k_weight, eps};
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, nullptr, nullptr, 16, dev_err, stream, &norm);
+}
+
+int cpp_norm_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                    const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                    int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                                    int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int64_t num_pages, void *q_out, void *k_cache, void *v_cache,
+                                    uint8_t *k_scale, uint8_t *v_scale, uint32_t *dev_err, void *stream)
+{
+    const HeadNorm norm{q_weight, k_weight, eps};
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, 8, dev_err, stream, &norm);
+}
+
+int cpp_norm_rope_kv_cache_write_q4(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                    const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                    int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                                    int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int64_t num_pages, void *q_out, void *k_cache, void *v_cache,
+                                    uint8_t *k_scale, uint8_t *v_scale, uint32_t *dev_err, void *stream)
+{
+    const HeadNorm norm{q_weight, k_weight, eps};
+    return rope_append_impl(q, k, v, q_stride, k_stride, v_stride, positions, cos_sin, max_positions, rotary_dim,
+                            interleaved, slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, page_size,
+                            num_pages, q_out, k_cache, v_cache, k_scale, v_scale, 4, dev_err, stream, &norm);
+}
+
+int cpp_kv_cache_read_q4(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                         const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                         int page_size, int64_t num_pages, void *k, void *v, uint32_t *dev_err, void *stream)
+{
+    if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX / 2 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+        num_pages < 0)
+        return CPSA_ERR_BAD_SHAPE;
+    if ((head_dim != 64 && head_dim != 128) || !pow2_in(page_size, 8, 256))
+        return CPSA_ERR_UNSUPPORTED;
+    if (num_pages > ((int64_t)1 << 62) / page_size)
+        return CPSA_ERR_BAD_SHAPE;
+    if (num_tokens == 0)
+        return CPSA_OK;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !slot_mapping || !k || !v || !dev_err)
+        return CPSA_ERR_NULL_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(k) ||
+        !aligned16(v))
+        return CPSA_ERR_MISALIGNED;
+    if (sm_count() <= 0)
+        return CPSA_ERR_NO_DEVICE;
+    const ReadQ4Params p{static_cast<const uint8_t *>(k_cache),
+                         static_cast<const uint8_t *>(v_cache),
+                         k_scale,
+                         v_scale,
+                         slot_mapping,
+                         num_tokens,
+                         num_pages,
+                         num_kv_heads,
+                         __builtin_ctz((unsigned)page_size),
+                         static_cast<__nv_bfloat16 *>(k),
+                         static_cast<__nv_bfloat16 *>(v),
+                         dev_err};
+    return launch_read_q4(p, head_dim, (cudaStream_t)stream) == cudaSuccess ? CPSA_OK : CPSA_ERR_CUDA;
 }
 
 size_t cpp_attn_workspace_bytes(int num_reqs, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,

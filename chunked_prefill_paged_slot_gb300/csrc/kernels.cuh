@@ -96,8 +96,21 @@ struct RopeParams {
     int Hq, Hkv, page_size, lg_page;
     int64_t num_pages;
     __nv_bfloat16 *q_out;
-    void *k_cache, *v_cache;   // bf16, or e4m3 bytes
-    uint8_t *k_scale, *v_scale;   // e4m3 cache: [pages][Hkv][page_size / min(16, page_size)], exponent + 127
+    void *k_cache, *v_cache;   // bf16, e4m3 bytes, or 4-bit codes
+    uint8_t *k_scale, *v_scale;   // e4m3: [pages][Hkv][page_size / min(16, page_size)], exponent + 127; 4 bits:
+                                  // [pages][Hkv][page_size][head_dim / 16], see q4.cuh
+    uint32_t *dev_err;
+    const float *q_weight, *k_weight;   // head norms: [head_dim]; k_weight = nullptr: none
+    float eps;
+};
+
+// Rows of the 4-bit cache read back (rope_append.cu).
+struct ReadQ4Params {
+    const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+    const int64_t *slot_mapping;
+    int64_t num_tokens, num_pages;
+    int Hkv, lg_page;
+    __nv_bfloat16 *k, *v;      // [num_tokens][Hkv][head_dim]
     uint32_t *dev_err;
 };
 
@@ -136,7 +149,9 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
 cudaError_t launch_decode_q8(const DecodeParams &p, const Q8Cache &c, const CUtensorMap &tk, const CUtensorMap &tv,
                              int head_dim, int heads_per_item, int grid, cudaStream_t s, bool early);
 int decode_q8_box_rows(int page_size, int heads_per_item);
-cudaError_t launch_rope_append(const RopeParams &p, int head_dim, bool q8, int num_sms, cudaStream_t s);
+// bits: of a cache's numbers, 16 (bf16), 8 (e4m3) or 4
+cudaError_t launch_rope_append(const RopeParams &p, int head_dim, int bits, int num_sms, cudaStream_t s);
+cudaError_t launch_read_q4(const ReadQ4Params &p, int head_dim, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,
                                     int32_t length_threshold, int32_t *out3, cudaStream_t s);
 

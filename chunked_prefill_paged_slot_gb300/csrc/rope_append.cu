@@ -1,8 +1,10 @@
 // rope_append.cu -- the rotary KV append: rotate the new tokens' q and k by
 // their positions, write the rotated q, and append k and v to the paged cache,
-// in one pass over the projection's output. Two cache formats: bf16, and e4m3
+// in one pass over the projection's output. Three cache formats: bf16; e4m3
 // bytes with a power-of-two scale per (page, kv head, block of SB tokens),
-// SB = min(16, page_size).
+// SB = min(16, page_size); and 4-bit codes with a scale per place, kv head and 16
+// columns (q4.cuh). With NORM every q and k head is first brought to unit mean square
+// and multiplied by its weights.
 //
 // Rotation of a pair (a, b) by the angle t of its position:
 //   (a cos t - b sin t, b cos t + a sin t),
@@ -23,6 +25,7 @@
 // replayed among others, 11 us a call).
 #include "common.cuh"
 #include "kernels.cuh"
+#include "q4.cuh"
 #include "q8.cuh"
 
 namespace cpsa {
@@ -105,13 +108,81 @@ __device__ __forceinline__ int position_state(const RopeParams &p, int64_t t, in
     return pos < 0 ? 1 : (pos >= p.max_positions ? 2 : 0);
 }
 
-// One unit column u of HPT consecutive heads of one token: q heads, then (WITH_KV:
-// the bf16 cache) k heads, then v heads. The table's values are loaded once for
+// Head norm: y_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c, in fp32. The D/16 threads of a head
+// are neighbours in a warp: each sums its 16 squares (exact products of bf16 numbers), a
+// butterfly adds up the threads', in an order that does not depend on anything.
+__device__ __forceinline__ float squares8(const uint4 &x)
+{
+    float f[8], a = 0.f;
+    widen8(x, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaf(f[i], f[i], a);
+    return a;
+}
+
+template <int D>
+__device__ __forceinline__ float inverse_rms(const uint4 &v0, const uint4 &v1, float eps, uint32_t mask)
+{
+    float a = squares8(v0) + squares8(v1);
+#pragma unroll
+    for (int o = D / 32; o > 0; o >>= 1) a += __shfl_xor_sync(mask, a, o);
+    return 1.f / sqrtf(a * (1.f / D) + eps);
+}
+
+__device__ __forceinline__ void scale8(float (&x)[8], float f, const float *w)
+{
+    float k[8];
+    load8(w, k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * f * k[i];
+}
+
+// What rope_heads does with k and v.
+enum { kNoKv, kKvBf16, kKvQ4 };
+
+// A unit of a k head whose 16 columns are two vectors of eight from c0 and c1 on, of two
+// groups: the amax bits of each vector's other half of its group. Vectors of eight are
+// numbered along the head; number i sits at (unit, which) = (i, 0) and (i - R, 1) for the R
+// split units' first and second vectors, (i / 2, i & 1) behind them.
+template <int D>
+__device__ __forceinline__ void group_partners(uint32_t m0, uint32_t m1, int u, int rot, bool inter, uint32_t mask,
+                                               uint32_t &o0, uint32_t &o1)
+{
+    if (inter || rot == 0) {
+        o0 = m1;
+        o1 = m0;
+        return;
+    }
+    if ((rot & 31) == 0) {   // both halves of a group sit in the same place of two neighbours
+        const uint32_t a = __shfl_xor_sync(mask, m0, 1), b = __shfl_xor_sync(mask, m1, 1);
+        const bool split = u < (rot >> 4);
+        o0 = split ? a : m1;
+        o1 = split ? b : m0;
+        return;
+    }
+    const int R = rot >> 4;
+    int c0, c1;
+    unit_cols(u, rot, inter, c0, c1);
+    auto fetch = [&](int i) -> uint32_t {
+        const int from = i < R ? i : (i < 2 * R ? i - R : i >> 1);
+        const bool second = i < R ? false : (i < 2 * R ? true : (i & 1) != 0);
+        const uint32_t a = __shfl_sync(mask, m0, from, D / 16), b = __shfl_sync(mask, m1, from, D / 16);
+        return second ? b : a;
+    };
+    o0 = fetch((c0 >> 3) ^ 1);
+    o1 = fetch((c1 >> 3) ^ 1);
+}
+
+// One unit column u of HPT consecutive heads of one token: q heads, then (KV: into the
+// bf16 or the 4-bit cache) k heads, then v heads. The table's values are loaded once for
 // all of them, and every head's vectors are in flight before the first is used.
-template <int D, int HPT, bool WITH_KV>
+template <int D, int HPT, int KV, bool NORM>
 __device__ __forceinline__ void rope_heads(const RopeParams &p, int64_t t, int head0, int u)
 {
+    constexpr bool WITH_KV = KV != kNoKv;
     const int heads = WITH_KV ? p.Hq + 2 * p.Hkv : p.Hq;
+    // the head's threads, which have the same way through here
+    const uint32_t mask = (D == 128 ? 0xffu : 0xfu) << (threadIdx.x & 31 & ~(D / 16 - 1));
     int64_t pos;
     const int state = position_state(p, t, pos);
     if (state != 0) {
@@ -140,8 +211,9 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int64_t t, int h
         const __nv_bfloat16 *src = h < p.Hq ? p.q + t * p.q_stride + h * D
                                    : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * D
                                                       : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
-        v0[i] = *reinterpret_cast<const uint4 *>(src + c0);
-        v1[i] = *reinterpret_cast<const uint4 *>(src + c1);
+        const bool whole = KV == kKvQ4 && h >= p.Hq + p.Hkv;   // a v unit of the 4-bit cache is one group
+        v0[i] = *reinterpret_cast<const uint4 *>(src + (whole ? 16 * u : c0));
+        v1[i] = *reinterpret_cast<const uint4 *>(src + (whole ? 16 * u + 8 : c1));
     }
     float c[8], s[8];
     if (turn) {
@@ -153,11 +225,44 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int64_t t, int h
         const int h = head0 + i;
         if (h >= heads || (h >= p.Hq && slot < 0))
             continue;
-        if (turn && h < p.Hq + p.Hkv) {
+        const bool normed = NORM && h < p.Hq + p.Hkv;
+        const bool four = KV == kKvQ4 && h >= p.Hq;
+        if ((turn && h < p.Hq + p.Hkv) || normed || four) {
             float x0[8], x1[8];
             widen8(v0[i], x0);
             widen8(v1[i], x1);
-            rotate_unit(x0, x1, c, s, p.inter);
+            if (normed) {
+                const float f = inverse_rms<D>(v0[i], v1[i], p.eps, mask);
+                const float *w = h < p.Hq ? p.q_weight : p.k_weight;
+                scale8(x0, f, w + c0);
+                scale8(x1, f, w + c1);
+            }
+            if (turn && h < p.Hq + p.Hkv)
+                rotate_unit(x0, x1, c, s, p.inter);
+            if (four) {
+                const bool is_k = h < p.Hq + p.Hkv;
+                const int kvh = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+                const int64_t row = ((slot >> p.lg_page) * p.Hkv + kvh) * p.page_size + (slot & (p.page_size - 1));
+                uint8_t *codes = reinterpret_cast<uint8_t *>(is_k ? p.k_cache : p.v_cache) + row * (D / 2);
+                uint8_t *scales = (is_k ? p.k_scale : p.v_scale) + row * (D / kQ4Group);
+                const uint32_t m0 = q4_amax(x0), m1 = q4_amax(x1);
+                if (!is_k) {
+                    const Q4Scale f(max(m0, m1));
+                    *reinterpret_cast<uint2 *>(codes + 8 * u) = make_uint2(q4_codes(x0, f), q4_codes(x1, f));
+                    scales[u] = f.byte;
+                } else {
+                    uint32_t o0, o1;
+                    group_partners<D>(m0, m1, u, p.rot, p.inter, mask, o0, o1);
+                    const Q4Scale f0(max(m0, o0)), f1(max(m1, o1));
+                    *reinterpret_cast<uint32_t *>(codes + (c0 >> 1)) = q4_codes(x0, f0);
+                    *reinterpret_cast<uint32_t *>(codes + (c1 >> 1)) = q4_codes(x1, f1);
+                    if ((c0 & 8) == 0)
+                        scales[c0 >> 4] = f0.byte;
+                    if ((c1 & 8) == 0)
+                        scales[c1 >> 4] = f1.byte;
+                }
+                continue;
+            }
             v0[i] = narrow8(x0);
             v1[i] = narrow8(x1);
         }
@@ -178,22 +283,23 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int64_t t, int h
 
 // Items (token, group of HPT heads), D/16 threads each, units fastest: the eight
 // threads of a 128-column head read 128 consecutive bytes twice.
-template <int D, int HPT, bool WITH_KV>
+template <int D, int HPT, int KV, bool NORM>
 __device__ __forceinline__ void rope_items(const RopeParams &p, int64_t first, int64_t step)
 {
     constexpr int UPH = D / 16;
-    const int groups = ((WITH_KV ? p.Hq + 2 * p.Hkv : p.Hq) + HPT - 1) / HPT;
+    const int groups = ((KV != kNoKv ? p.Hq + 2 * p.Hkv : p.Hq) + HPT - 1) / HPT;
     const int64_t total = p.num_tokens * groups;
     for (int64_t i = first / UPH; i < total; i += step / UPH)
-        rope_heads<D, HPT, WITH_KV>(p, i / groups, (int)(i % groups) * HPT, (int)(first % UPH));
+        rope_heads<D, HPT, KV, NORM>(p, i / groups, (int)(i % groups) * HPT, (int)(first % UPH));
 }
 
-template <int D, int HPT>
+template <int D, int HPT, int KV, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p)
 {
     pdl_trigger();
     pdl_wait();
-    rope_items<D, HPT, true>(p, (int64_t)blockIdx.x * kRopeThreads + threadIdx.x, (int64_t)gridDim.x * kRopeThreads);
+    rope_items<D, HPT, KV, NORM>(p, (int64_t)blockIdx.x * kRopeThreads + threadIdx.x,
+                                 (int64_t)gridDim.x * kRopeThreads);
 }
 
 // ---------------------------------------------------------------------------
@@ -260,7 +366,7 @@ __device__ __forceinline__ uint32_t rescale_bytes(uint32_t w, uint32_t f16x2_fac
     return out;
 }
 
-template <int D>
+template <int D, bool NORM>
 __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t window, int job, int lane)
 {
     constexpr int LPR = D / 16;              // lanes per row
@@ -277,6 +383,7 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
     // always they are the rows to do (else they are loaded again), and the two latencies
     // overlap.
     uint4 v0[PASSES], v1[PASSES];
+    float norm[PASSES];                      // NORM: 1 / root mean square of the k rows
     int c0, c1;
     unit_cols(u, is_k ? p.rot : 0, p.inter, c0, c1);
     const __nv_bfloat16 *src = is_k ? p.k + kvh * D : p.v + kvh * D;
@@ -374,6 +481,10 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
         auto values = [&](int q, bool on, float (&x0)[8], float (&x1)[8]) {
             widen8(v0[q], x0);
             widen8(v1[q], x1);
+            if (NORM && is_k) {
+                scale8(x0, norm[q], p.k_weight + c0);
+                scale8(x1, norm[q], p.k_weight + c1);
+            }
             const int64_t at = __shfl_sync(0xffffffffu, rpos, q * RPP + rsub);
             if (on && is_k && u < (p.rot >> 4)) {
                 float c[8], s[8];
@@ -382,6 +493,10 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
                 rotate_unit(x0, x1, c, s, p.inter);
             }
         };
+        if (NORM && is_k) {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) norm[q] = inverse_rms<D>(v0[q], v1[q], p.eps, 0xffffffffu);
+        }
         // 1. the rows' largest finite magnitudes. Infinities, which neither count nor saturate
         // but become NaN, are rare: whether there are any is seen from the maxima, and only
         // then is every value looked at for itself. (A maximum passes over NaN.)
@@ -507,7 +622,7 @@ __device__ __forceinline__ void append_q8_window(const RopeParams &p, int64_t wi
 // at a plain copy's rate) takes 148 us; 161 us with the 116 registers the compiler takes by
 // itself, 159, 147, 151 and 194 us with four, six, seven and eight blocks. (181 us when the
 // rows were asked for only once their slots were known and kept rotated in registers.)
-template <int D, int HPT>
+template <int D, int HPT, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const RopeParams p, int kv_blocks)
 {
     pdl_trigger();
@@ -516,10 +631,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const R
         const int64_t windows = (p.num_tokens + kQ8Rows - 1) / kQ8Rows;
         const int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
         if (w < windows * 2 * p.Hkv)
-            append_q8_window<D>(p, w / (2 * p.Hkv), (int)(w % (2 * p.Hkv)), threadIdx.x & 31);
+            append_q8_window<D, NORM>(p, w / (2 * p.Hkv), (int)(w % (2 * p.Hkv)), threadIdx.x & 31);
     } else {
-        rope_items<D, HPT, false>(p, (int64_t)(blockIdx.x - kv_blocks) * kRopeThreads + threadIdx.x,
-                                  (int64_t)(gridDim.x - kv_blocks) * kRopeThreads);
+        rope_items<D, HPT, kNoKv, NORM>(p, (int64_t)(blockIdx.x - kv_blocks) * kRopeThreads + threadIdx.x,
+                                        (int64_t)(gridDim.x - kv_blocks) * kRopeThreads);
     }
 }
 
@@ -530,9 +645,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_q8_kernel(const R
 // 123 us with two and 127 with four, into the 8-bit cache 161 and 148.
 constexpr int kRopeHeads = 2, kRopeHeadsQ8 = 4;
 
-template <int D>
-cudaError_t launch_rope_t(const RopeParams &p, bool q8, int num_sms, cudaStream_t s)
+template <int D, bool NORM>
+cudaError_t launch_rope_t(const RopeParams &p, int bits, int num_sms, cudaStream_t s)
 {
+    const bool q8 = bits == 8;
     const int heads = q8 ? p.Hq : p.Hq + 2 * p.Hkv;
     const int many = q8 ? kRopeHeadsQ8 : kRopeHeads;
     const bool one = p.num_tokens * heads * (D / 16) <= (int64_t)num_sms * 1024;
@@ -540,24 +656,77 @@ cudaError_t launch_rope_t(const RopeParams &p, bool q8, int num_sms, cudaStream_
     int64_t blocks = (items + kRopeThreads - 1) / kRopeThreads;
     if (blocks > (int64_t)num_sms * 64)
         blocks = (int64_t)num_sms * 64;
-    if (!q8)
-        return launch_pdl(false, one ? rope_append_kernel<D, 1> : rope_append_kernel<D, kRopeHeads>,
-                          dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, p);
+    if (!q8) {
+        auto k = bits == 4 ? (one ? rope_append_kernel<D, 1, kKvQ4, NORM> : rope_append_kernel<D, kRopeHeads, kKvQ4, NORM>)
+                           : (one ? rope_append_kernel<D, 1, kKvBf16, NORM> : rope_append_kernel<D, kRopeHeads, kKvBf16, NORM>);
+        return launch_pdl(false, k, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, p);
+    }
     const int64_t warps = (p.num_tokens + kQ8Rows - 1) / kQ8Rows * 2 * p.Hkv;
     const int64_t kv_blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
     if (kv_blocks + blocks > 0x7fffffff)
         return cudaErrorInvalidValue;
-    return launch_pdl(false, one ? rope_append_q8_kernel<D, 1> : rope_append_q8_kernel<D, kRopeHeadsQ8>,
+    return launch_pdl(false, one ? rope_append_q8_kernel<D, 1, NORM> : rope_append_q8_kernel<D, kRopeHeadsQ8, NORM>,
                       dim3((unsigned)(kv_blocks + blocks)), dim3(kRopeThreads), 0, s, p, (int)kv_blocks);
+}
+
+// Rows of the 4-bit cache as bf16, gathered by slot: a thread takes eight columns of one
+// token's k and v of one head, so that a row's threads write whole 16-byte units side by side.
+// Bound by memory: 0.56 bytes in and 2 out per element.
+constexpr int kReadThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kReadThreads) read_q4_kernel(const ReadQ4Params p)
+{
+    constexpr int TPR = D / 8;   // threads per row
+    pdl_trigger();
+    pdl_wait();
+    const int64_t t = (int64_t)blockIdx.x * (kReadThreads / TPR) + threadIdx.x / TPR;
+    const int u = threadIdx.x % TPR, h = blockIdx.y;
+    if (t >= p.num_tokens)
+        return;
+    const int64_t slot = __ldg(p.slot_mapping + t);
+    if (slot < 0)
+        return;
+    if (slot >= p.num_pages << p.lg_page) {
+        if (h == 0 && u == 0)
+            set_dev_error(p.dev_err, CPSA_DEV_SLOT_OUT_OF_RANGE);
+        return;
+    }
+    const int64_t row = (((slot >> p.lg_page) * p.Hkv + h) << p.lg_page) + (slot & ((1 << p.lg_page) - 1));
+    const uint32_t kc = __ldg(reinterpret_cast<const uint32_t *>(p.k_cache + row * (D / 2)) + u);
+    const uint32_t vc = __ldg(reinterpret_cast<const uint32_t *>(p.v_cache + row * (D / 2)) + u);
+    const uint32_t ks = __ldg(p.k_scale + row * (D / kQ4Group) + (u >> 1));
+    const uint32_t vs = __ldg(p.v_scale + row * (D / kQ4Group) + (u >> 1));
+    const int64_t at = ((t * p.Hkv + h) * D) / 8 + u;
+    __stcs(reinterpret_cast<uint4 *>(p.k) + at, q4_bf16x8(kc, ks));
+    __stcs(reinterpret_cast<uint4 *>(p.v) + at, q4_bf16x8(vc, vs));
+}
+
+template <int D>
+cudaError_t launch_read_t(const ReadQ4Params &p, cudaStream_t s)
+{
+    constexpr int rows = kReadThreads / (D / 8);
+    return launch_pdl(false, read_q4_kernel<D>, dim3((unsigned)((p.num_tokens + rows - 1) / rows), (unsigned)p.Hkv),
+                      dim3(kReadThreads), 0, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_rope_append(const RopeParams &p, int head_dim, bool q8, int num_sms, cudaStream_t s)
+cudaError_t launch_rope_append(const RopeParams &p, int head_dim, int bits, int num_sms, cudaStream_t s)
 {
     if (p.num_tokens == 0)
         return cudaSuccess;
-    return head_dim == 128 ? launch_rope_t<128>(p, q8, num_sms, s) : launch_rope_t<64>(p, q8, num_sms, s);
+    const bool norm = p.k_weight != nullptr;
+    if (head_dim == 128)
+        return norm ? launch_rope_t<128, true>(p, bits, num_sms, s) : launch_rope_t<128, false>(p, bits, num_sms, s);
+    return norm ? launch_rope_t<64, true>(p, bits, num_sms, s) : launch_rope_t<64, false>(p, bits, num_sms, s);
+}
+
+cudaError_t launch_read_q4(const ReadQ4Params &p, int head_dim, cudaStream_t s)
+{
+    if (p.num_tokens == 0)
+        return cudaSuccess;
+    return head_dim == 128 ? launch_read_t<128>(p, s) : launch_read_t<64>(p, s);
 }
 
 }  // namespace cpsa

@@ -166,6 +166,83 @@ int cpp_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int6
                                uint32_t *dev_err, void *stream);
 
 /*
+ * cpp_rope_kv_cache_write into a 4-bit cache.
+ *
+ * k_cache, v_cache: codes, two to a byte, [num_pages][num_kv_heads][page_size]
+ * [head_dim / 2], the even column in the low half: sign and 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 (e2m1). k_scale, v_scale: a byte for every 16 columns of a place and head,
+ * [num_pages][num_kv_heads][page_size][head_dim / 16], 16-byte aligned: 5 bits of
+ * exponent and 3 of mantissa, no sign; byte << 7 are the bits of the f16 number that
+ * it stands for (248: infinity, above: NaN). A number is code * scale.
+ * page_size: a power of two in [8, 256].
+ *
+ * scale = amax / 6 over the group's 16 values (k after its rotation, not rounded
+ * before), to the nearest scale (ties to even), at least 2^-17, at most 10240; codes
+ * are value / scale to the nearest (ties to even), magnitudes above 6 as 6. A
+ * group that holds a NaN or an infinity gets the scale byte 255: all its numbers
+ * are NaN. Every place is written for itself: what other places hold, and in which
+ * order tokens come, does not matter. Duplicate slots within one call leave an
+ * unspecified mix of the writers' codes and scales.
+ * Everything else is cpp_rope_kv_cache_write's. (The pages have no counterpart.)
+ */
+int cpp_rope_kv_cache_write_q4(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                               int64_t max_positions, int rotary_dim, int interleaved,
+                               const int64_t *slot_mapping, int64_t num_tokens, int num_q_heads,
+                               int num_kv_heads, int head_dim, int page_size, int64_t num_pages, void *q_out,
+                               void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale,
+                               uint32_t *dev_err, void *stream);
+
+/*
+ * The rotary KV appends with head norms: before its rotation every q and k head
+ * becomes, in fp32 and without a rounding in between,
+ *   y_c = x_c / sqrt(mean_c x_c^2 + eps) * w_c   over its head_dim columns c,
+ * w = q_weight for q heads, k_weight for k heads: fp32 [head_dim], 16-byte aligned
+ * (q_weight may be NULL when num_q_heads is 0). v passes through. eps: positive and
+ * finite (else CPSA_ERR_BAD_SHAPE). Heads whose squares' sum is beyond fp32 (values
+ * from about 1e18 on) become zero, and NaN where they hold an infinity.
+ * Everything else is cpp_rope_kv_cache_write's, _q8's and _q4's: rotary_dim = 0 norms
+ * without rotating. (The pages have no counterpart.)
+ */
+int cpp_norm_rope_kv_cache_write(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                 int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                 const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                 int rotary_dim, int interleaved, const int64_t *slot_mapping, int64_t num_tokens,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                                 int64_t num_pages, void *q_out, void *k_cache, void *v_cache, uint32_t *dev_err,
+                                 void *stream);
+int cpp_norm_rope_kv_cache_write_q8(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                    const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                    int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                                    int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int64_t num_pages, void *q_out, void *k_cache, void *v_cache,
+                                    uint8_t *k_scale, uint8_t *v_scale, uint32_t *dev_err, void *stream);
+int cpp_norm_rope_kv_cache_write_q4(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                                    const int64_t *positions, const float *cos_sin, int64_t max_positions,
+                                    int rotary_dim, int interleaved, const int64_t *slot_mapping,
+                                    int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int64_t num_pages, void *q_out, void *k_cache, void *v_cache,
+                                    uint8_t *k_scale, uint8_t *v_scale, uint32_t *dev_err, void *stream);
+
+/*
+ * Rows of a 4-bit cache back as bf16 (exact for the scales that the append stores:
+ * a number of the cache has at most 6 significant bits): for each token t with s =
+ * slot_mapping[t] >= 0 and every kv head h, the numbers of place s % page_size of
+ * page s / page_size go to k[t][h][:] and v[t][h][:], bf16
+ * [num_tokens][num_kv_heads][head_dim], contiguous. A slot may come any number of
+ * times. s < 0: the token's rows are left as they were; s past the cache sets
+ * CPSA_DEV_SLOT_OUT_OF_RANGE and leaves them too. Cache, scales and sizes are
+ * cpp_rope_kv_cache_write_q4's; k and v 16-byte aligned. It serves programs that
+ * hand cached tokens on to a bf16 cache (cpp_kv_cache_write takes k and v as they
+ * are) or to another machine. (The pages have no counterpart.)
+ */
+int cpp_kv_cache_read_q4(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                         const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                         int page_size, int64_t num_pages, void *k, void *v, uint32_t *dev_err, void *stream);
+
+/*
  * Workspace for cpp_chunked_prefill_attn, in bytes.
  *
  * cpp_attn_workspace_bytes is the size that lets every row use up to
