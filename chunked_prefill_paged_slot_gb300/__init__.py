@@ -17,6 +17,8 @@ this package is its Python binding plus host-side orchestration:
                             the KV write fused into that attention call
   cpp_chunked_prefill_attn_q8
                             the attention over the 8-bit cache
+  cpp_chunked_prefill_attn_q4
+                            and over the 4-bit cache
   cpp_split_microbatch      balanced micro-batch split point
   cpp_plan_chunk_sizes      dynamic chunk planner (quadratic latency model)
   OnlineChunker             online chunk-size controller (windowed refit of f(C, H))
@@ -31,7 +33,7 @@ from ._lib import (  # noqa: F401
     cpp_rope_kv_cache_write_q4, cpp_norm_rope_kv_cache_write, cpp_norm_rope_kv_cache_write_q8,
     cpp_norm_rope_kv_cache_write_q4, cpp_kv_cache_read_q4,
     cpp_attn_workspace_bytes, cpp_attn_workspace_min_bytes,
-    cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_q8, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
+    cpp_chunked_prefill_attn, cpp_chunked_prefill_attn_q8, cpp_chunked_prefill_attn_q4, cpp_chunked_prefill_attn_events, cpp_chunked_prefill_attn_noalloc,
     cpp_noalloc_scratch_address,
     cpp_chunked_prefill_attn_write_kv,
     cpp_split_microbatch, cpp_read_device_error, cpp_get_device_error, cpp_plan_chunk_sizes,

@@ -74,6 +74,8 @@ def load():
                                              _c_p, _c_p]
     lib.cpp_chunked_prefill_attn_q8.restype = _c_int
     lib.cpp_chunked_prefill_attn_q8.argtypes = [_c_p] * 2 + lib.cpp_chunked_prefill_attn.argtypes
+    lib.cpp_chunked_prefill_attn_q4.restype = _c_int
+    lib.cpp_chunked_prefill_attn_q4.argtypes = lib.cpp_chunked_prefill_attn_q8.argtypes
     lib.cpp_chunked_prefill_attn_events.restype = _c_int
     lib.cpp_chunked_prefill_attn_events.argtypes = lib.cpp_chunked_prefill_attn.argtypes + [_c_p]
     lib.cpp_chunked_prefill_attn_write_kv.restype = _c_int
@@ -417,16 +419,31 @@ def cpp_chunked_prefill_attn_q8(q, k_cache, v_cache, k_scale, v_scale, query_len
     """cpp_chunked_prefill_attn over an 8-bit cache: caches [pages, Hkv, P, d] torch.float8_e4m3fn (or uint8),
     k_scale, v_scale [pages, Hkv, P / min(16, P)] torch.float8_e8m0fnu (or uint8), as cpp_rope_kv_cache_write_q8
     fills them; the rest as for cpp_chunked_prefill_attn."""
-    what = "cpp_chunked_prefill_attn_q8"
+    _attn_call("cpp_chunked_prefill_attn_q8", load().cpp_chunked_prefill_attn_q8, _q8_pointers, 1, q, k_cache, v_cache,
+               k_scale, v_scale, query_lens, seq_lens, block_table, out, workspace, dev_err, scale, max_kv_splits, stream)
+
+
+def cpp_chunked_prefill_attn_q4(q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table, out,
+                                workspace, dev_err, scale=0.0, max_kv_splits=8, stream=None):
+    """cpp_chunked_prefill_attn over a 4-bit cache: caches [pages, Hkv, P, d / 2] torch.float4_e2m1fn_x2 (or uint8),
+    k_scale, v_scale [pages, Hkv, P, d / 16] uint8, as cpp_rope_kv_cache_write_q4 fills them; the rest as for
+    cpp_chunked_prefill_attn."""
+    _attn_call("cpp_chunked_prefill_attn_q4", load().cpp_chunked_prefill_attn_q4, _q4_pointers, 2, q, k_cache, v_cache,
+               k_scale, v_scale, query_lens, seq_lens, block_table, out, workspace, dev_err, scale, max_kv_splits, stream)
+
+
+def _attn_call(what, fn, pointers, per_byte, q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table,
+               out, workspace, dev_err, scale, max_kv_splits, stream):
+    """Attention over a cache with scales, `per_byte` columns to a byte."""
     handle, device = _where(stream, k_cache, "k_cache")
-    caches = _q8_pointers(k_cache, v_cache, k_scale, v_scale, device)
+    caches = pointers(k_cache, v_cache, k_scale, v_scale, device)
     T, Hq, d = qshape = q.shape
     pages, Hkv, P, d2 = k_cache.shape
     B = query_lens.shape[0]
     table = block_table.shape
-    if out.shape != qshape or d2 != d or seq_lens.shape != (B,) or len(table) != 2 or table[0] != B:
+    if out.shape != qshape or d2 * per_byte != d or seq_lens.shape != (B,) or len(table) != 2 or table[0] != B:
         raise CpsaError(f"{what}: inconsistent shapes")
-    st = load().cpp_chunked_prefill_attn_q8(
+    st = fn(
         _ptr(q, _BF16, "q", device), *caches, _ptr(query_lens, _I32, "query_lens", device),
         _ptr(seq_lens, _I32, "seq_lens", device), _ptr(block_table, _I32, "block_table", device), B, T, table[1], Hq,
         Hkv, d, P, pages, float(scale), int(max_kv_splits), _ptr(out, _BF16, "out", device),

@@ -193,7 +193,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
               int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads, int num_kv_heads,
               int head_dim, int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
               void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events,
-              const uint8_t *k_scale = nullptr, const uint8_t *v_scale = nullptr);
+              const uint8_t *k_scale = nullptr, const uint8_t *v_scale = nullptr, int bits = 16);
 
 int check_attn_shape(int num_reqs, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                      int max_kv_splits)
@@ -497,7 +497,24 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
     return attn_impl(q, nullptr, nullptr, nullptr, const_cast<void *>(k_cache), const_cast<void *>(v_cache),
                      query_lens, seq_lens, block_table, num_reqs, num_tokens, max_blocks_per_req, num_q_heads,
                      num_kv_heads, head_dim, page_size, num_pages, scale, max_kv_splits, out, workspace,
-                     workspace_bytes, dev_err, stream, nullptr, k_scale, v_scale);
+                     workspace_bytes, dev_err, stream, nullptr, k_scale, v_scale, 8);
+}
+
+int cpp_chunked_prefill_attn_q4(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
+                                const int32_t *block_table, int num_reqs, int64_t num_tokens, int max_blocks_per_req,
+                                int num_q_heads, int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                float scale, int max_kv_splits, void *out, void *workspace, size_t workspace_bytes,
+                                uint32_t *dev_err, void *stream)
+{
+    if (num_tokens > 0 && (!k_scale || !v_scale))
+        return CPSA_ERR_NULL_ARG;
+    if (num_tokens > 0 && (!aligned16(k_scale) || !aligned16(v_scale)))
+        return CPSA_ERR_MISALIGNED;
+    return attn_impl(q, nullptr, nullptr, nullptr, const_cast<void *>(k_cache), const_cast<void *>(v_cache),
+                     query_lens, seq_lens, block_table, num_reqs, num_tokens, max_blocks_per_req, num_q_heads,
+                     num_kv_heads, head_dim, page_size, num_pages, scale, max_kv_splits, out, workspace,
+                     workspace_bytes, dev_err, stream, nullptr, k_scale, v_scale, 4);
 }
 
 int cpp_chunked_prefill_attn_events(const void *q, const void *k_cache, const void *v_cache,
@@ -551,17 +568,18 @@ int cpp_chunked_prefill_attn_write_kv_events(const void *q, const void *k, const
 
 namespace {
 
-// The attention call; k_scale != nullptr: over the 8-bit cache; k_new != nullptr fuses the KV write (k_new, v_new,
+// The attention call over a cache of `bits` a number (k_scale, v_scale: of 8 and 4); k_new != nullptr fuses the KV write (k_new, v_new,
 // slot_mapping non-null then).
 int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t *slot_mapping, void *k_cache,
               void *v_cache, const int32_t *query_lens, const int32_t *seq_lens, const int32_t *block_table,
               int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads, int num_kv_heads,
               int head_dim, int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
               void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream, void *const *events,
-              const uint8_t *k_scale, const uint8_t *v_scale)
+              const uint8_t *k_scale, const uint8_t *v_scale, int bits)
 {
     const bool fused = k_new != nullptr;
-    const bool q8 = k_scale != nullptr;   // the cache is e4m3 bytes with scales
+    const bool q8 = bits == 8;   // the cache is e4m3 bytes with scales
+    const bool q4 = bits == 4;   // e2m1 codes with scales
     cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
     if (events)
         for (int i = 0; i < 5; ++i)
@@ -662,7 +680,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     // compute their runs themselves, and it is the call's first kernel.
     const bool single_prefill = num_reqs == 1 && num_tokens >= 2;
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
-    const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
+    const bool self_plan = !q4 && single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
                                                             q8 ? kSelfPlanCapQ8 : kSelfPlanCap, pp.unit_cost);
     mark(0, s);
     if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
@@ -717,6 +735,13 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
                                   D * 2 * num_q_heads, 64, 1, 32)
                      ? 1
                      : 0;
+    if (q4) {
+        const Q4Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
+                        __builtin_ctz((unsigned)page_size)};
+        return launch_attn_q4_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) == cudaSuccess
+                   ? CPSA_OK
+                   : CPSA_ERR_CUDA;
+    }
     if (q8) {
         const Q8Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                         __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};

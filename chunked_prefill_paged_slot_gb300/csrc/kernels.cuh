@@ -42,6 +42,12 @@ struct Q8Cache {
     int lg_page, lg_sb;
 };
 
+// The 4-bit cache: codes [pages][Hkv][P][D / 2] and scale bytes [pages][Hkv][P][D / 16] (q4.cuh).
+struct Q4Cache {
+    const uint8_t *k, *v, *ks, *vs;
+    int lg_page;
+};
+
 struct ChunkParams : AttnCommon {
     const PrefillItem *pitems;
     const int32_t *run_first;   // CTA c processes pieces [run_first[c], run_first[c + 1])
@@ -148,6 +154,8 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
 // x heads_per_item heads (see abi.cu: make_map_q8)
 cudaError_t launch_decode_q8(const DecodeParams &p, const Q8Cache &c, const CUtensorMap &tk, const CUtensorMap &tv,
                              int head_dim, int heads_per_item, int grid, cudaStream_t s, bool early);
+cudaError_t launch_attn_q4_rows(const AttnCommon &p, const Q4Cache &c, const void *q, int head_dim, int num_reqs,
+                                int num_tokens, cudaStream_t s, bool early);
 int decode_q8_box_rows(int page_size, int heads_per_item);
 // bits: of a cache's numbers, 16 (bf16), 8 (e4m3) or 4
 cudaError_t launch_rope_append(const RopeParams &p, int head_dim, int bits, int num_sms, cudaStream_t s);

@@ -336,6 +336,28 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
                                 void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream);
 
 /*
+ * cpp_chunked_prefill_attn over a 4-bit cache, the one that cpp_rope_kv_cache_write_q4
+ * fills: k_cache, v_cache codes [num_pages][num_kv_heads][page_size][head_dim / 2],
+ * k_scale, v_scale bytes [num_pages][num_kv_heads][page_size][head_dim / 16], 16-byte
+ * aligned. Places behind a sequence's end may hold anything. A NaN key makes the rows
+ * that see it NaN, a NaN value its 16 columns (and it may do so for those columns of
+ * earlier rows of the same chunk). Scale bytes above 226 (10240), which the append stores
+ * for NaN alone, stand for numbers that f16 may not hold: infinities and NaN may come of
+ * them. (The pages have no counterpart.)
+ * Every other argument, the workspace (same size functions), the device flags, CUDA
+ * graph capture and the splits are cpp_chunked_prefill_attn_q8's.
+ * Arithmetic: stored numbers enter the MMAs as f16, exact; q rows as f16 under a power of
+ * two of their own; probabilities in f16; partial results of a chunk's split units in
+ * bf16, as in cpp_chunked_prefill_attn; everything else in fp32.
+ */
+int cpp_chunked_prefill_attn_q4(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                const uint8_t *v_scale, const int32_t *query_lens, const int32_t *seq_lens,
+                                const int32_t *block_table, int num_reqs, int64_t num_tokens,
+                                int max_blocks_per_req, int num_q_heads, int num_kv_heads, int head_dim,
+                                int page_size, int64_t num_pages, float scale, int max_kv_splits, void *out,
+                                void *workspace, size_t workspace_bytes, uint32_t *dev_err, void *stream);
+
+/*
  * cpp_chunked_prefill_attn with timing marks: when `events` is not NULL it
  * points to 5 cudaEvent_t handles (any may be NULL) recorded on `stream`:
  * [0] before the plan kernel (when one runs), [1] before the chunk kernel, [2] after it,

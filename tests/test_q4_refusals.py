@@ -97,3 +97,37 @@ def test_bindings_refuse_host_tensors_and_wrong_shapes():
         cpsa.cpp_norm_rope_kv_cache_write(None, x, x[:2], None, w, None, None, slots, wide, wide, None, err)
     with pytest.raises(cpsa.CpsaError, match="CUDA tensor"):
         cpsa.cpp_kv_cache_read_q4(*held, slots, x, x, err)
+
+
+def attn(**over):
+    a = dict(q=A, kc=A, vc=A, ks=A, vs=A, ql=A, sl=A, bt=A, B=2, T=5, M=4, Hq=4, Hkv=2, d=64, P=16, pages=8, scale=0.0,
+             splits=8, out=A, ws=A, wsb=1 << 30, err=A, stream=None)
+    assert set(over) <= set(a), over
+    a.update(over)
+    return cpsa.load().cpp_chunked_prefill_attn_q4(*a.values())
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(ks=None), NULL), (dict(vs=None), NULL), (dict(q=None), NULL), (dict(kc=None), NULL), (dict(vc=None), NULL),
+    (dict(ql=None), NULL), (dict(sl=None), NULL), (dict(bt=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
+    (dict(err=None), NULL), (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(B=0), SHAPE), (dict(M=-1), SHAPE),
+    (dict(pages=-1), SHAPE), (dict(pages=1 << 40), SHAPE), (dict(splits=0), SHAPE), (dict(splits=33), SHAPE),
+    (dict(q=A + 8), ALIGN), (dict(kc=A + 8), ALIGN), (dict(vc=A + 8), ALIGN), (dict(ks=A + 8), ALIGN), (dict(vs=A + 4), ALIGN),
+    (dict(out=A + 2), ALIGN), (dict(ws=A + 4), ALIGN), (dict(d=96), UNSUP), (dict(P=4), UNSUP), (dict(P=24), UNSUP),
+    (dict(P=512), UNSUP), (dict(Hq=5), UNSUP), (dict(Hq=34), UNSUP), (dict(wsb=100), -5)], ids=str)
+def test_attention_refuses(over, status):
+    assert attn(**over) == status
+
+
+def test_empty_attention():
+    assert attn(T=0, B=0, q=None, ks=None, vs=None) == OK
+    if not torch.cuda.is_available():
+        assert attn() == NODEV
+
+
+def test_attention_binding_refuses_wrong_types():
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    c, sc = torch.zeros(2, 2, 16, 32, dtype=torch.uint8), torch.zeros(2, 2, 16, 4, dtype=torch.uint8)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(cpsa.CpsaError, match="k_cache must be"):
+        cpsa.cpp_chunked_prefill_attn_q4(q, c, c, sc, sc, i, i, i.view(1, 1), q, c.view(-1), i)
