@@ -154,6 +154,39 @@ bool make_map_q8(CUtensorMap *m, const void *base, int head_dim, int page_size, 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The 4-bit cache's four maps for its decode kernel: codes [pages][Hkv][P][D / 2], rows of 64
+// bytes (D 128) swizzled over themselves, rows of 32 as they are; scales [pages][Hkv][P][D / 16],
+// a head's rows of a page as one row of words. Boxes of `rows` rows of `heads` heads.
+bool make_maps_q4(Q4Maps *m, const Q4Cache &c, int head_dim, int page_size, int num_kv_heads, int64_t num_pages,
+                  uint32_t rows, uint32_t heads)
+{
+    auto enc = encode_fn();
+    if (!enc)
+        return false;
+    const uint64_t row = (uint64_t)head_dim / 2, sc_row = (uint64_t)head_dim / 16;
+    auto codes = [&](CUtensorMap *t, const void *base) {
+        const uint64_t head_bytes = row * (uint64_t)page_size;
+        cuuint64_t dims[4] = {row, (cuuint64_t)page_size, (cuuint64_t)num_kv_heads, (cuuint64_t)num_pages};
+        cuuint64_t strides[3] = {row, head_bytes, head_bytes * (uint64_t)num_kv_heads};
+        cuuint32_t box[4] = {(cuuint32_t)row, rows, heads, 1};
+        cuuint32_t estr[4] = {1, 1, 1, 1};
+        return enc(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    auto scales = [&](CUtensorMap *t, const void *base) {
+        const uint64_t head_bytes = sc_row * (uint64_t)page_size;
+        cuuint64_t dims[3] = {head_bytes / 4, (cuuint64_t)num_kv_heads, (cuuint64_t)num_pages};
+        cuuint64_t strides[2] = {head_bytes, head_bytes * (uint64_t)num_kv_heads};
+        cuuint32_t box[3] = {(cuuint32_t)(rows * sc_row / 4), heads, 1};
+        cuuint32_t estr[3] = {1, 1, 1};
+        return enc(t, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return codes(&m->k, c.k) && codes(&m->v, c.v) && scales(&m->ks, c.ks) && scales(&m->vs, c.vs);
+}
+
 int nq_for_group(int group) { return (group % 2 == 0) ? 2 : 1; }
 
 // Every attention call gets its own nonzero epoch: the merge counters it leaves
@@ -580,6 +613,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     const bool fused = k_new != nullptr;
     const bool q8 = bits == 8;   // the cache is e4m3 bytes with scales
     const bool q4 = bits == 4;   // e2m1 codes with scales
+    const bool scaled = q8 || q4;
     cudaEvent_t ev[5] = {nullptr, nullptr, nullptr, nullptr, nullptr};
     if (events)
         for (int i = 0; i < 5; ++i)
@@ -650,11 +684,11 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.group = group;
     pp.nq = nq;
     pp.max_splits = max_kv_splits;
-    const int dec_heads = q8 ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
+    const int dec_heads = scaled ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
-    pp.unit_cost = q8 ? unit_cost_q8(head_dim) : kUnitCostTiles;
+    pp.unit_cost = scaled ? unit_cost_q8(head_dim) : kUnitCostTiles;
     pp.dec_keys = dec_heads > 1 ? kDecodeKeysPerSplitGrouped : kDecodeKeysPerSplit;
-    if (q8) {
+    if (scaled) {
         const int64_t items = (num_reqs < num_tokens ? num_reqs : num_tokens) * (num_kv_heads / dec_heads);
         pp.dec_keys = 2 * items >= sms   ? kDecodeKeysPerSplitGrouped
                       : 8 * items > sms ? kDecodeKeysPerSplitQ8Few
@@ -680,8 +714,8 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     // compute their runs themselves, and it is the call's first kernel.
     const bool single_prefill = num_reqs == 1 && num_tokens >= 2;
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
-    const bool self_plan = !q4 && single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
-                                                            q8 ? kSelfPlanCapQ8 : kSelfPlanCap, pp.unit_cost);
+    const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
+                                                            scaled ? kSelfPlanCapQ8 : kSelfPlanCap, pp.unit_cost);
     mark(0, s);
     if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
         return CPSA_ERR_CUDA;
@@ -735,27 +769,15 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
                                   D * 2 * num_q_heads, 64, 1, 32)
                      ? 1
                      : 0;
-    if (q4) {
-        const Q4Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
-                        __builtin_ctz((unsigned)page_size)};
-        return launch_attn_q4_rows(ac, c, q, head_dim, num_reqs, (int)num_tokens, s, early) == cudaSuccess
-                   ? CPSA_OK
-                   : CPSA_ERR_CUDA;
-    }
-    if (q8) {
+    if (scaled) {
         const Q8Cache c{static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale, v_scale,
                         __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};
         cp.q = q;
         cp.q8 = c;
-        if (!single_decode &&
-            launch_chunk_q8(cp, to, head_dim, nq, pp.chunk_grid, s, early && !self_plan) != cudaSuccess)
+        if (!single_decode && (q4 ? launch_chunk_q4 : launch_chunk_q8)(cp, to, head_dim, nq, pp.chunk_grid, s,
+                                                                       early && !self_plan) != cudaSuccess)
             return CPSA_ERR_CUDA;
         if (!single_prefill) {
-            CUtensorMap tk, tv;
-            const uint32_t rows = (uint32_t)decode_q8_box_rows(page_size, dec_heads);
-            if (!make_map_q8(&tk, k_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||
-                !make_map_q8(&tv, v_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads))
-                return CPSA_ERR_CUDA;
             DecodeParams dp;
             static_cast<AttnCommon &>(dp) = ac;
             dp.ditems = ditems;
@@ -763,8 +785,20 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             dp.k_cache_ptr = k_cache;
             dp.v_cache_ptr = v_cache;
             const int grid_d = (int)(L.max_ditems < sms ? L.max_ditems : sms);
-            if (launch_decode_q8(dp, c, tk, tv, head_dim, dec_heads, grid_d, s, early) != cudaSuccess)
+            CUtensorMap tk, tv;
+            Q4Maps maps;
+            const Q4Cache c4{c.k, c.v, c.ks, c.vs, c.lg_page};
+            const uint32_t rows = (uint32_t)decode_q8_box_rows(page_size, dec_heads);
+            if (q4) {
+                if (!make_maps_q4(&maps, c4, head_dim, page_size, num_kv_heads, num_pages,
+                                  (uint32_t)decode_q4_box_rows(page_size, dec_heads, group), (uint32_t)dec_heads) ||
+                    launch_decode_q4(dp, c4, maps, head_dim, dec_heads, grid_d, s, early) != cudaSuccess)
+                    return CPSA_ERR_CUDA;
+            } else if (!make_map_q8(&tk, k_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||
+                       !make_map_q8(&tv, v_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||
+                       launch_decode_q8(dp, c, tk, tv, head_dim, dec_heads, grid_d, s, early) != cudaSuccess) {
                 return CPSA_ERR_CUDA;
+            }
             if (cap > 0) {
                 CombineParams cb{counts, citems, part_o, part_ml, out, num_q_heads};
                 if (launch_combine(cb, head_dim, 4 * sms, s, early) != cudaSuccess)

@@ -66,7 +66,7 @@ struct ChunkParams : AttnCommon {
     int split_clamped;          // self-planned batch: splits were asked for but the partials do not fit
     int out_tma;                // head_dim 128, `out` mapped for TMA stores (whole units' rows without the KV
                                 // write, merged rows at the end of a run)
-    // over the 8-bit cache (launch_chunk_q8) only
+    // over the 8-bit and 4-bit caches (launch_chunk_q8, launch_chunk_q4) only
     const void *q;              // bf16 [T][Hq][D]
     Q8Cache q8;
 };
@@ -137,6 +137,9 @@ cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const
 // the chunk kernel over the 8-bit cache (p.q, p.q8)
 cudaError_t launch_chunk_q8(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
                             cudaStream_t s, bool early);
+// and over the 4-bit cache (p.q, p.q8; lg_sb not used)
+cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
+                            cudaStream_t s, bool early);
 cudaError_t launch_decode_attn(const DecodeParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int head_dim,
                                int grid, cudaStream_t s, bool early);
 // the grouped decode kernel: items of heads_per_item (4 or 8) kv heads; tk / tv
@@ -154,10 +157,17 @@ cudaError_t launch_kv_cache_write(const void *k, const void *v, const int64_t *s
 // x heads_per_item heads (see abi.cu: make_map_q8)
 cudaError_t launch_decode_q8(const DecodeParams &p, const Q8Cache &c, const CUtensorMap &tk, const CUtensorMap &tv,
                              int head_dim, int heads_per_item, int grid, cudaStream_t s, bool early);
-cudaError_t launch_attn_q4_rows(const AttnCommon &p, const Q4Cache &c, const void *q, int head_dim, int num_reqs,
-                                int num_tokens, cudaStream_t s, bool early);
 int decode_q8_box_rows(int page_size, int heads_per_item);
 // bits: of a cache's numbers, 16 (bf16), 8 (e4m3) or 4
+// decode rows over the 4-bit cache; maps: codes as [D / 2 bytes][P][Hkv][pages] in boxes of
+// decode_q4_box_rows rows x heads_per_item heads, scales as [P rows' bytes][Hkv][pages] in
+// boxes of the same rows and heads (see abi.cu: make_maps_q4)
+struct Q4Maps {
+    CUtensorMap k, v, ks, vs;
+};
+cudaError_t launch_decode_q4(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, int head_dim,
+                             int heads_per_item, int grid, cudaStream_t s, bool early);
+int decode_q4_box_rows(int page_size, int heads_per_item, int group);
 cudaError_t launch_rope_append(const RopeParams &p, int head_dim, int bits, int num_sms, cudaStream_t s);
 cudaError_t launch_read_q4(const ReadQ4Params &p, int head_dim, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,

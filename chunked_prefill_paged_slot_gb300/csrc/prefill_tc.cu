@@ -48,6 +48,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "plan.cuh"
+#include "q4.cuh"
 #include "q8.cuh"
 
 namespace cpsa {
@@ -67,10 +68,12 @@ constexpr int kMergeMaxOthers = 3;
 constexpr int kMergeStageBytes = kMergeMaxOthers * 32 * 128 * 2;
 
 constexpr int kQ8Stages = 2;   // e4m3 tiles on their way (see q8_convert)
+constexpr int kQ4Stages = 3;   // 4-bit tiles
 
 // Over the 8-bit cache the kernel has another cast of warps (see chunk_attn_kernel)
-// and keeps a little more in shared memory, so fewer self-planned pieces.
-template <int D, int NQ, bool Q8 = false>
+// and keeps a little more in shared memory, so fewer self-planned pieces. Q8 && Q4: over
+// the 4-bit cache, the same cast.
+template <int D, int NQ, bool Q8 = false, bool Q4 = false>
 struct ChunkCfg {
     static constexpr int kHalves = D / 64;             // 128-byte swizzle atoms across a row
     static constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16
@@ -80,7 +83,11 @@ struct ChunkCfg {
     static constexpr int kSlotOff = NQ * kTileBytes;
     static constexpr int kStageOff = kSlotOff + kSlots * kTileBytes;   // the cache writer's buffer; rows on their way out
     static constexpr int kQ8StageOff = kStageOff + kTileBytes;         // Q8: e4m3 tiles
-    static constexpr int kBarOff = kStageOff + kTileBytes + (Q8 ? kQ8Stages * 128 * D : 0);
+    // a tile on its way: 128 rows of bytes, or of codes and then of scales
+    static constexpr int kRawStages = Q4 ? kQ4Stages : kQ8Stages;
+    static constexpr int kRawCodes = Q4 ? 128 * D / 2 : 128 * D;
+    static constexpr int kRawBytes = kRawCodes + (Q4 ? 128 * D / kQ4Group : 0);
+    static constexpr int kBarOff = (kStageOff + kTileBytes + (Q8 ? kRawStages * kRawBytes : 0) + 1023) / 1024 * 1024;
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
     static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
     static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
@@ -121,7 +128,7 @@ struct ChunkBars {
 struct Q8Tiles {
     int kx[8], vx[8];
     int8_t qe[2][256];
-    uint64_t full[kQ8Stages], empty[kQ8Stages];   // e4m3 half-tiles: landed, converted
+    uint64_t full[4], empty[4];   // half-tiles on their way: landed, converted
     struct {
         int8_t ek[16], ev[16];   // per group of eight keys: its factor's exponent
         uint32_t there;          // bit l: group l is loaded
@@ -786,12 +793,104 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
     mbar_drain(q8t->full, half, kQ8Stages);
 }
 
+// The 4-bit cache's loader: pages looked up two tiles ahead, a tile's codes and scales by
+// bulk copies, all rows of a page at once, kQ4Stages half-tiles ahead. Its numbers are exact
+// in f16 (q4.cuh): no exponents to be told to anyone, only which groups are there.
 template <int D, int NQ>
+__device__ __forceinline__ void q4_load(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+                                        const PrefillItem *items, int it_begin, int it_end, int lane)
+{
+    using C = ChunkCfg<D, NQ, true, true>;
+    constexpr uint32_t kRow = D / 2, kScRow = D / kQ4Group;
+    volatile int *abort = &bars->abort;
+    const int lg_page = p.q8.lg_page, pmask = p.page_size - 1;
+    // lane l stands for the group of rows 8 l .. of a tile; the first of a page copies all
+    // that follow in the page and tile
+    const int key_l = 8 * (lane & 15);
+    const bool copier = lane < 16 && (lane == 0 || (key_l & pmask) == 0);
+    const uint32_t copy_rows = (uint32_t)(min(128, (key_l | pmask) + 1) - key_l);
+    uint8_t *stages = smem + C::kQ8StageOff;
+    uint32_t half = 0, tile = 0;   // half-tiles and tiles issued
+    bool ok = true;
+    for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
+        const PrefillItem w = items[it];
+        const int kvh = w.kvh_hp & 0xFFFF;
+        const int s_len = p.seq_lens[w.r];
+        const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
+        // the page of this lane's group in tile kt as it stands in the table, -1 where there is none
+        auto page_of = [&](int kt) -> int {
+            const int key = kt * 128 + key_l;
+            return kt < w.kt1 && key < s_len ? ldg_here(bt_row + (key >> lg_page)) : -1;
+        };
+        int pg0 = page_of(w.kt0), pg1 = page_of(w.kt0 + 1);
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++tile) {
+            const int pg2 = page_of(kt + 2);
+            const bool mine = pg0 >= 0 && pg0 < p.num_pages;
+            if (!mine && kt * 128 + key_l < s_len)
+                set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+            const uint32_t there = __ballot_sync(0xffffffffu, mine) & 0xffffu;
+            const int64_t row = (((int64_t)pg0 * p.num_kv_heads + kvh) << lg_page) + ((kt * 128 + key_l) & pmask);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ++half) {
+                const int st = half % C::kRawStages;
+                if (half >= (uint32_t)C::kRawStages &&
+                    !mbar_wait_warp(&q8t->empty[st], ((half / C::kRawStages) - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                // after the wait: the tile four before, whose entry this is, is converted
+                if (kv == 0 && lane == 16)
+                    q8t->tile[tile & 3].there = there;
+                __syncwarp();
+                // each lane announces its own copies' bytes right before it issues them
+                if (copier) {
+                    if (mine) {
+                        mbar_arrive_expect_tx(&q8t->full[st], copy_rows * (kRow + kScRow));
+                        uint8_t *dst = stages + st * C::kRawBytes;
+                        bulk_load(dst + key_l * kRow, (kv == 0 ? p.q8.k : p.q8.v) + row * kRow, copy_rows * kRow,
+                                  &q8t->full[st]);
+                        bulk_load(dst + C::kRawCodes + key_l * kScRow, (kv == 0 ? p.q8.ks : p.q8.vs) + row * kScRow,
+                                  copy_rows * kScRow, &q8t->full[st]);
+                    } else {
+                        mbar_arrive(&q8t->full[st]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok)
+                break;
+            pg0 = pg1;
+            pg1 = pg2;
+        }
+    }
+    mbar_drain(q8t->full, half, C::kRawStages);
+}
+
+// This thread's 32 columns of a row of the 4-bit cache, two groups, from a load of codes
+// and one of scale bytes to four chunks of a row of the f16 tile at `dst` + off[].
+__device__ __forceinline__ void q4_convert_row(const uint4 &v, uint32_t scales, uint32_t dst, const uint32_t (&off)[4])
+{
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t f0 = q4_scale2(scales & 0xffu), f1 = q4_scale2(scales >> 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t y[4];
+        e2m1x8(x[j], y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = q4_mul(y[i], j < 2 ? f0 : f1);
+        sts128(dst + off[j], make_uint4(y[0], y[1], y[2], y[3]));
+    }
+}
+
+// Q4: the 4-bit cache's tiles instead. A thread takes 32 columns of a row (two groups) at a
+// time: one load, one of the two scale bytes, sixteen conversions and multiplications, four
+// stores; eight threads in a row (of the warp) store to eight different 16-byte banks.
+template <int D, int NQ, bool Q4 = false>
 __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
                                            const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
                                            int lane)
 {
-    using C = ChunkCfg<D, NQ, true>;
+    using C = ChunkCfg<D, NQ, true, Q4>;
     constexpr int kGroups = 16 / C::kConverters;   // groups of eight rows per warp
     constexpr int RPW = 512 / D;                   // rows per warp and pass: 4 or 8
     constexpr int NP = 8 / RPW;                    // passes per group
@@ -812,6 +911,13 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         off0[q] = f16_chunk_off(r0 + RPW * q, 2 * c);
         off1[q] = f16_chunk_off(r0 + RPW * q, 2 * c + 1);
     }
+    // Q4: this thread's row within a pass of 1024 / D rows and its 32 columns 32 c4 ..
+    const int r4 = D == 128 ? (lane & 3) | (lane >> 2 & 4) : (lane & 3) | (lane >> 1 & 12);
+    const int c4 = D == 128 ? lane >> 2 & 3 : lane >> 2 & 1;
+    constexpr int kPass = 1024 / D;
+    uint32_t off4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off4[j] = f16_chunk_off(r4, 4 * c4 + j);
     uint32_t q_uses = 0, half = 0, tile = 0;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return mbar_wait_warp(bar, parity, abort);
@@ -881,9 +987,9 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                 // Q after the first K tile, whose slot frees earlier than Q's buffer
                 if (kt == w.kt0 && kv == 1 && !(ok = convert_q()))
                     break;
-                const int st = half % kQ8Stages;
+                const int st = half % C::kRawStages;
                 const int slot = half % C::kSlots;
-                ok = wait(&q8t->full[st], (half / kQ8Stages) & 1);
+                ok = wait(&q8t->full[st], (half / C::kRawStages) & 1);
                 if (!ok)
                     break;
                 const auto &e = q8t->tile[tile & 3];
@@ -894,8 +1000,32 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                     if (!ok)
                         break;
                 }
-                const uint32_t src = src0 + st * (128 * D);
                 const uint32_t dst = dst0 + slot * C::kTileBytes;
+                if constexpr (Q4) {
+                    const uint32_t raw = smem_u32(smem + C::kQ8StageOff) + st * C::kRawBytes;
+#pragma unroll 1
+                    for (int x = 0; x < 8 * kGroups / kPass; ++x) {
+                        const int in_warp = x * kPass + r4, row = 8 * g0 + in_warp;
+                        uint4 v = lds128(raw + row * (D / 2) + 16 * c4);
+                        uint32_t sc = lds_u16(raw + C::kRawCodes + row * (D / kQ4Group) + 2 * c4);
+                        if (nlive < 128 || there != 0xffffu) {
+                            if (row >= nlive || !((there >> (row >> 3)) & 1u)) {
+                                v = make_uint4(0, 0, 0, 0);
+                                sc = 0;
+                            }
+                        }
+                        q4_convert_row(v, sc, dst + x * kPass * 128, off4);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars->slot_full[slot]);
+                        mbar_arrive(&q8t->empty[st]);
+                    }
+                    ++half;
+                    continue;
+                }
+                const uint32_t src = src0 + st * C::kRawBytes;
                 // One group at a time: with the softmax and the MMA issuer unrolled as they are,
                 // instruction fetch is what runs short. On an otherwise idle SM six groups (a warp's
                 // share of a tile among three converters) take 890 clocks this way and 645 by twos,
@@ -972,14 +1102,15 @@ __device__ __noinline__ void scale_o_row(uint32_t tO, float f)
 // 1 / l. Measured on 512 tokens at history 32256 (32/8 heads, D 128): three converter
 // warps in 384 threads of 168 registers 254 us, four this way 237 us, four in 416
 // threads (128 registers, 0.6 KB of spills) 468 us.
-template <int D, int NQ, bool SELF, bool Q8>
+// Q8 && Q4: over the 4-bit cache, the same cast; its K and V operands are the very numbers.
+template <int D, int NQ, bool SELF, bool Q8, bool Q4 = false>
 __global__ void __launch_bounds__(Q8 ? 512 : 352, 1)
 chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                   const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_v4)
 {
-    using C = ChunkCfg<D, NQ, Q8>;
+    using C = ChunkCfg<D, NQ, Q8, Q4>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
@@ -1002,7 +1133,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         }
         if (Q8) {
             Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
-            for (int s = 0; s < kQ8Stages; ++s) {
+            for (int s = 0; s < C::kRawStages; ++s) {
                 mbar_init(&q8t->full[s], (uint32_t)(128 / (p.page_size < 128 ? p.page_size : 128)));   // one per copy
                 mbar_init(&q8t->empty[s], C::kConverters);
             }
@@ -1068,7 +1199,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     if (Q8 && warp >= C::kLoadWarp && warp < C::kLoadWarp + C::kConverters) {
         if constexpr (Q8) {
             regs_keep_96();
-            q8_convert<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, SELF, warp - C::kLoadWarp, lane);
+            q8_convert<D, NQ, Q4>(p, smem, bars, q8t, items, it_begin, it_end, SELF, warp - C::kLoadWarp, lane);
         }
     } else if (!Q8 && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ producer
@@ -1354,13 +1485,15 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     const volatile Q8Tiles *qt = q8t;
                     // (the lift with the q row's exponent: the K tile's may be the smallest there is)
                     if (t == 0)
-                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]) * exp2i(-kQ8Lift);
+                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]) * (Q4 ? 1.f : exp2i(-kQ8Lift));
                     // never 0 or infinite: a masked score times it stays -inf, a zero one 0
-                    tsl2 = fminf(fmaxf(q_sl2 * exp2i(qt->kx[s_uses & 7]), 1.2e-38f), 3.0e38f);
-                    const int x = qt->vx[s_uses & 7];
-                    if (t > 0)
-                        xs = exp2i(max(vx - x, -126));
-                    vx = x;
+                    tsl2 = fminf(fmaxf(Q4 ? q_sl2 : q_sl2 * exp2i(qt->kx[s_uses & 7]), 1.2e-38f), 3.0e38f);
+                    if constexpr (!Q4) {
+                        const int x = qt->vx[s_uses & 7];
+                        if (t > 0)
+                            xs = exp2i(max(vx - x, -126));
+                        vx = x;
+                    }
                 }
                 ++s_uses;
                 tc_fence_after_sync();
@@ -1396,7 +1529,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     l *= alpha;
                     m_use = m_tile;
                 }
-                if constexpr (Q8) {
+                if constexpr (Q8 && !Q4) {
                     alpha *= xs;                          // O under the tile's value exponent
                     need = need || xs != 1.f;
                 }
@@ -1473,7 +1606,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             const int64_t t_row = (int64_t)row0(w.r) + i;
             const int npieces = w.piece_np >> 16;
             float own_f = 1.f;
-            if constexpr (Q8) {
+            if constexpr (Q8 && !Q4) {
                 // O stands for O * 2^(vx - kQ8Lift). Where this and 1 / l together could leave the
                 // normal numbers and lose digits (values below 2^-44), O takes a part of it first
                 int e = vx - kQ8Lift;
@@ -1670,8 +1803,12 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             regs_keep_96();
         if (Q8 && warp != C::kMmaWarp) {
             if constexpr (Q8) {
-                if (warp == C::kQ8LoadWarp)
-                    q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+                if (warp == C::kQ8LoadWarp) {
+                    if constexpr (Q4)
+                        q4_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+                    else
+                        q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+                }
             }
         } else {
             // ------------------------------------------------------------ MMA issuer
@@ -1818,6 +1955,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     }
 }
 
+#ifndef CPSA_CHUNK_Q4   // prefill_q4.cu compiles the kernel over the 4-bit cache
 template <int D, int NQ>
 cudaError_t launch_chunk_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                            const CUtensorMap &tv, const CUtensorMap &tkn, const CUtensorMap &tvn,
@@ -1867,5 +2005,29 @@ cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const
     return nq == 2 ? launch_chunk_t<64, 2>(p, tq, tk, tv, tkn, tvn, to, tv4, grid, s, early)
                    : launch_chunk_t<64, 1>(p, tq, tk, tv, tkn, tvn, to, tv4, grid, s, early);
 }
+#else
+template <int D, int NQ>
+cudaError_t launch_chunk_q4_t(const ChunkParams &p, const CUtensorMap &to, int grid, cudaStream_t s, bool early)
+{
+    using C = ChunkCfg<D, NQ, true, true>;
+    static std::atomic<uint64_t> done_self{0}, done_plan{0};
+    auto k = p.self_plan ? chunk_attn_kernel<D, NQ, true, true, true> : chunk_attn_kernel<D, NQ, false, true, true>;
+    return launch_with_smem(p.self_plan ? done_self : done_plan, reinterpret_cast<const void *>(k), C::kSmemBytes,
+                            [&] {
+                                return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, to,
+                                                  to, to, to, to, to, to);
+                            });
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
+                            cudaStream_t s, bool early)
+{
+    if (head_dim == 128)
+        return nq == 2 ? launch_chunk_q4_t<128, 2>(p, to, grid, s, early) : launch_chunk_q4_t<128, 1>(p, to, grid, s, early);
+    return nq == 2 ? launch_chunk_q4_t<64, 2>(p, to, grid, s, early) : launch_chunk_q4_t<64, 1>(p, to, grid, s, early);
+}
+#endif
 
 }  // namespace cpsa

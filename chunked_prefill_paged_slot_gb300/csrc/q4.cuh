@@ -81,6 +81,13 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4])
         : "r"(w));
 }
 
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
 // A scale byte as an f16 pair.
 __device__ __forceinline__ uint32_t q4_scale2(uint32_t byte) { return byte * 0x00800080u; }
 
