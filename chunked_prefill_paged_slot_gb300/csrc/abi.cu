@@ -684,6 +684,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.group = group;
     pp.nq = nq;
     pp.max_splits = max_kv_splits;
+    pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
     const int dec_heads = scaled ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
     pp.unit_cost = scaled ? unit_cost_q8(head_dim) : kUnitCostTiles;
@@ -693,8 +694,10 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
         pp.dec_keys = 2 * items >= sms   ? kDecodeKeysPerSplitGrouped
                       : 8 * items > sms ? kDecodeKeysPerSplitQ8Few
                                         : kDecodeKeysPerSplitQ8Fewest;
+        pp.dec_stream = q4 && 2 * items >= sms ? 1 : 0;
+        pp.dec_grid = (int)(L.max_ditems < pp.chunk_grid ? L.max_ditems : pp.chunk_grid);
+        pp.dec_first = reinterpret_cast<int32_t *>(ws + L.off_dec_runs);
     }
-    pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
     pp.fused = fused ? 1 : 0;
     pp.prow_capacity = cap;
     pp.counts = counts;
@@ -784,7 +787,8 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             dp.q = q;
             dp.k_cache_ptr = k_cache;
             dp.v_cache_ptr = v_cache;
-            const int grid_d = (int)(L.max_ditems < sms ? L.max_ditems : sms);
+            dp.run_first = pp.dec_stream ? pp.dec_first : nullptr;
+            const int grid_d = pp.dec_stream ? pp.dec_grid : (int)(L.max_ditems < sms ? L.max_ditems : sms);
             CUtensorMap tk, tv;
             Q4Maps maps;
             const Q4Cache c4{c.k, c.v, c.ks, c.vs, c.lg_page};
@@ -852,6 +856,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     DecodeParams dp;
     static_cast<AttnCommon &>(dp) = ac;
     dp.ditems = ditems;
+    dp.run_first = nullptr;
     dp.q = q;
     dp.k_cache_ptr = k_cache;
     dp.v_cache_ptr = v_cache;

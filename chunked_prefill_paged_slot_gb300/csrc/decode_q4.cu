@@ -147,7 +147,11 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
     }
     pdl_trigger();
     pdl_wait();
-    const int n_items = p.counts[kCntDecode];
+    // this CTA's items: a run of the plan's list, or every gridDim.x-th
+    const bool runs = p.run_first != nullptr;
+    const int it_begin = runs ? p.run_first[blockIdx.x] : blockIdx.x;
+    const int it_end = runs ? p.run_first[blockIdx.x + 1] : p.counts[kCntDecode];
+    const int it_step = runs ? 1 : gridDim.x;
     __syncthreads();
     volatile int *abort = &bars->abort;
     // rows per box: within a page, and on the 64-key grid that items start on
@@ -168,12 +172,12 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
         uint32_t g = 0;
         bool stop = false;
         DecodeItem w_next{};
-        if (blockIdx.x < n_items)
-            w_next = p.ditems[blockIdx.x];
-        for (int it = blockIdx.x; it < n_items && !stop && !warp_aborted(abort); it += gridDim.x) {
+        if (it_begin < it_end)
+            w_next = p.ditems[it_begin];
+        for (int it = it_begin; it < it_end && !stop && !warp_aborted(abort); it += it_step) {
             const DecodeItem w = w_next;
-            if (it + (int)gridDim.x < n_items)
-                w_next = p.ditems[it + gridDim.x];
+            if (it + it_step < it_end)
+                w_next = p.ditems[it + it_step];
             const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
             const int head0 = w.kvh * HG;
             const int nst = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
@@ -248,7 +252,7 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
     const uint32_t vs_piece = D == 128 ? vpiece : vpiece >> 1;
     const uint32_t vs_off0 = vkey0 * C::kScRow + vs_piece, vs_off1 = vkey1 * C::kScRow + vs_piece;
     uint32_t gs = 0;
-    for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+    for (int it = it_begin; it < it_end; it += it_step) {
         const DecodeItem w = p.ditems[it];
         const int nst = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
         const int kvh = w.kvh * HG + h;

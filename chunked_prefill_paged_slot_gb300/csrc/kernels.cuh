@@ -73,6 +73,7 @@ struct ChunkParams : AttnCommon {
 
 struct DecodeParams : AttnCommon {
     const DecodeItem *ditems;
+    const int32_t *run_first;  // CTA c's items are [run_first[c], run_first[c + 1]) (4-bit cache only); nullptr: dealt round
     const void *q;             // bf16 [T][Hq][D]
     const void *k_cache_ptr;   // bf16 [pages][Hkv][P][D]
     const void *v_cache_ptr;

@@ -35,15 +35,17 @@ struct Req {
     int q, s, hist;
 };
 
-__device__ Req load_req(const PlanParams &p, int r)
+__device__ Req make_req(const PlanParams &p, int query_len, int seq_len)
 {
     Req q;
-    q.q = p.query_lens[r];
-    q.s = p.seq_lens[r];
+    q.q = query_len;
+    q.s = seq_len;
     q.valid = !(q.q < 0 || q.s < q.q) && (int64_t)q.s <= (int64_t)p.max_blocks * p.page_size;
     q.hist = q.s - q.q;
     return q;
 }
+
+__device__ Req load_req(const PlanParams &p, int r) { return make_req(p, p.query_lens[r], p.seq_lens[r]); }
 
 // KV tiles of one unit of query tile qt (rows [128 qt, 128 qt + rows)); see the
 // tile grids in plan.cuh.
@@ -58,11 +60,10 @@ __device__ int prefill_tiles(const PlanParams &p, const Req &rq)
 {
     if (!rq.valid || rq.q < 2)
         return 0;
-    const int units_per_qtile = p.Hkv * (p.group / p.nq);
-    int tiles = 0;
-    for (int qt = 0; qt * kTileM < rq.q; ++qt)
-        tiles += (unit_tiles(p, rq, qt, min(kTileM, rq.q - qt * kTileM)) + p.unit_cost) * units_per_qtile;
-    return tiles;
+    // query tile qt has hb + qt + 1 tiles, but for the last, which may be short
+    const int nqt = ceil_div(rq.q, kTileM), hb = ceil_div(rq.hist, kTileN);
+    const int last = unit_tiles(p, rq, nqt - 1, rq.q - (nqt - 1) * kTileM);
+    return p.Hkv * (p.group / p.nq) * (last + (nqt - 1) * (hb + 1) + (nqt - 1) * (nqt - 2) / 2 + nqt * p.unit_cost);
 }
 
 // Positions of the request's longest unit (its last query tile), 0 for decode /
@@ -123,6 +124,8 @@ __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int ti
 {
     Counts c{0, 0, 0, 0, 0, 0};
     if (!rq.valid || rq.q == 0)
+        return c;
+    if (rq.q == 1 && p.dec_stream)   // see DecodeStream
         return c;
     if (rq.q == 1) {
         const int ns = decode_splits(rq, max_splits, p.dec_keys);
@@ -270,18 +273,18 @@ __device__ void fill_run_first(const PlanParams &p, int n_pieces, int grid, bool
 }
 
 // Block-wide exclusive scan of N ints; returns the totals.
-template <int N>
-__device__ void block_scan(int (&v)[N], int (&tot)[N])
+template <int N, typename T>
+__device__ void block_scan(T (&v)[N], T (&tot)[N])
 {
-    __shared__ int warp_sums[kPlanThreads / 32][kScan];
+    __shared__ T warp_sums[kPlanThreads / 32][N];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl[N];
+    T incl[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        int x = v[j];
+        T x = v[j];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            const T y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
         incl[j] = x;
@@ -291,10 +294,10 @@ __device__ void block_scan(int (&v)[N], int (&tot)[N])
     __syncthreads();
     if (warp == 0) {
         for (int j = 0; j < N; ++j) {
-            int x = warp_sums[lane][j];
+            T x = warp_sums[lane][j];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                const T y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
             warp_sums[lane][j] = x;   // inclusive over warps
@@ -303,103 +306,206 @@ __device__ void block_scan(int (&v)[N], int (&tot)[N])
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int before = warp > 0 ? warp_sums[warp - 1][j] : 0;
+        const T before = warp > 0 ? warp_sums[warp - 1][j] : 0;
         tot[j] = warp_sums[kPlanThreads / 32 - 1][j];
         v[j] = before + incl[j] - v[j];
     }
     __syncthreads();
 }
 
-// Block-wide maximum (hi) or minimum (!hi).
-__device__ int block_extreme(int x, bool hi)
+// Decode rows cut stream-K style (dec_stream, see plan.cuh): a unit is a row and one item's
+// heads; a request's units follow one another from tile u0 on. One thread does one request.
+struct DecodeStream {
+    long long tiles;   // of all units
+    int run;           // tiles per CTA
+    bool cut;          // whether a run boundary may split a unit (else a unit goes whole to the run of its first tile)
+};
+
+__device__ __forceinline__ int decode_tiles(const PlanParams &p, const Req &rq)
 {
-    __shared__ int red[kPlanThreads / 32];
-    for (int o = 16; o > 0; o >>= 1) {
-        const int y = __shfl_xor_sync(0xffffffffu, x, o);
-        x = hi ? max(x, y) : min(x, y);
-    }
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int m = red[0];
-    for (int w = 1; w < kPlanThreads / 32; ++w) m = hi ? max(m, red[w]) : min(m, red[w]);
-    __syncthreads();
-    return m;
+    return p.dec_stream && rq.valid && rq.q == 1 ? ceil_div(rq.s, kDecodeChunk) : 0;
 }
 
-template <typename T>
-__device__ T block_sum(T x)
+// Partial rows that a request's units can take, before the run is known (a bound: max_splits each).
+__device__ __forceinline__ int decode_stream_rows(const PlanParams &p, int tiles)
 {
-    __shared__ long long red[kPlanThreads / 32];
-    long long a = x;
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    return tiles > 1 ? p.Hq * p.max_splits : 0;
+}
+
+// The bound of all: a boundary between two runs leaves two more pieces of one unit at most.
+__device__ __forceinline__ long long decode_stream_bound(const PlanParams &p, long long rows)
+{
+    return min(rows, (long long)2 * p.dec_grid * p.dec_heads * p.group);
+}
+
+__device__ DecodeStream decode_stream(const PlanParams &p, long long tiles, int longest, int max_splits)
+{
+    DecodeStream d;
+    d.tiles = tiles;
+    d.cut = max_splits > 1;
+    d.run = (int)max((tiles + p.dec_grid - 1) / p.dec_grid, (long long)kMinDecodeRun);
+    if (d.cut)
+        d.run = max(d.run, ceil_div(longest - 1, max_splits - 1));
+    return d;
+}
+
+// A request's counts; with emit its items at the given offsets.
+__device__ Counts decode_stream_work(const PlanParams &p, const DecodeStream &d, int r, const Req &rq, long long u0,
+                                     bool emit, int q_off, const Counts &off)
+{
+    Counts c{0, 0, 0, 0, 0, 0};
+    const int n = decode_tiles(p, rq);
+    if (n == 0)
+        return c;
+    const int ngroups = p.Hkv / p.dec_heads, nh = p.dec_heads * p.group;
+    for (int g = 0; g < ngroups; ++g, u0 += n) {
+        const long long first = u0 / d.run;
+        const int np = d.cut ? (int)((u0 + n - 1) / d.run - first + 1) : 1;
+        if (emit) {
+            const int item = off.ditems + c.ditems, rows = off.prows + c.prows;
+            for (int k = 0; k < np; ++k) {
+                // piece k: the tiles of run first + k
+                const long long lo = k == 0 ? u0 : (first + k) * d.run;
+                const long long hi = k == np - 1 ? u0 + n : (first + k + 1) * d.run;
+                p.ditems[item + k] = DecodeItem{r, g, (int)(lo - u0) * kDecodeChunk,
+                                                min((int)(hi - u0) * kDecodeChunk, rq.s), k, np,
+                                                np > 1 ? rows - g * nh * np : -1, q_off};
+                if (d.cut && lo == (first + k) * d.run)
+                    p.dec_first[first + k] = item + k;
+            }
+            if (!d.cut) {
+                if (u0 == 0)
+                    p.dec_first[0] = item;
+                for (long long x = first + 1; x <= min((u0 + n) / d.run, (long long)p.dec_grid); ++x)
+                    p.dec_first[x] = item + 1;
+            }
+            if (np > 1)
+                p.citems[off.citems + c.citems] = CombineItem{q_off, 1, g * nh, nh, rows, np, off.cunits + c.cunits, 0};
+        }
+        c.ditems += np;
+        if (np > 1) {
+            c.prows += nh * np;
+            c.citems += 1;
+            c.cunits += nh;
+        }
+    }
+    return c;
+}
+
+// dec_first of the runs behind the last tile.
+__device__ void decode_stream_tail(const PlanParams &p, const DecodeStream &d, int n_items, int tid, int nthreads)
+{
+    const long long behind = d.cut || d.tiles == 0 ? (d.tiles + d.run - 1) / d.run : d.tiles / d.run + 1;
+    for (long long x = behind + tid; x <= p.dec_grid; x += nthreads) p.dec_first[x] = n_items;
+}
+
+// What the block sums up (and takes the extremes of) before it walks the requests.
+struct PlanTotals {
+    long long tok, tiles, dprows, dtiles;
+    int longest, shortest, dlongest;
+};
+
+__device__ __forceinline__ void warp_totals(PlanTotals &t)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        t.tok += __shfl_xor_sync(0xffffffffu, t.tok, o);
+        t.tiles += __shfl_xor_sync(0xffffffffu, t.tiles, o);
+        t.dprows += __shfl_xor_sync(0xffffffffu, t.dprows, o);
+        t.dtiles += __shfl_xor_sync(0xffffffffu, t.dtiles, o);
+        t.longest = max(t.longest, __shfl_xor_sync(0xffffffffu, t.longest, o));
+        t.shortest = min(t.shortest, __shfl_xor_sync(0xffffffffu, t.shortest, o));
+        t.dlongest = max(t.dlongest, __shfl_xor_sync(0xffffffffu, t.dlongest, o));
+    }
+}
+
+// Over the block, for all its threads: the warps' totals meet in shared memory, and every warp adds them up.
+__device__ void block_totals(PlanTotals &t)
+{
+    __shared__ PlanTotals red[kPlanThreads / 32];
+    warp_totals(t);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
     __syncthreads();
-    long long t = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) t += red[w];
-    __syncthreads();
-    return (T)t;
+    t = red[threadIdx.x & 31];
+    warp_totals(t);
+}
+
+// One request's part of the totals.
+__device__ __forceinline__ void add_request(const PlanParams &p, const Req &rq, PlanTotals &t)
+{
+    t.tok += rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
+    t.tiles += prefill_tiles(p, rq);
+    t.longest = max(t.longest, longest_unit(p, rq));
+    t.shortest = min(t.shortest, shortest_unit(p, rq));
+    if (p.dec_stream) {
+        const int n = decode_tiles(p, rq);
+        t.dtiles += (long long)n * (p.Hkv / p.dec_heads);
+        t.dlongest = max(t.dlongest, n);
+        t.dprows += decode_stream_rows(p, n);
+    } else if (rq.valid && rq.q == 1) {
+        const int ns = decode_splits(rq, p.max_splits, p.dec_keys);
+        if (ns > 1) t.dprows += (long long)p.Hq * ns;
+    }
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
 {
     // dependents are released at the end (see plan_small_kernel)
     pdl_wait();
-    // ---- pass 1: tokens, prefill tiles, decode partial rows
-    long long tok = 0, tiles = 0, dprows = 0;
-    int longest = 0, shortest = 0x7fffffff;
+    // ---- pass 1: tokens, prefill tiles, decode tiles and partial rows
+    PlanTotals tot{0, 0, 0, 0, 0, 0x7fffffff, 0};
     for (int base = 0; base < p.num_reqs; base += kPlanThreads) {
         const int r = base + threadIdx.x;
-        if (r < p.num_reqs) {
-            const Req rq = load_req(p, r);
-            tok += rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
-            tiles += prefill_tiles(p, rq);
-            longest = max(longest, longest_unit(p, rq));
-            shortest = min(shortest, shortest_unit(p, rq));
-            if (rq.valid && rq.q == 1) {
-                const int ns = decode_splits(rq, p.max_splits, p.dec_keys);
-                if (ns > 1) dprows += (long long)p.Hq * ns;
-            }
-        }
+        if (r < p.num_reqs)
+            add_request(p, load_req(p, r), tot);
     }
-    tok = block_sum(tok);
-    tiles = block_sum(tiles);
-    dprows = block_sum(dprows);
-    longest = block_extreme(longest, true);
-    shortest = block_extreme(shortest, false);
-    if (tok != p.num_tokens) {
+    block_totals(tot);
+    const long long tiles = tot.tiles;
+    if (p.dec_stream)
+        tot.dprows = decode_stream_bound(p, tot.dprows);
+    if (tot.tok != p.num_tokens) {
         if (threadIdx.x == 0) set_dev_error(p.dev_err, CPSA_DEV_TOKENS_MISMATCH);
         if (threadIdx.x < kCntSlots) p.counts[threadIdx.x] = 0;
         for (int c = threadIdx.x; c <= p.chunk_grid; c += kPlanThreads) p.run_first[c] = 0;
+        for (int c = threadIdx.x; p.dec_stream && c <= p.dec_grid; c += kPlanThreads) p.dec_first[c] = 0;
         return;
     }
     const int grid = max(1, p.chunk_grid);
-    const SplitChoice sc = choose_split(p, tiles, shortest, longest, dprows);
+    const SplitChoice sc = choose_split(p, tiles, tot.shortest, tot.longest, tot.dprows);
+    DecodeStream ds{0, 1, false};
+    if (p.dec_stream)
+        ds = decode_stream(p, tot.dtiles, tot.dlongest, sc.max_splits);
     const int run = sc.run, max_splits = sc.max_splits;
     const bool split_prefill = sc.split_prefill;
     if (sc.clamped && threadIdx.x == 0)
         set_dev_error(p.dev_err, CPSA_DEV_SPLITS_CLAMPED);
 
     // ---- pass 2: offsets and lists, 1024 requests at a time
-    __shared__ int s_qoff[kPlanThreads], s_toff[kPlanThreads];
+    __shared__ int s_qoff[kPlanThreads], s_toff[kPlanThreads], s_q[kPlanThreads], s_s[kPlanThreads];
     __shared__ int s_cnt[kPlanThreads][kScan];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int carry_a[2] = {0, 0};                        // tokens, tiles
+    long long carry_d = 0;                          // streamed decode tiles
     int carry_b[kScan] = {0, 0, 0, 0, 0, 0};        // pieces, prows, cunits, citems, ditems, sunits
     for (int base = 0; base < p.num_reqs; base += kPlanThreads) {
         const int nloc = min(kPlanThreads, p.num_reqs - base);
         // (a) token and tile offsets: one thread per request
+        Req mine{false, 0, 0, 0};
         {
             const int r = base + threadIdx.x;
             int va[2] = {0, 0};
             if (threadIdx.x < nloc) {
-                const Req rq = load_req(p, r);
+                mine = load_req(p, r);
+                const Req &rq = mine;
+                s_q[threadIdx.x] = rq.q;
+                s_s[threadIdx.x] = rq.s;
                 va[0] = rq.q > 0 ? rq.q : 0;
                 va[1] = prefill_tiles(p, rq);
                 if (!rq.valid)
                     set_dev_error(p.dev_err, (rq.q < 0 || rq.s < rq.q) ? CPSA_DEV_SEQ_LT_QUERY : CPSA_DEV_SEQ_GT_TABLE);
             }
             int ta[2];
-            block_scan<2>(va, ta);
+            block_scan(va, ta);
             s_qoff[threadIdx.x] = carry_a[0] + va[0];
             s_toff[threadIdx.x] = carry_a[1] + va[1];
             if (threadIdx.x < nloc)
@@ -407,10 +513,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
             carry_a[0] += ta[0];
             carry_a[1] += ta[1];
         }
+        // streamed decode rows: one thread per request
+        long long my_u0 = 0;
+        Counts my_dec{0, 0, 0, 0, 0, 0};
+        if (p.dec_stream) {
+            long long vd[1] = {(long long)decode_tiles(p, mine) * (p.Hkv / p.dec_heads)}, td[1];
+            block_scan(vd, td);
+            my_u0 = carry_d + vd[0];
+            carry_d += td[0];
+            my_dec = decode_stream_work(p, ds, base + threadIdx.x, mine, my_u0, false, 0, Counts{0, 0, 0, 0, 0, 0});
+        }
         __syncthreads();
         // (b) per-request counts: one warp per request
         for (int l = warp; l < nloc; l += kPlanThreads / 32) {
-            const Req rq = load_req(p, base + l);
+            const Req rq = make_req(p, s_q[l], s_s[l]);
             const Counts c = request_work(p, base + l, rq, s_toff[l], run, split_prefill, max_splits, false,
                                           s_qoff[l], Counts{0, 0, 0, 0, 0, 0}, lane);
             if (lane == 0) {
@@ -427,15 +543,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
         {
             int vb[kScan];
             for (int j = 0; j < kScan; ++j) vb[j] = threadIdx.x < nloc ? s_cnt[threadIdx.x][j] : 0;
+            vb[1] += my_dec.prows;
+            vb[2] += my_dec.cunits;
+            vb[3] += my_dec.citems;
+            vb[4] += my_dec.ditems;
             int tb[kScan];
-            block_scan<kScan>(vb, tb);   // ends with a barrier: s_cnt reads are done
+            block_scan(vb, tb);   // ends with a barrier: s_cnt reads are done
             for (int j = 0; j < kScan; ++j) s_cnt[threadIdx.x][j] = carry_b[j] + vb[j];
             for (int j = 0; j < kScan; ++j) carry_b[j] += tb[j];
         }
         __syncthreads();
-        // (d) the lists: one warp per request
+        // (d) the lists: streamed decode rows, then one warp per request
+        if (my_dec.ditems > 0) {
+            const int *o = s_cnt[threadIdx.x];
+            decode_stream_work(p, ds, base + threadIdx.x, mine, my_u0, true, s_qoff[threadIdx.x],
+                               Counts{o[0], o[1], o[2], o[3], o[4], o[5]});
+        }
         for (int l = warp; l < nloc; l += kPlanThreads / 32) {
-            const Req rq = load_req(p, base + l);
+            const Req rq = make_req(p, s_q[l], s_s[l]);
             const Counts off{s_cnt[l][0], s_cnt[l][1], s_cnt[l][2], s_cnt[l][3], s_cnt[l][4], s_cnt[l][5]};
             request_work(p, base + l, rq, s_toff[l], run, split_prefill, max_splits, true, s_qoff[l], off, lane);
         }
@@ -444,6 +569,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
     __syncthreads();   // this block's piece writes are visible to the whole block
     const int n_pieces = (int)min((int64_t)carry_b[0], p.max_pitems);
     fill_run_first(p, n_pieces, grid, split_prefill, tiles, run, threadIdx.x, kPlanThreads);
+    if (p.dec_stream)
+        decode_stream_tail(p, ds, carry_b[4], threadIdx.x, kPlanThreads);
     if (threadIdx.x == 0) {
         p.cu_q[p.num_reqs] = carry_a[0];
         p.counts[kCntPrefill] = (int)min((int64_t)carry_b[0], p.max_pitems);
@@ -475,27 +602,20 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
         rq = load_req(p, lane);
     const int tok = mine && rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
     const int tiles = mine ? prefill_tiles(p, rq) : 0;
-    int longest = mine ? longest_unit(p, rq) : 0;
-    int shortest = mine ? shortest_unit(p, rq) : 0x7fffffff;
-    int dprows = 0;
-    if (mine && rq.valid && rq.q == 1) {
-        const int ns = decode_splits(rq, p.max_splits, p.dec_keys);
-        if (ns > 1) dprows = p.Hq * ns;
-    }
     // totals in 64 bits first: the 32-bit scans below are only used once they fit
-    long long tok_sum = tok, tile_sum = tiles, dprow_sum = dprows;
-    for (int o = 16; o > 0; o >>= 1) {
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-        shortest = min(shortest, __shfl_xor_sync(0xffffffffu, shortest, o));
-        tok_sum += __shfl_xor_sync(0xffffffffu, tok_sum, o);
-        tile_sum += __shfl_xor_sync(0xffffffffu, tile_sum, o);
-        dprow_sum += __shfl_xor_sync(0xffffffffu, dprow_sum, o);
-    }
+    PlanTotals tot{0, 0, 0, 0, 0, 0x7fffffff, 0};
+    if (mine)
+        add_request(p, rq, tot);
+    warp_totals(tot);
+    if (p.dec_stream)
+        tot.dprows = decode_stream_bound(p, tot.dprows);
+    const long long tok_sum = tot.tok, tile_sum = tot.tiles;
     const int grid = max(1, p.chunk_grid);
     if (tok_sum != p.num_tokens) {
         if (lane == 0) set_dev_error(p.dev_err, CPSA_DEV_TOKENS_MISMATCH);
         if (lane < kCntSlots) p.counts[lane] = 0;
         for (int c = lane; c <= p.chunk_grid; c += 32) p.run_first[c] = 0;
+        for (int c = lane; p.dec_stream && c <= p.dec_grid; c += 32) p.dec_first[c] = 0;
         return;
     }
     if (mine && !rq.valid)
@@ -505,10 +625,31 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
     const int tile_off = warp_excl_scan(tiles, lane, tile_total);
     if (mine)
         p.cu_q[lane] = tok_off;
-    const SplitChoice sc = choose_split(p, tile_sum, shortest, longest, dprow_sum);
+    const SplitChoice sc = choose_split(p, tile_sum, tot.shortest, tot.longest, tot.dprows);
     if (sc.clamped && lane == 0)
         set_dev_error(p.dev_err, CPSA_DEV_SPLITS_CLAMPED);
     Counts off{0, 0, 0, 0, 0, 0};
+    DecodeStream ds{0, 1, false};
+    if (p.dec_stream) {
+        // streamed decode rows: a lane per request, ahead of the prefill requests' lists
+        ds = decode_stream(p, tot.dtiles, tot.dlongest, sc.max_splits);
+        long long u0 = (long long)decode_tiles(p, rq) * (p.Hkv / p.dec_heads);
+        const long long own = u0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, u0, o);
+            if (lane >= o) u0 += y;
+        }
+        u0 -= own;
+        const Counts c = decode_stream_work(p, ds, lane, rq, u0, false, 0, off);
+        Counts at;
+        at.pieces = at.sunits = 0;
+        at.prows = warp_excl_scan(c.prows, lane, off.prows);
+        at.cunits = warp_excl_scan(c.cunits, lane, off.cunits);
+        at.citems = warp_excl_scan(c.citems, lane, off.citems);
+        at.ditems = warp_excl_scan(c.ditems, lane, off.ditems);
+        decode_stream_work(p, ds, lane, rq, u0, true, tok_off, at);
+    }
     for (int r = 0; r < p.num_reqs; ++r) {
         Req rr;
         rr.valid = __shfl_sync(0xffffffffu, rq.valid ? 1 : 0, r) != 0;
@@ -528,6 +669,8 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
     __syncwarp();   // the warp's piece writes are visible to all its lanes
     const int n_pieces = (int)min((int64_t)off.pieces, p.max_pitems);
     fill_run_first(p, n_pieces, grid, sc.split_prefill, tile_sum, sc.run, lane, 32);
+    if (p.dec_stream)
+        decode_stream_tail(p, ds, off.ditems, lane, 32);
     if (lane == 0) {
         p.cu_q[p.num_reqs] = tok_total;
         p.counts[kCntPrefill] = n_pieces;

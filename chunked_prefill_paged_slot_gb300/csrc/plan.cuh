@@ -69,6 +69,14 @@ constexpr int kDecodeKeysPerSplitGrouped = 1024;
 // 32768 keys 140 us).
 constexpr int kDecodeKeysPerSplitQ8Few = 256;
 constexpr int kDecodeKeysPerSplitQ8Fewest = 128;
+// Over the 4-bit cache, where a whole row each would occupy half the SMs, decode rows are cut
+// stream-K style like prefill units (dec_stream): the 64-key tiles of all (row, heads item)
+// units laid end to end in equal runs, one per CTA of the decode kernel, at least kMinDecodeRun
+// tiles and long enough that no unit becomes more than max_kv_splits pieces. Every CTA reads
+// the same number of keys, and at most a row per run boundary leaves partials. (384 rows of 1024
+// to 8192 keys, 32/8 heads, with splits every 1024 keys dealt round: SMs active 90 % of the
+// kernel, 375 us, and 15 us of the combine kernel.)
+constexpr int kMinDecodeRun = 2;
 constexpr int kMaxSplitUnits = kMaxChunkGrid;   // a split unit holds a run boundary: at most grid - 1
 constexpr int kMergeCounters = 2 * 4;          // per split unit: q heads (<= 2) x 4 softmax warps
 // A batch of one prefill request skips the plan kernel: every chunk-kernel CTA
@@ -112,7 +120,7 @@ enum CountSlot {
 };
 
 struct WsLayout {
-    size_t off_counts, off_cuq, off_runs, off_flags, off_pitems, off_ditems, off_citems, off_pml, off_po, end_meta,
+    size_t off_counts, off_cuq, off_runs, off_dec_runs, off_flags, off_pitems, off_ditems, off_citems, off_pml, off_po, end_meta,
         end_full;
     int64_t max_pitems, max_ditems, max_citems, max_prows_full;
 };
@@ -132,7 +140,8 @@ inline WsLayout ws_layout(int num_reqs, int64_t num_tokens, int Hq, int Hkv, int
     int64_t units = qtiles * Hkv * ((Hq / Hkv) / nq_per_cta);
     L.max_pitems = units + kMaxChunkGrid;
     L.max_ditems = ndecode * Hkv * max_splits;
-    L.max_citems = ndecode;   // split decode rows
+    // split decode rows; streamed, a row splits by heads item, a unit per run boundary at most
+    L.max_citems = ndecode + (Hkv > 1 && ndecode > 0 ? kMaxChunkGrid : 0);
     // prefill: a cut inside a unit adds one piece, at most 2 pieces' partials per cut
     const int64_t prefill_rows = max_splits > 1 ? (int64_t)2 * kMaxChunkGrid * 128 * nq_per_cta : 0;
     const int64_t decode_rows = max_splits > 1 ? ndecode * Hq * max_splits : 0;
@@ -141,6 +150,7 @@ inline WsLayout ws_layout(int num_reqs, int64_t num_tokens, int Hq, int Hkv, int
     L.off_counts = o; o = ws_align(o + sizeof(int32_t) * kCntSlots);
     L.off_cuq = o;    o = ws_align(o + sizeof(int32_t) * (size_t)(B + 1));
     L.off_runs = o;   o = ws_align(o + sizeof(int32_t) * (size_t)(kMaxChunkGrid + 1));
+    L.off_dec_runs = o; o = ws_align(o + sizeof(int32_t) * (size_t)(kMaxChunkGrid + 1));
     L.off_flags = o;  o = ws_align(o + sizeof(unsigned long long) * (size_t)kMaxSplitUnits * kMergeCounters);
     L.off_pitems = o; o = ws_align(o + sizeof(PrefillItem) * (size_t)L.max_pitems);
     L.off_ditems = o; o = ws_align(o + sizeof(DecodeItem) * (size_t)L.max_ditems);
@@ -174,6 +184,9 @@ struct PlanParams {
     int dec_heads;             // kv heads per decode item: 1, or a group of 4 or 8 (the grouped decode kernel)
     int unit_cost;             // a unit's fixed cost in KV tiles: kUnitCostTiles, or unit_cost_q8
     int dec_keys;              // keys per decode split (a multiple of kDecodeChunk)
+    int dec_stream;            // decode rows cut stream-K style, in runs of dec_grid CTAs
+    int dec_grid;
+    int32_t *dec_first;        // [dec_grid + 1]: first decode item of each CTA's run (dec_stream)
     int chunk_grid;            // CTAs of the chunk kernel (stream-K runs)
     int fused;                 // KV write fused: the chunk's own keys form tiles of their own
     int64_t prow_capacity;     // partial rows that fit

@@ -344,8 +344,12 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
  * earlier rows of the same chunk). Scale bytes above 226 (10240), which the append stores
  * for NaN alone, stand for numbers that f16 may not hold: infinities and NaN may come of
  * them. (The pages have no counterpart.)
- * Every other argument, the workspace (same size functions), the device flags, CUDA
- * graph capture and the splits are cpp_chunked_prefill_attn_q8's.
+ * Every other argument, the workspace (same size functions), the device flags and CUDA
+ * graph capture are cpp_chunked_prefill_attn_q8's, and so are the splits, but that where a
+ * call can hold enough decode rows to occupy half the GPU, these are cut like prefill
+ * units: laid end to end in equal runs, one per CTA, no row in more than max_kv_splits
+ * pieces. A decode row's last-bit rounding can then depend on the other requests (it does
+ * not depend on timing).
  * Arithmetic: stored numbers enter the MMAs as f16, exact; q rows as f16 under a power of
  * two of their own; probabilities in f16; partial results of a chunk's split units in
  * bf16, as in cpp_chunked_prefill_attn; everything else in fp32.

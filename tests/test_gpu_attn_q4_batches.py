@@ -62,3 +62,48 @@ def test_more_tokens_than_one_warp_plans(cuda_lib, d, hq, hkv):
     at = np.r_[0, 1:4001:37, 4000, 4001, 4002:7779:41, 7778, 7779:8479:13, 8478, 8479]
     ref, vmax = reference(b, caches, rows=at)
     close(got[at], ref, vmax)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(1500, 4, 1, 64), (1100, 6, 6, 128), (2100, 2, 2, 64)])
+def test_more_rows_than_one_pass_of_the_plan(cuda_lib, n, hq, hkv, d):
+    """Decode rows beside requests without tokens, more than 1024 requests; one row much longer than the others."""
+    rng = np.random.default_rng(n)
+    hist, qlen = [int(x) for x in rng.integers(0, 130, n)], [1] * n
+    hist[n // 2] = 9000
+    for i in range(5, n, 97):
+        qlen[i] = 0
+    check(cuda_lib, W.BatchSpec(hist=hist, qlen=qlen, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=16,
+                                seed=4400 + n))
+
+
+@pytest.mark.parametrize("n,hq,hkv", [(160, 8, 8), (60, 12, 6), (90, 16, 1)])
+@pytest.mark.parametrize("prompts", [0, 2])
+def test_rows_in_whole_where_partials_do_not_fit(cuda_lib, n, hq, hkv, prompts):
+    hist, qlen = rows(n, n) + [300] * prompts, [1] * n + [140] * prompts
+    T = n + 140 * prompts
+    small = cuda_lib.cpp_attn_workspace_min_bytes(n + prompts, T, hq, hkv, 128, 8)
+    check(cuda_lib, W.BatchSpec(hist=hist, qlen=qlen, num_q_heads=hq, num_kv_heads=hkv, head_dim=128, page_size=32,
+                                seed=4500 + n), workspace_bytes=small, expect_flags=cuda_lib.DEV_SPLITS_CLAMPED)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 8])
+def test_rows_of_equal_and_of_one_length(cuda_lib, splits):
+    """Runs that end where rows do, and rows of one key."""
+    for hist in ([127] * 304, [0] * 200, [4095] * 80, [63] * 151 + [20000]):
+        check(cuda_lib, W.BatchSpec(hist=hist, qlen=[1] * len(hist), num_q_heads=8, num_kv_heads=8, head_dim=64,
+                                    page_size=64, seed=4600 + len(hist)), max_kv_splits=splits)
+
+
+def test_invalid_rows_among_many(cuda_lib):
+    """Rows that are refused take no part; the others come out as they should."""
+    n = 120
+    b, caches = draw(W.BatchSpec(hist=rows(n, 3), qlen=[1] * n, num_q_heads=8, num_kv_heads=8, head_dim=128, page_size=16,
+                                 seed=4700))
+    ref, vmax = reference(b, caches)
+    b.seq_lens[7] = 0
+    b.seq_lens[50] = 1 << 20
+    got, flags = run(cuda_lib, b, caches)
+    assert flags == cuda_lib.DEV_SEQ_LT_QUERY | cuda_lib.DEV_SEQ_GT_TABLE
+    keep = np.delete(np.arange(n), [7, 50])
+    close(got[keep], ref[keep], vmax[keep])
+    assert np.isnan(got[[7, 50]]).all()
