@@ -767,7 +767,8 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     // write, whose cache writer holds the staging buffer) and of merged rows at
     // the end of a run; without the map the rows are stored directly
     CUtensorMap to{};
-    cp.out_tma = head_dim == 128 && aligned16(out) &&
+    // (over the 4-bit cache that buffer holds Q)
+    cp.out_tma = head_dim == 128 && !q4 && aligned16(out) &&
                          make_map(&to, out, D, (uint64_t)num_q_heads, (uint64_t)num_tokens, D * 2,
                                   D * 2 * num_q_heads, 64, 1, 32)
                      ? 1
@@ -777,9 +778,15 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
                         __builtin_ctz((unsigned)page_size), page_size < 16 ? 3 : 4};
         cp.q = q;
         cp.q8 = c;
-        if (!single_decode && (q4 ? launch_chunk_q4 : launch_chunk_q8)(cp, to, head_dim, nq, pp.chunk_grid, s,
-                                                                       early && !self_plan) != cudaSuccess)
+        if (q4 && !single_decode) {
+            CUtensorMap tq;
+            if (!make_map(&tq, q, D, (uint64_t)num_q_heads, (uint64_t)num_tokens, D * 2, D * 2 * num_q_heads, 64, 1, 128) ||
+                launch_chunk_q4(cp, tq, to, head_dim, nq, pp.chunk_grid, s, early && !self_plan) != cudaSuccess)
+                return CPSA_ERR_CUDA;
+        } else if (!single_decode &&
+                   launch_chunk_q8(cp, to, head_dim, nq, pp.chunk_grid, s, early && !self_plan) != cudaSuccess) {
             return CPSA_ERR_CUDA;
+        }
         if (!single_prefill) {
             DecodeParams dp;
             static_cast<AttnCommon &>(dp) = ac;

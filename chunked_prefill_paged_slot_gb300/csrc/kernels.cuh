@@ -138,9 +138,9 @@ cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const
 // the chunk kernel over the 8-bit cache (p.q, p.q8)
 cudaError_t launch_chunk_q8(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
                             cudaStream_t s, bool early);
-// and over the 4-bit cache (p.q, p.q8; lg_sb not used)
-cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
-                            cudaStream_t s, bool early);
+// and over the 4-bit cache (p.q8; lg_sb not used)
+cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &to, int head_dim, int nq,
+                            int grid, cudaStream_t s, bool early);
 cudaError_t launch_decode_attn(const DecodeParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int head_dim,
                                int grid, cudaStream_t s, bool early);
 // the grouped decode kernel: items of heads_per_item (4 or 8) kv heads; tk / tv

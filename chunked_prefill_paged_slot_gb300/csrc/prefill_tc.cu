@@ -45,6 +45,8 @@
 // maximum exceeds it by more than 8 (a factor 256 in the exponent), which keeps
 // p <= 256 and leaves the final O / l unchanged.
 // TMEM columns: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [256+D, 256+2D).
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "plan.cuh"
@@ -91,7 +93,10 @@ struct ChunkCfg {
     static constexpr int kItemOff = kBarOff + 256;             // self-planned pieces (after ChunkBars)
     static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
     static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
-    static constexpr int kBarBytes = 256 + kSelfPlanCap * 32;  // barriers + pieces (+ Q8Tiles)
+    static constexpr int kBarBytes = 256 + kSelfPlanCap * 32 + (Q4 ? 512 : 0);  // barriers + pieces (+ Q8Tiles, Q4Tiles)
+    // Q4: the ring of Q tiles
+    static constexpr int kQRing = NQ + 1;
+    __host__ __device__ static constexpr int q_tile(uint32_t i) { return i < (uint32_t)NQ ? (int)i * kTileBytes : kStageOff; }
     static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
     static_assert(D != 128 || NQ * 4 * kMergeStageBytes <= kSlotOff + 4 * kTileBytes,
@@ -102,6 +107,7 @@ struct ChunkCfg {
     static constexpr int kMmaWarp = Q8 ? 12 : 9;
     static constexpr int kWriteWarp = 10;
     static constexpr int kQ8LoadWarp = 13;
+    static constexpr int kQ4QLoadWarp = 14;                    // Q4: Q by TMA
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t s_col(int n) { return (uint32_t)n * 128u; }
     __host__ __device__ static constexpr uint32_t o_col(int n) { return 256u + (uint32_t)n * D; }
@@ -128,13 +134,27 @@ struct ChunkBars {
 struct Q8Tiles {
     int kx[8], vx[8];
     int8_t qe[2][256];
-    uint64_t full[4], empty[4];   // half-tiles on their way: landed, converted
+    uint64_t full[kQ8Stages], empty[kQ8Stages];   // e4m3 half-tiles: landed, converted
     struct {
         int8_t ek[16], ev[16];   // per group of eight keys: its factor's exponent
         uint32_t there;          // bit l: group l is loaded
         uint32_t pad[3];
     } tile[4];
 };
+// The same place over the 4-bit cache. Q tiles (a head's 128 rows) have a ring of NQ + 1 buffers,
+// tile u of the CTA's run in buffer u % (NQ + 1): the last is the staging buffer of the output,
+// which that kernel does without. Their exponents live longer, until the softmax has looked at
+// its first tile: an entry is written again only after an MMA of a later item (see Q8Tiles).
+struct Q4Tiles {
+    int8_t qe[6][128];
+    uint64_t full[4], empty[4];                      // half-tiles on their way: landed, converted
+    uint64_t q_raw[3], q_full[3], q_empty[3];        // Q tiles: landed as bf16, converted, used up
+    uint32_t there[4];                               // per KV tile (modulo 4), bit l: group l of eight keys is loaded
+};
+constexpr int kQ4Room = 512;   // what the 4-bit cache's kernel keeps beyond that of the 8-bit cache's
+static_assert(sizeof(Q4Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32 + kQ4Room, "in place of the pieces it gave up, and its own");
+template <bool Q4>
+using Tiles = std::conditional_t<Q4, Q4Tiles, Q8Tiles>;
 static_assert(sizeof(Q8Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32, "in place of the pieces it gave up");
 static_assert(sizeof(ChunkBars) <= 256, "the self-planned pieces follow the barriers at +256");
 static_assert(sizeof(PrefillItem) == 32, "piece size");
@@ -797,7 +817,7 @@ __device__ __forceinline__ void q8_load(const ChunkParams &p, uint8_t *smem, Chu
 // bulk copies, all rows of a page at once, kQ4Stages half-tiles ahead. Its numbers are exact
 // in f16 (q4.cuh): no exponents to be told to anyone, only which groups are there.
 template <int D, int NQ>
-__device__ __forceinline__ void q4_load(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+__device__ __forceinline__ void q4_load(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q4Tiles *q8t,
                                         const PrefillItem *items, int it_begin, int it_end, int lane)
 {
     using C = ChunkCfg<D, NQ, true, true>;
@@ -840,7 +860,7 @@ __device__ __forceinline__ void q4_load(const ChunkParams &p, uint8_t *smem, Chu
                 }
                 // after the wait: the tile four before, whose entry this is, is converted
                 if (kv == 0 && lane == 16)
-                    q8t->tile[tile & 3].there = there;
+                    q8t->there[tile & 3] = there;
                 __syncwarp();
                 // each lane announces its own copies' bytes right before it issues them
                 if (copier) {
@@ -866,6 +886,67 @@ __device__ __forceinline__ void q4_load(const ChunkParams &p, uint8_t *smem, Chu
     mbar_drain(q8t->full, half, C::kRawStages);
 }
 
+// The 4-bit cache's Q tiles, as bf16, into the buffers that they are converted in: the next
+// item's first head while this item's last tiles are still being multiplied.
+template <int D, int NQ>
+__device__ __forceinline__ void q4_load_q(const ChunkParams &p, const CUtensorMap *tm_q, uint8_t *smem, ChunkBars *bars,
+                                          Q4Tiles *q4t, const PrefillItem *items, int it_begin, int it_end, bool self,
+                                          int lane)
+{
+    using C = ChunkCfg<D, NQ, true, true>;
+    volatile int *abort = &bars->abort;
+    uint32_t u = 0;
+    bool ok = true;
+    for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
+        const PrefillItem w = items[it];
+        const int h0 = (w.kvh_hp & 0xFFFF) * p.group + (w.kvh_hp >> 16) * NQ;
+        const int row0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
+        for (int n = 0; n < NQ; ++n, ++u) {
+            const uint32_t b = u % C::kQRing;
+            if (u >= (uint32_t)C::kQRing &&
+                !(ok = mbar_wait_warp(&q4t->q_empty[b], ((u / C::kQRing) - 1) & 1, abort)))
+                break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q4t->q_raw[b], C::kTileBytes);
+                for (int c = 0; c < C::kHalves; ++c)
+                    tma_load_3d(smem + C::q_tile(b) + c * C::kHalfBytes, tm_q, &q4t->q_raw[b], c * 64, h0 + n, row0);
+            }
+            __syncwarp();
+        }
+    }
+    mbar_drain(q4t->q_raw, u, C::kQRing);
+}
+
+// This thread's row of a Q tile from bf16 to f16, in place (swizzled rows side by side: no bank
+// conflicts); returns its exponent.
+template <int D>
+__device__ __forceinline__ int q4_convert_q_row(uint32_t tile, int row)
+{
+    const uint32_t k = 0x7fff7fffu;
+    uint32_t w = 0;
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 x = lds128(tile + f16_chunk_off(row, ch));
+        w = __vmaxu2(w, __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k)));
+    }
+    uint32_t top = max(w & 0xffffu, w >> 16);
+    float amax = __uint_as_float(top << 16);
+    if (top >= 0x7f80u) {   // an infinity or NaN: the largest of the others
+        amax = 0.f;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 8; ++ch) amax = fmaxf(amax, bf16x8_amax(lds128(tile + f16_chunk_off(row, ch))));
+    }
+    const int e = q_exponent(amax);
+    const float f = exp2i(-e);
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 x = lds128(tile + f16_chunk_off(row, ch));
+        sts128(tile + f16_chunk_off(row, ch), make_uint4(bf16x2_to_f16x2(x.x, f), bf16x2_to_f16x2(x.y, f),
+                                                         bf16x2_to_f16x2(x.z, f), bf16x2_to_f16x2(x.w, f)));
+    }
+    return e;
+}
+
 // This thread's 32 columns of a row of the 4-bit cache, two groups, from a load of codes
 // and one of scale bytes to four chunks of a row of the f16 tile at `dst` + off[].
 __device__ __forceinline__ void q4_convert_row(const uint4 &v, uint32_t scales, uint32_t dst, const uint32_t (&off)[4])
@@ -886,7 +967,7 @@ __device__ __forceinline__ void q4_convert_row(const uint4 &v, uint32_t scales, 
 // time: one load, one of the two scale bytes, sixteen conversions and multiplications, four
 // stores; eight threads in a row (of the warp) store to eight different 16-byte banks.
 template <int D, int NQ, bool Q4 = false>
-__device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Q8Tiles *q8t,
+__device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Tiles<Q4> *q8t,
                                            const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
                                            int lane)
 {
@@ -931,8 +1012,23 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
         // Q, head by head: a warp's rows of every STEP, this thread's columns 16 c .. 16 c + 15;
         // the first loads are on their way before the wait for the buffer
         auto convert_q = [&]() -> bool {
-            constexpr int STEP = C::kConverters * RPW, BATCH = D == 128 ? 4 : 2;   // of the 8 or 4 rows a thread has per head
+            if constexpr (Q4) {
+#pragma unroll 1
+                for (int n = 0; n < NQ; ++n, ++q_uses) {   // q_uses: tiles here
+                    const uint32_t b = q_uses % C::kQRing;
+                    if (!wait(&q8t->q_raw[b], (q_uses / C::kQRing) & 1))
+                        return false;
+                    const int row = cw * 32 + lane;
+                    q8t->qe[q_uses % 6][row] = (int8_t)q4_convert_q_row<D>(smem_u32(smem + C::q_tile(b)), row);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&q8t->q_full[b]);
+                }
+                return true;
+            } else {
             int8_t *qe = q8t->qe[q_uses & 1];
+            constexpr int STEP = C::kConverters * RPW, BATCH = D == 128 ? 4 : 2;   // of the 8 or 4 rows a thread has per head
             const int64_t t0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
 #pragma unroll 1
             for (int x = 0; x < NQ * (128 / STEP / BATCH); ++x) {
@@ -979,6 +1075,7 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
             if (lane == 0)
                 mbar_arrive(&bars->q_full);
             return true;
+            }
         };
         for (int kt = w.kt0; kt < w.kt1 && ok; ++kt, ++tile) {
             const int nlive = s_len - kt * 128;
@@ -992,9 +1089,14 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
                 ok = wait(&q8t->full[st], (half / C::kRawStages) & 1);
                 if (!ok)
                     break;
-                const auto &e = q8t->tile[tile & 3];
-                const uint32_t there = e.there;
-                const uint32_t fl = f16x2_pow2((kv == 0 ? e.ek : e.ev)[lane & 15]);
+                uint32_t there, fl = 0;
+                if constexpr (Q4) {
+                    there = q8t->there[tile & 3];
+                } else {
+                    const auto &e = q8t->tile[tile & 3];
+                    there = e.there;
+                    fl = f16x2_pow2((kv == 0 ? e.ek : e.ev)[lane & 15]);
+                }
                 if (half >= (uint32_t)C::kSlots) {
                     ok = wait(&bars->slot_empty[slot], ((half / C::kSlots) - 1) & 1);
                     if (!ok)
@@ -1073,6 +1175,10 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
 // one of these instructions, not just one alike in another branch.
 __device__ __forceinline__ void regs_keep_96() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 __device__ __forceinline__ void regs_take_160() { asm volatile("setmaxnreg.inc.sync.aligned.u32 160;"); }
+// Over the 4-bit cache, whose converters need fewer (256 x 176 + 256 x 80 = 512 x 128): 512 tokens at
+// history 32256 (32/8 heads) 195 us, with 160 and 96 201 us.
+__device__ __forceinline__ void regs_q4_others() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void regs_q4_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
 
 // This thread's row of O times f. Out of line: rarely called, and the softmax loop's code stays as it is.
 template <int D>
@@ -1132,7 +1238,14 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             mbar_init(&bars->slot_empty[s], 1);
         }
         if (Q8) {
-            Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
+            Tiles<Q4> *q8t = reinterpret_cast<Tiles<Q4> *>(smem + C::kQ8Off);
+            if constexpr (Q4) {
+                for (int s = 0; s < C::kQRing; ++s) {
+                    mbar_init(&q8t->q_raw[s], 1);
+                    mbar_init(&q8t->q_full[s], C::kConverters);
+                    mbar_init(&q8t->q_empty[s], 1);
+                }
+            }
             for (int s = 0; s < C::kRawStages; ++s) {
                 mbar_init(&q8t->full[s], (uint32_t)(128 / (p.page_size < 128 ? p.page_size : 128)));   // one per copy
                 mbar_init(&q8t->empty[s], C::kConverters);
@@ -1195,10 +1308,13 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
     // first row of a request in q / out (a self-planned batch has one request)
     auto row0 = [&](int r) -> int { return SELF ? 0 : p.cu_q[r]; };
 
-    Q8Tiles *q8t = reinterpret_cast<Q8Tiles *>(smem + C::kQ8Off);
+    Tiles<Q4> *q8t = reinterpret_cast<Tiles<Q4> *>(smem + C::kQ8Off);
     if (Q8 && warp >= C::kLoadWarp && warp < C::kLoadWarp + C::kConverters) {
         if constexpr (Q8) {
-            regs_keep_96();
+            if constexpr (Q4)
+                regs_q4_others();
+            else
+                regs_keep_96();
             q8_convert<D, NQ, Q4>(p, smem, bars, q8t, items, it_begin, it_end, SELF, warp - C::kLoadWarp, lane);
         }
     } else if (!Q8 && warp == C::kLoadWarp) {
@@ -1445,7 +1561,9 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         }
     } else if (warp / 4 < NQ) {
         // ------------------------------------------------------------ softmax
-        if constexpr (Q8)
+        if constexpr (Q4)
+            regs_q4_softmax();
+        else if constexpr (Q8)
             regs_take_160();
         const int wg = warp / 4;
         const int sub = warp & 3;
@@ -1482,13 +1600,17 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     break;
                 float tsl2 = sl2, xs = 1.f;
                 if constexpr (Q8) {
-                    const volatile Q8Tiles *qt = q8t;
-                    // (the lift with the q row's exponent: the K tile's may be the smallest there is)
-                    if (t == 0)
-                        q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]) * (Q4 ? 1.f : exp2i(-kQ8Lift));
-                    // never 0 or infinite: a masked score times it stays -inf, a zero one 0
-                    tsl2 = fminf(fmaxf(Q4 ? q_sl2 : q_sl2 * exp2i(qt->kx[s_uses & 7]), 1.2e-38f), 3.0e38f);
-                    if constexpr (!Q4) {
+                    const volatile Tiles<Q4> *qt = q8t;
+                    if constexpr (Q4) {
+                        // never 0 or infinite: a masked score times it stays -inf, a zero one 0
+                        if (t == 0)
+                            q_sl2 = fminf(fmaxf(sl2 * exp2i(qt->qe[((it - it_begin) * NQ + wg) % 6][row]), 1.2e-38f), 3.0e38f);
+                        tsl2 = q_sl2;
+                    } else {
+                        // (the lift with the q row's exponent: the K tile's may be the smallest there is)
+                        if (t == 0)
+                            q_sl2 = sl2 * exp2i(qt->qe[(it - it_begin) & 1][wg * 128 + row]) * exp2i(-kQ8Lift);
+                        tsl2 = fminf(fmaxf(q_sl2 * exp2i(qt->kx[s_uses & 7]), 1.2e-38f), 3.0e38f);
                         const int x = qt->vx[s_uses & 7];
                         if (t > 0)
                             xs = exp2i(max(vx - x, -126));
@@ -1799,15 +1921,19 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
         // but instruction fetch is what runs short: with this group before the softmax, 512 tokens
         // at history 32256 (32/8 heads) take 216 us instead of 210, eight fresh prompts of 2600
         // tokens 692 instead of 630.
-        if constexpr (Q8)
+        if constexpr (Q4)
+            regs_q4_others();
+        else if constexpr (Q8)
             regs_keep_96();
         if (Q8 && warp != C::kMmaWarp) {
             if constexpr (Q8) {
-                if (warp == C::kQ8LoadWarp) {
-                    if constexpr (Q4)
+                if constexpr (Q4) {
+                    if (warp == C::kQ8LoadWarp)
                         q4_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
-                    else
-                        q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
+                    else if (warp == C::kQ4QLoadWarp)
+                        q4_load_q<D, NQ>(p, &tm_q, smem, bars, q8t, items, it_begin, it_end, SELF, lane);
+                } else if (warp == C::kQ8LoadWarp) {
+                    q8_load<D, NQ>(p, smem, bars, q8t, items, it_begin, it_end, lane);
                 }
             }
         } else {
@@ -1829,10 +1955,11 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     umma_commit(bar);
             };
             auto issue_qk = [&](int n, int slot) {
+                const uint32_t q_tile = Q4 ? q_addr + C::q_tile((q_uses * NQ + n) % C::kQRing) : q_addr + n * C::kTileBytes;
     #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t koff = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
-                    const uint64_t a = smem_desc_sw128(q_addr + n * C::kTileBytes + koff, 0, 1024);
+                    const uint64_t a = smem_desc_sw128(q_tile + koff, 0, 1024);
                     const uint64_t b = smem_desc_sw128(slot_addr + slot * C::kTileBytes + koff, 0, 1024);
                     if (elect_one_sync())
                         umma_ss(tmem + C::s_col(n), a, b, idesc_qk, kk > 0);
@@ -1870,21 +1997,44 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 const int n = w.kt1 - w.kt0;
                 // tiles from nh on hold the chunk's own keys, loaded from k/v (fused KV write)
                 const int nh = v_pages && p.fused ? (p.seq_lens[w.r] - p.query_lens[w.r] + 127) / 128 : 0x7fffffff;
-                if (!wait(&bars->q_full, q_uses & 1))
-                    break;
-                ++q_uses;
-                tc_fence_after_sync();
                 int sK, sV;
-                if (!wait_slot(sK))
-                    break;
-                for (int qn = 0; qn < NQ; ++qn) {
-                    issue_qk(qn, sK);
-                    commit(&bars->s_full[qn]);
-                }
-                commit(&bars->slot_empty[sK]);
-                if (n == 1)
-                    commit(&bars->q_empty);
                 bool ok = true;
+                // Q4: head by head, as its Q tile is there; used up with the item's last scores
+                auto q_done = [&](int qn) {
+                    if constexpr (Q4)
+                        commit(&q8t->q_empty[(q_uses * NQ + qn) % C::kQRing]);
+                };
+                if constexpr (Q4) {
+                    if (!wait_slot(sK))
+                        break;
+                    for (int qn = 0; qn < NQ && ok; ++qn) {
+                        const uint32_t u = q_uses * NQ + qn;
+                        if (!(ok = wait(&q8t->q_full[u % C::kQRing], (u / C::kQRing) & 1)))
+                            break;
+                        tc_fence_after_sync();
+                        issue_qk(qn, sK);
+                        commit(&bars->s_full[qn]);
+                        if (n == 1)
+                            q_done(qn);
+                    }
+                    if (!ok)
+                        break;
+                    commit(&bars->slot_empty[sK]);
+                } else {
+                    if (!wait(&bars->q_full, q_uses & 1))
+                        break;
+                    ++q_uses;
+                    tc_fence_after_sync();
+                    if (!wait_slot(sK))
+                        break;
+                    for (int qn = 0; qn < NQ; ++qn) {
+                        issue_qk(qn, sK);
+                        commit(&bars->s_full[qn]);
+                    }
+                    commit(&bars->slot_empty[sK]);
+                    if (n == 1)
+                        commit(&bars->q_empty);
+                }
                 for (int t = 0; t < n && ok; ++t) {
                     if (!(ok = wait_slot(sV)))
                         break;
@@ -1901,6 +2051,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                             break;
                         issue_qk(0, sK);
                         commit(&bars->s_full[0]);
+                        if (t + 2 == n)
+                            q_done(0);
                     }
                     if (NQ == 2) {
                         if (!(ok = wait(&bars->p_full[1], p_uses[1] & 1)))
@@ -1915,14 +2067,18 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (NQ == 2) {
                             issue_qk(1, sK);
                             commit(&bars->s_full[1]);
+                            if (t + 2 == n)
+                                q_done(1);
                         }
                         commit(&bars->slot_empty[sK]);
-                        if (t + 2 == n)
+                        if (!Q4 && t + 2 == n)
                             commit(&bars->q_empty);
                     }
                 }
                 if (!ok)
                     break;
+                if constexpr (Q4)
+                    ++q_uses;   // items here
             }
             if (aborted()) {
                 // let every MMA issued so far finish before TMEM is released
@@ -1936,7 +2092,10 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
             __syncwarp();
         }
     } else if constexpr (Q8) {
-        regs_keep_96();   // one q head a CTA: the other softmax group is idle
+        if constexpr (Q4)
+            regs_q4_others();
+        else
+            regs_keep_96();   // one q head a CTA: the other softmax group is idle
     }
 
     // the softmax warps' output stores are complete before the CTA ends
@@ -2007,26 +2166,28 @@ cudaError_t launch_chunk_attn(const ChunkParams &p, const CUtensorMap &tq, const
 }
 #else
 template <int D, int NQ>
-cudaError_t launch_chunk_q4_t(const ChunkParams &p, const CUtensorMap &to, int grid, cudaStream_t s, bool early)
+cudaError_t launch_chunk_q4_t(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &to, int grid, cudaStream_t s, bool early)
 {
     using C = ChunkCfg<D, NQ, true, true>;
     static std::atomic<uint64_t> done_self{0}, done_plan{0};
     auto k = p.self_plan ? chunk_attn_kernel<D, NQ, true, true, true> : chunk_attn_kernel<D, NQ, false, true, true>;
     return launch_with_smem(p.self_plan ? done_self : done_plan, reinterpret_cast<const void *>(k), C::kSmemBytes,
                             [&] {
-                                return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, to,
+                                return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, tq,
                                                   to, to, to, to, to, to);
                             });
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &to, int head_dim, int nq, int grid,
-                            cudaStream_t s, bool early)
+cudaError_t launch_chunk_q4(const ChunkParams &p, const CUtensorMap &tq, const CUtensorMap &to, int head_dim, int nq,
+                            int grid, cudaStream_t s, bool early)
 {
     if (head_dim == 128)
-        return nq == 2 ? launch_chunk_q4_t<128, 2>(p, to, grid, s, early) : launch_chunk_q4_t<128, 1>(p, to, grid, s, early);
-    return nq == 2 ? launch_chunk_q4_t<64, 2>(p, to, grid, s, early) : launch_chunk_q4_t<64, 1>(p, to, grid, s, early);
+        return nq == 2 ? launch_chunk_q4_t<128, 2>(p, tq, to, grid, s, early)
+                       : launch_chunk_q4_t<128, 1>(p, tq, to, grid, s, early);
+    return nq == 2 ? launch_chunk_q4_t<64, 2>(p, tq, to, grid, s, early)
+                   : launch_chunk_q4_t<64, 1>(p, tq, to, grid, s, early);
 }
 #endif
 
