@@ -687,7 +687,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
     const int dec_heads = scaled ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.dec_heads = dec_heads;
-    pp.unit_cost = scaled ? unit_cost_q8(head_dim) : kUnitCostTiles;
+    pp.unit_cost = q8 ? unit_cost_q8(head_dim) : kUnitCostTiles;
     pp.dec_keys = dec_heads > 1 ? kDecodeKeysPerSplitGrouped : kDecodeKeysPerSplit;
     if (scaled) {
         const int64_t items = (num_reqs < num_tokens ? num_reqs : num_tokens) * (num_kv_heads / dec_heads);

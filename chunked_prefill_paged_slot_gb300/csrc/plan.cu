@@ -247,7 +247,7 @@ __device__ SplitChoice choose_split(const PlanParams &p, long long tiles, int sh
         c.split_prefill = false;
         c.clamped = true;
     }
-    if (c.split_prefill && shortest >= c.run && longest <= c.run + kCutCostTiles)
+    if (c.split_prefill && !cut_units(shortest, longest, c.run))
         c.split_prefill = false;
     return c;
 }

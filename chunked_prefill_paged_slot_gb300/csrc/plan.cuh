@@ -51,9 +51,22 @@ constexpr int kUnitCostTiles = CPSA_UNIT_COST_TILES;   // a unit's fixed cost, i
 // chunk of 512 19.6 us, at 2 687 and 25.7 (one prompt of 2000 tokens: 67.3 and 64.3 us);
 // with 64 columns six prompts of 1187 tokens (14/2 heads) take 86.8 us at 3, 84.1 at 2.
 __host__ __device__ constexpr int unit_cost_q8(int head_dim) { return head_dim == 128 ? 3 : kUnitCostTiles; }
+// Over the 4-bit cache, whose Q is there ahead of its item, it costs no more than elsewhere. Only a
+// batch of one request with so little to do that its runs have their least length counts more: its
+// units are then at least a run long each, and stay whole, one a run (a fresh chunk of 512 tokens at
+// 32/8 heads 19.2 us, 23.7 at 2; of 64 tokens 13.0 and 17.5; eight fresh prompts of up to 2600
+// tokens 444 us at 2, 456 at 3).
+constexpr int kUnitCostQ4Few = 3;
+static_assert(kUnitCostQ4Few + 1 >= kMinRunTiles, "a unit of one tile is a run long");
 static_assert(unit_cost_q8(128) < kMinRunTiles, "a run must hold more than one unit's start");
 static_assert(kUnitCostTiles >= 0 && kUnitCostTiles < kMinRunTiles, "a run must hold more than one unit's start");
 constexpr int kCutCostTiles = 6;            // a run's extra item and merge when a unit is cut, in KV tiles
+// Whether run boundaries cut units: not where every unit is at least a run long and the longest
+// within a few tiles of it.
+__host__ __device__ constexpr bool cut_units(long long shortest, long long longest, long long run)
+{
+    return !(shortest >= run && longest <= run + kCutCostTiles);
+}
 constexpr int kMaxChunkGrid = 256;          // upper bound of the chunk kernel's grid (SMs)
 constexpr int kDecodeChunk = 64;            // keys per decode pipeline stage
 constexpr int kDecodeKeysPerSplit = 4096;   // keys per decode split (multiple of kDecodeChunk)
