@@ -802,7 +802,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             const uint32_t rows = (uint32_t)decode_q8_box_rows(page_size, dec_heads);
             if (q4) {
                 if (!make_maps_q4(&maps, c4, head_dim, page_size, num_kv_heads, num_pages,
-                                  (uint32_t)decode_q4_box_rows(page_size, dec_heads, group), (uint32_t)dec_heads) ||
+                                  (uint32_t)decode_q4_box_rows(head_dim, page_size, dec_heads, group), (uint32_t)dec_heads) ||
                     launch_decode_q4(dp, c4, maps, head_dim, dec_heads, grid_d, s, early) != cudaSuccess)
                     return CPSA_ERR_CUDA;
             } else if (!make_map_q8(&tk, k_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||

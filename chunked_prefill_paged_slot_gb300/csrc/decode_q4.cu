@@ -40,25 +40,26 @@ namespace {
 
 constexpr int kP2 = 7;   // probabilities are held times 2^kP2
 
-template <int D, int HG, bool HI>
+// ROWS: q heads per kv head that a warp has room for: 4, 8 or 16.
+template <int D, int HG, int ROWS>
 struct Q4DecCfg {
     static constexpr int kParts = 8 / HG;                 // warps per head
-    // keys of a stage per warp: 64, 32 where a stage would have over 32 boxes or the scores of 16
-    // heads would spill
-    static constexpr int WK = HG == 1 || HI ? 32 : 64;
-    static constexpr int kKeys = WK * kParts;             // keys per stage
     static constexpr int kRow = D / 2, kScRow = D / kQ4Group;   // bytes of a row's codes and scales
+    static constexpr int kMergeFloats = kParts == 1 ? 0 : 4 * ROWS * (D + 2);
+    // keys of a stage per warp: 64 (384 rows of 1024 to 8192 keys, 32/8 heads: 371 us, 401 us at 32);
+    // 32 where a stage would have over 32 boxes, the scores of 16 heads would spill, or only two
+    // stages would fit beside the merge
+    static constexpr int WK = HG == 1 || ROWS == 16 || (D == 128 && kParts > 1 && ROWS > 4) ? 32 : 64;
+    static constexpr int kKeys = WK * kParts;             // keys per stage
     static constexpr int kTileBytes = kKeys * HG * kRow;  // codes of K (or V) of one stage
     static constexpr int kScTile = 4096;                  // its scales, in boxes of at least 128 bytes
     static constexpr int kStageBytes = 2 * (kTileBytes + kScTile);
-    static constexpr int kRows = HI ? 16 : 8;             // q rows kept per warp
-    static constexpr int kMergeFloats = kParts == 1 ? 0 : 8 * kRows * (D + 2);
     static constexpr int kRoom = (232448 - 1024 - 256 - 4 * kMergeFloats) / kStageBytes;
     static constexpr int kStages = kRoom < 6 ? kRoom : 6;
     static constexpr int kMergeOff = kStages * kStageBytes;
     static constexpr int kBarOff = kMergeOff + 4 * kMergeFloats;
     static constexpr int kSmemBytes = kBarOff + 256 + 1024;
-    static_assert(kSmemBytes <= 232448 && kStages >= 2, "beyond the 227 KB of shared memory a CTA may have");
+    static_assert(kSmemBytes <= 232448 && kStages >= 3, "beyond the 227 KB of shared memory a CTA may have");
     static_assert(kKeys * HG * kScRow <= kScTile, "a stage's scales");
     static constexpr int kThreads = 288;
 };
@@ -125,17 +126,18 @@ __device__ __forceinline__ int chi(int g)
     return D == 128 ? ((g & 1) | (g & 2) << 1 | (g & 4) >> 1) : g;
 }
 
-template <int D, int HG, bool HI>
+template <int D, int HG, int ROWS>
 __global__ void __launch_bounds__(288, 1)
 decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
                  const __grid_constant__ CUtensorMap tm_vs)
 {
-    using C = Q4DecCfg<D, HG, HI>;
+    using C = Q4DecCfg<D, HG, ROWS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     Q4DecBars *bars = reinterpret_cast<Q4DecBars *>(smem + C::kBarOff);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (one value a warp, which keeps the arithmetic on it off the lanes)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int G = p.group;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -232,7 +234,7 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
     }
 
     // ---------------------------------------------------------------- consumers
-    constexpr int NH = HI ? 2 : 1;             // n tiles of eight q heads
+    constexpr int NH = ROWS == 16 ? 2 : 1;             // n tiles of eight q heads
     constexpr int KS = D / 16;                 // k steps of a score
     constexpr int MT = D / 16;                 // m tiles of the output
     constexpr int R8 = C::WK / 8;              // eights of a warp's keys
@@ -327,32 +329,33 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                 for (int mt = 0; mt < R8 / 2; ++mt)
 #pragma unroll
                     for (int nh = 0; nh < NH; ++nh) s[mt][nh][0] = s[mt][nh][1] = s[mt][nh][2] = s[mt][nh][3] = 0.f;
+                // the m tiles in turn, so that no mma waits for the one right before it
+                uint32_t x[R8][KW], sc[R8];
 #pragma unroll
-                for (int mt = 0; mt < R8 / 2; ++mt) {
-                    uint32_t x[2][KW], sc[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if (D == 128) {
-                            const uint4 v = lds128(row8[2 * mt + b] + k_off);
-                            x[b][0] = v.x;
-                            x[b][1] = v.y;
-                            x[b][2 % KW] = v.z;
-                            x[b][3 % KW] = v.w;
-                            sc[b] = lds_u16(sc8[2 * mt + b] + ks_off);
-                        } else {
-                            const uint2 v = lds64(row8[2 * mt + b] + k_off);
-                            x[b][0] = v.x;
-                            x[b][1] = v.y;
-                            sc[b] = lds8(sc8[2 * mt + b] + ks_off);
-                        }
+                for (int r8 = 0; r8 < R8; ++r8) {
+                    if (D == 128) {
+                        const uint4 v = lds128(row8[r8] + k_off);
+                        x[r8][0] = v.x;
+                        x[r8][1] = v.y;
+                        x[r8][2 % KW] = v.z;
+                        x[r8][3 % KW] = v.w;
+                        sc[r8] = lds_u16(sc8[r8] + ks_off);
+                    } else {
+                        const uint2 v = lds64(row8[r8] + k_off);
+                        x[r8][0] = v.x;
+                        x[r8][1] = v.y;
+                        sc[r8] = lds8(sc8[r8] + ks_off);
                     }
+                }
 #pragma unroll
-                    for (int k = 0; k < KW; ++k) {
+                for (int k = 0; k < KW; ++k)
+#pragma unroll
+                    for (int mt = 0; mt < R8 / 2; ++mt) {
                         uint32_t f[2][4];
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const uint32_t sf = q4_scale2(k < 2 ? sc[b] & 0xffu : sc[b] >> 8);
-                            e2m1x8(x[b][k], f[b]);
+                            const uint32_t sf = q4_scale2(k < 2 ? sc[2 * mt + b] & 0xffu : sc[2 * mt + b] >> 8);
+                            e2m1x8(x[2 * mt + b][k], f[b]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) f[b][i] = q4_mul(f[b][i], sf);
                         }
@@ -364,7 +367,6 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                                 mma_f16(s[mt][nh], a, qb[2 * k + i][nh][0], qb[2 * k + i][nh][1]);
                         }
                     }
-                }
                 // keys behind the last one
                 if (nv < C::WK) {
 #pragma unroll
@@ -495,7 +497,63 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) l_run[nh][e] += __shfl_xor_sync(0xffffffffu, l_run[nh][e], x);
-        if constexpr (C::kParts == 1) {
+        if constexpr (C::kParts > 1) {
+            // the warps of a head meet by halves: the upper ones leave their maximum, sum and O in
+            // shared memory, the lower ones take them in, until one is left
+            float *mm = reinterpret_cast<float *>(smem + C::kMergeOff);
+            float *ll = mm + 4 * ROWS;
+            float *oo = ll + 4 * ROWS;
+#pragma unroll
+            for (int half = C::kParts / 2; half >= 1; half /= 2) {
+                const int at = (part % half) * HG + h;      // of a pair of warps
+                if (part >= half && part < 2 * half) {
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 2 * t + e + 8 * nh;
+                            if (row >= G)
+                                continue;
+                            if (g == 0) {
+                                mm[at * ROWS + row] = m_run[nh][e];
+                                ll[at * ROWS + row] = l_run[nh][e];
+                            }
+                            float *dst = oo + (at * ROWS + row) * D + col0;
+#pragma unroll
+                            for (int j = 0; j < MT; j += 2)
+                                *reinterpret_cast<float4 *>(dst + 2 * j) =
+                                    make_float4(o[j][nh][e], o[j][nh][2 + e], o[j + 1][nh][e], o[j + 1][nh][2 + e]);
+                        }
+                }
+                named_bar_sync(1, 256);
+                if (part < half) {
+#pragma unroll
+                    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 2 * t + e + 8 * nh;
+                            if (row >= G)
+                                continue;
+                            const float m2 = mm[at * ROWS + row], M = fmaxf(m_run[nh][e], m2);
+                            const float Mref = M == -INFINITY ? 0.f : M;
+                            const float f1 = ex2_approx(m_run[nh][e] - Mref), f2 = ex2_approx(m2 - Mref);
+                            m_run[nh][e] = M;
+                            l_run[nh][e] = f1 * l_run[nh][e] + f2 * ll[at * ROWS + row];
+                            const float *src = oo + (at * ROWS + row) * D + col0;
+#pragma unroll
+                            for (int j = 0; j < MT; j += 2) {
+                                const float4 x = *reinterpret_cast<const float4 *>(src + 2 * j);
+                                o[j][nh][e] = f1 * o[j][nh][e] + f2 * x.x;
+                                o[j][nh][2 + e] = f1 * o[j][nh][2 + e] + f2 * x.y;
+                                o[j + 1][nh][e] = f1 * o[j + 1][nh][e] + f2 * x.z;
+                                o[j + 1][nh][2 + e] = f1 * o[j + 1][nh][2 + e] + f2 * x.w;
+                            }
+                        }
+                }
+                named_bar_sync(1, 256);
+            }
+        }
+        if (part == 0) {
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -527,67 +585,18 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                         }
                     }
                 }
-        } else {
-            // the warps of a head meet: [warp][row] max and sum, [warp][row][D] O
-            float *mm = reinterpret_cast<float *>(smem + C::kMergeOff);
-            float *ll = mm + 8 * C::kRows;
-            float *oo = ll + 8 * C::kRows;
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = 2 * t + e + 8 * nh;
-                    if (row >= G)
-                        continue;
-                    if (g == 0) {
-                        mm[warp * C::kRows + row] = m_run[nh][e];
-                        ll[warp * C::kRows + row] = l_run[nh][e];
-                    }
-                    float *dst = oo + (warp * C::kRows + row) * D + col0;
-#pragma unroll
-                    for (int j = 0; j < MT; j += 2)
-                        *reinterpret_cast<float4 *>(dst + 2 * j) =
-                            make_float4(o[j][nh][e], o[j][nh][2 + e], o[j + 1][nh][e], o[j + 1][nh][2 + e]);
-                }
-            named_bar_sync(1, 256);
-            for (int e = threadIdx.x; e < HG * G * D; e += 256) {
-                const int hh = e / (G * D), row = e / D % G, d = e % D;
-                float M = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < C::kParts; ++x) M = fmaxf(M, mm[(x * HG + hh) * C::kRows + row]);
-                const float Mref = M == -INFINITY ? 0.f : M;
-                float L = 0.f, acc = 0.f;
-#pragma unroll
-                for (int x = 0; x < C::kParts; ++x) {
-                    const int at = (x * HG + hh) * C::kRows + row;
-                    const float f = ex2_approx(mm[at] - Mref);
-                    L += f * ll[at];
-                    acc += f * oo[at * D + d];
-                }
-                const int hq = (w.kvh * HG + hh) * G + row;
-                if (w.nsplit > 1) {
-                    const int64_t pr = (int64_t)w.pbase + (int64_t)hq * w.nsplit + w.split;
-                    p.part_o[pr * D + d] = acc;
-                    if (d == 0)
-                        reinterpret_cast<float2 *>(p.part_ml)[pr] = make_float2(M, L);
-                } else {
-                    reinterpret_cast<__nv_bfloat16 *>(p.out)[((int64_t)w.t * p.num_q_heads + hq) * D + d] =
-                        __float2bfloat16_rn(acc * (L > 0.f ? 1.f / L : 0.f));
-                }
-            }
-            named_bar_sync(1, 256);
         }
     }
     if (threadIdx.x == 0 && *abort)
         set_dev_error(p.dev_err, CPSA_DEV_WAIT_TIMEOUT);
 }
 
-template <int D, int HG, bool HI>
+template <int D, int HG, int ROWS>
 cudaError_t launch_t(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, int grid, cudaStream_t s, bool early)
 {
-    using C = Q4DecCfg<D, HG, HI>;
+    using C = Q4DecCfg<D, HG, ROWS>;
     static std::atomic<uint64_t> done{0};
-    auto k = decode_q4_kernel<D, HG, HI>;
+    auto k = decode_q4_kernel<D, HG, ROWS>;
     return launch_with_smem(done, reinterpret_cast<const void *>(k), C::kSmemBytes, [&] {
         return launch_pdl(early, k, dim3(grid), dim3(C::kThreads), C::kSmemBytes, s, p, c, m.k, m.v, m.ks, m.vs);
     });
@@ -596,7 +605,11 @@ cudaError_t launch_t(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, i
 template <int D, int HG>
 cudaError_t launch_hg(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, int grid, cudaStream_t s, bool early)
 {
-    return p.group > 8 ? launch_t<D, HG, true>(p, c, m, grid, s, early) : launch_t<D, HG, false>(p, c, m, grid, s, early);
+    if (p.group > 8)
+        return launch_t<D, HG, 16>(p, c, m, grid, s, early);
+    // all of a page's heads to a warp each: nothing to merge, and no room to keep for it
+    return p.group > 4 || HG == 8 ? launch_t<D, HG, 8>(p, c, m, grid, s, early)
+                                  : launch_t<D, HG, HG == 8 ? 8 : 4>(p, c, m, grid, s, early);
 }
 
 template <int D>
@@ -611,8 +624,22 @@ cudaError_t launch_d(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, i
     }
 }
 
-template <int HG>
-int stage_keys(int group) { return group > 8 ? Q4DecCfg<128, HG, true>::kKeys : Q4DecCfg<128, HG, false>::kKeys; }
+template <int D, int HG>
+int stage_keys(int group)
+{
+    return group > 8   ? Q4DecCfg<D, HG, 16>::kKeys
+           : group > 4 ? Q4DecCfg<D, HG, 8>::kKeys
+                       : Q4DecCfg<D, HG, HG == 8 ? 8 : 4>::kKeys;
+}
+
+template <int D>
+int stage_keys(int heads, int group)
+{
+    return heads == 8   ? stage_keys<D, 8>(group)
+           : heads == 4 ? stage_keys<D, 4>(group)
+           : heads == 2 ? stage_keys<D, 2>(group)
+                        : stage_keys<D, 1>(group);
+}
 
 }  // namespace
 
@@ -624,12 +651,9 @@ cudaError_t launch_decode_q4(const DecodeParams &p, const Q4Cache &c, const Q4Ma
 }
 
 // Rows per TMA box of the decode kernel (abi.cu builds the maps with it).
-int decode_q4_box_rows(int page_size, int heads_per_item, int group)
+int decode_q4_box_rows(int head_dim, int page_size, int heads_per_item, int group)
 {
-    const int keys = heads_per_item == 8   ? stage_keys<8>(group)
-                     : heads_per_item == 4 ? stage_keys<4>(group)
-                     : heads_per_item == 2 ? stage_keys<2>(group)
-                                           : stage_keys<1>(group);
+    const int keys = head_dim == 128 ? stage_keys<128>(heads_per_item, group) : stage_keys<64>(heads_per_item, group);
     const int rows = page_size < keys ? page_size : keys;
     return rows < 64 ? rows : 64;
 }

@@ -168,7 +168,7 @@ struct Q4Maps {
 };
 cudaError_t launch_decode_q4(const DecodeParams &p, const Q4Cache &c, const Q4Maps &m, int head_dim,
                              int heads_per_item, int grid, cudaStream_t s, bool early);
-int decode_q4_box_rows(int page_size, int heads_per_item, int group);
+int decode_q4_box_rows(int head_dim, int page_size, int heads_per_item, int group);
 cudaError_t launch_rope_append(const RopeParams &p, int head_dim, int bits, int num_sms, cudaStream_t s);
 cudaError_t launch_read_q4(const ReadQ4Params &p, int head_dim, cudaStream_t s);
 cudaError_t launch_split_microbatch(const int32_t *query_lens, int num_reqs, float balance_threshold,
