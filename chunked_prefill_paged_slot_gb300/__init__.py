@@ -25,7 +25,7 @@ this package is its Python binding plus host-side orchestration:
   BatchScheduler            token-budget batch builder with page allocation
   AttentionStep             one step (KV write + attention) with its workspace,
                             on one stream or as two micro-batches on two streams,
-                            with rotary positions and over an 8-bit cache where asked
+                            with head norms, rotary positions and over an 8-bit or 4-bit cache where asked
   rope_table                cosines and sines for the rotary appends
 """
 from ._lib import (  # noqa: F401

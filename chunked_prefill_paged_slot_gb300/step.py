@@ -28,25 +28,39 @@ def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, devic
 
 
 class AttentionStep:
-    """kv_dtype: torch.bfloat16, or torch.float8_e4m3fn for an 8-bit cache (run then takes its k_scale and v_scale).
+    """kv_dtype: torch.bfloat16, or torch.float8_e4m3fn for an 8-bit cache, torch.float4_e2m1fn_x2 for a 4-bit one (run
+    then takes its k_scale and v_scale).
     rope: a cos_sin table (see rope_table): q and k are then rotated by `positions` on their way (q into the step's own
-    buffer, k into the cache), and q, k and v may be slices of one projection's output."""
+    buffer, k into the cache), and q, k and v may be slices of one projection's output.
+    q_norm, k_norm: fp32 [head_dim] weights of an RMS norm of every q and k head, on their way too, before the rotation;
+    norm_eps: what is added to the mean square."""
+
+    q4 = False
+    norm = None
 
     def __init__(self, num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  max_kv_splits: int = 8, device=None, workspace_bytes: int | None = None,
                  two_stream: bool = False, balance_threshold: float = 0.1, length_threshold: int = 256,
                  fused_kv_write: bool = False, kv_dtype: torch.dtype = torch.bfloat16,
-                 rope: torch.Tensor | None = None, rope_interleaved: bool = False):
-        if kv_dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-            raise _lib.CpsaError(f"AttentionStep: kv_dtype must be torch.bfloat16 or torch.float8_e4m3fn, got {kv_dtype}")
-        if fused_kv_write and (rope is not None or kv_dtype != torch.bfloat16):
-            raise _lib.CpsaError("AttentionStep: the KV write fuses into the attention of a bf16 cache without rotation")
+                 rope: torch.Tensor | None = None, rope_interleaved: bool = False,
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, norm_eps: float = 1e-6):
+        if kv_dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.float4_e2m1fn_x2):
+            raise _lib.CpsaError("AttentionStep: kv_dtype must be torch.bfloat16, torch.float8_e4m3fn or "
+                                 f"torch.float4_e2m1fn_x2, got {kv_dtype}")
+        if (q_norm is None) != (k_norm is None):
+            raise _lib.CpsaError("AttentionStep: q_norm and k_norm go together")
+        if fused_kv_write and (rope is not None or q_norm is not None or kv_dtype != torch.bfloat16):
+            raise _lib.CpsaError("AttentionStep: the KV write fuses into the attention of a bf16 cache without rotation "
+                                 "and head norms")
         device = torch.device(device if device is not None else "cuda")
         self.q8 = kv_dtype == torch.float8_e4m3fn
+        self.q4 = kv_dtype == torch.float4_e2m1fn_x2
         self.rope = rope
         self.rope_interleaved = rope_interleaved
-        self.q_rot = None if rope is None else torch.empty((num_tokens, num_q_heads, head_dim), dtype=torch.bfloat16,
-                                                           device=device)
+        self.norm = None if q_norm is None else (q_norm, k_norm)
+        self.norm_eps = norm_eps
+        self.q_rot = None if rope is None and q_norm is None else torch.empty((num_tokens, num_q_heads, head_dim),
+                                                                              dtype=torch.bfloat16, device=device)
         self.fused_kv_write = fused_kv_write
         self.dims = (num_q_heads, num_kv_heads, head_dim)
         self.max_kv_splits = max_kv_splits
@@ -65,13 +79,15 @@ class AttentionStep:
 
     def run(self, q, k, v, slot_mapping, k_cache, v_cache, query_lens, seq_lens, block_table, out,
             scale: float = 0.0, stream=None, workspace=None, positions=None, k_scale=None, v_scale=None, q_rot=None):
-        """KV write of the new tokens (rotated, or into 8 bits, when the step was built so), then attention, on one
-        stream. positions: int64 [T], with rope; k_scale, v_scale: the 8-bit cache's; q_rot: where the rotated q goes
-        (the step's own buffer)."""
+        """KV write of the new tokens (normed, rotated, into 8 or 4 bits, when the step was built so), then attention,
+        on one stream. positions: int64 [T], with rope; k_scale, v_scale: the 8-bit or 4-bit cache's; q_rot: where the
+        normed and rotated q goes (the step's own buffer)."""
         if (self.rope is None) != (positions is None):
             raise _lib.CpsaError("AttentionStep.run: positions go with a step built with rope, and only with it")
-        if self.q8 != (k_scale is not None) or self.q8 != (v_scale is not None):
-            raise _lib.CpsaError("AttentionStep.run: k_scale and v_scale go with a step of an 8-bit cache, and only with it")
+        scaled = self.q8 or self.q4
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise _lib.CpsaError("AttentionStep.run: k_scale and v_scale go with a step of an 8-bit or 4-bit cache, and "
+                                 "only with it")
         ws = self.workspaces[0] if workspace is None else workspace
         if self.fused_kv_write:
             _lib.cpp_chunked_prefill_attn_write_kv(q, k, v, slot_mapping, k_cache, v_cache, query_lens, seq_lens,
@@ -79,22 +95,29 @@ class AttentionStep:
                                                    max_kv_splits=self.max_kv_splits, stream=stream)
             return
         q_in = None
-        if self.rope is not None:
+        if self.rope is not None or self.norm is not None:
             q_in = q
             q = self.q_rot[:q.shape[0]] if q_rot is None else q_rot
-        if self.q8:
-            _lib.cpp_rope_kv_cache_write_q8(q_in, k, v, positions, self.rope, slot_mapping, k_cache, v_cache, k_scale,
-                                            v_scale, q if q_in is not None else None, self.dev_err,
-                                            interleaved=self.rope_interleaved, stream=stream)
-            _lib.cpp_chunked_prefill_attn_q8(q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table,
-                                             out, ws, self.dev_err, scale=scale, max_kv_splits=self.max_kv_splits,
-                                             stream=stream)
-            return
-        if q_in is not None:
+        if self.norm is not None:
+            caches = (k_cache, v_cache) + ((k_scale, v_scale) if scaled else ())
+            write = (_lib.cpp_norm_rope_kv_cache_write_q4 if self.q4 else _lib.cpp_norm_rope_kv_cache_write_q8 if self.q8
+                     else _lib.cpp_norm_rope_kv_cache_write)
+            write(q_in, k, v, *self.norm, positions, self.rope, slot_mapping, *caches, q, self.dev_err,
+                  eps=self.norm_eps, interleaved=self.rope_interleaved, stream=stream)
+        elif scaled:
+            write = _lib.cpp_rope_kv_cache_write_q4 if self.q4 else _lib.cpp_rope_kv_cache_write_q8
+            write(q_in, k, v, positions, self.rope, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                  q if q_in is not None else None, self.dev_err, interleaved=self.rope_interleaved, stream=stream)
+        elif q_in is not None:
             _lib.cpp_rope_kv_cache_write(q_in, k, v, positions, self.rope, slot_mapping, k_cache, v_cache, q,
                                          self.dev_err, interleaved=self.rope_interleaved, stream=stream)
         else:
             _lib.cpp_kv_cache_write(k, v, slot_mapping, k_cache, v_cache, self.dev_err, stream=stream)
+        if scaled:
+            attend = _lib.cpp_chunked_prefill_attn_q4 if self.q4 else _lib.cpp_chunked_prefill_attn_q8
+            attend(q, k_cache, v_cache, k_scale, v_scale, query_lens, seq_lens, block_table, out, ws, self.dev_err,
+                   scale=scale, max_kv_splits=self.max_kv_splits, stream=stream)
+            return
         _lib.cpp_chunked_prefill_attn(q, k_cache, v_cache, query_lens, seq_lens, block_table, out, ws,
                                       self.dev_err, scale=scale, max_kv_splits=self.max_kv_splits, stream=stream)
 
