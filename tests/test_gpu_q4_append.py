@@ -3,8 +3,9 @@
 Tolerances before a value's one rounding to its output's type (fp32 roundings are half steps of 2^-24):
   rotated          2^-22 (|a| + |b|), as in test_gpu_rope_append.py
   head norm        the sum of squares of positive terms passes at most 16 / 2 + 1 + 3 + 1 additions and a division by
-                   head_dim (exact), eps is one more: 14 * 2^-24 of it, halved by the root; root, reciprocal and the two
-                   products round once each: 11 * 2^-24 < 2^-20 of the value, and with its rotation 2^-20 (|a| + |b|)
+                   head_dim (exact), eps is one more: 14 * 2^-24 of it, halved by the root; the reciprocal root is off
+                   by at most two last places, 4 * 2^-24, and the two products round once each: 13 * 2^-24 < 2^-20 of
+                   the value, and with its rotation's 3 * 2^-24 at most 2^-20 (|a| + |b|)
 What is neither normed nor rotated is exact before its rounding, and then codes and scales are those of the definition.
 bf16 adds half a step, 2^-8 of the value; 4 bits: q4_helpers.check_group_values.
 """
