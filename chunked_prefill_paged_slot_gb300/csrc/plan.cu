@@ -16,8 +16,8 @@
 // choose_split). Pass 2 walks the requests in chunks of 1024: one block scan
 // gives each request its token and tile offsets, a second its list offsets, and
 // a warp per request then writes that request's entries. Batches of at most 32
-// requests and 8192 tokens (or of one request) take a one-warp kernel that
-// builds the same lists without block barriers.
+// requests, 8192 tokens and some 400 units (or of one request) take a one-warp kernel
+// that builds the same lists without block barriers.
 #include "common.cuh"
 #include "plan.cuh"
 
@@ -26,6 +26,7 @@ namespace cpsa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+static_assert(kPlanThreads == 32 * 32, "the block's scans and totals are of 32 warps, a lane each");
 constexpr int kScan = 6;
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -691,12 +692,16 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
 // The one-warp kernel walks every request's units itself (about 0.5 us per 32
 // units: 166 us for 32 prompts of 2600 tokens at 32/8 heads), the block kernel
 // gives each request a warp of its own but pays its barriers: one warp while
-// the lists are short or there is one request to walk.
-constexpr int64_t kPlanSmallMaxTokens = 8192;
+// the lists are short or there is one request to walk. (Over the 4-bit cache at 14/2
+// heads, D 64: six ragged prompts of 1187 tokens, about 600 units, 73.7 us by one warp and 68.6 by
+// the block, two of them, 240 units, 43.9 and 47.6.)
+constexpr int64_t kPlanSmallMaxTokens = 8192, kPlanSmallMaxUnits = 400;
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s, bool early)
 {
-    if (p.num_reqs <= 32 && (p.num_reqs == 1 || p.num_tokens <= kPlanSmallMaxTokens))
+    const int64_t units = p.num_tokens / kTileM * p.Hkv * (p.group / p.nq);   // about
+    if (p.num_reqs <= 32 &&
+        (p.num_reqs == 1 || (p.num_tokens <= kPlanSmallMaxTokens && units <= kPlanSmallMaxUnits)))
         return launch_pdl(early, plan_small_kernel, dim3(1), dim3(32), 0, s, p);
     return launch_pdl(early, plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
 }
