@@ -719,8 +719,10 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     const bool single_decode = num_reqs == 1 && num_tokens == 1;
     const bool self_plan = single_prefill && self_plan_fits(num_tokens, num_kv_heads * (group / nq), pp.chunk_grid,
                                                             scaled ? kSelfPlanCapQ8 : kSelfPlanCap, pp.unit_cost);
+    // So does a single decode row over the 4-bit cache.
+    const bool self_row = q4 && single_decode;
     mark(0, s);
-    if (!self_plan && launch_plan(pp, s, false) != cudaSuccess)
+    if (!self_plan && !self_row && launch_plan(pp, s, false) != cudaSuccess)
         return CPSA_ERR_CUDA;
     mark(1, s);
 
@@ -794,8 +796,15 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             dp.q = q;
             dp.k_cache_ptr = k_cache;
             dp.v_cache_ptr = v_cache;
-            dp.run_first = pp.dec_stream ? pp.dec_first : nullptr;
-            const int grid_d = pp.dec_stream ? pp.dec_grid : (int)(L.max_ditems < sms ? L.max_ditems : sms);
+            dp.run_first = pp.dec_stream && !self_row ? pp.dec_first : nullptr;
+            // the plan's rule (plan.cu: choose_split): partial rows for every split the row can have
+            dp.self_plan = self_row ? 1 : 0;
+            dp.dec_keys = pp.dec_keys;
+            dp.split_clamped = max_kv_splits > 1 && cap < (int64_t)num_q_heads * max_kv_splits ? 1 : 0;
+            dp.max_splits = dp.split_clamped ? 1 : max_kv_splits;
+            dp.counts_w = counts;
+            dp.citems_w = citems;
+            const int grid_d = pp.dec_stream && !self_row ? pp.dec_grid : (int)(L.max_ditems < sms ? L.max_ditems : sms);
             CUtensorMap tk, tv;
             Q4Maps maps;
             const Q4Cache c4{c.k, c.v, c.ks, c.vs, c.lg_page};
@@ -803,7 +812,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             if (q4) {
                 if (!make_maps_q4(&maps, c4, head_dim, page_size, num_kv_heads, num_pages,
                                   (uint32_t)decode_q4_box_rows(head_dim, page_size, dec_heads, group), (uint32_t)dec_heads) ||
-                    launch_decode_q4(dp, c4, maps, head_dim, dec_heads, grid_d, s, early) != cudaSuccess)
+                    launch_decode_q4(dp, c4, maps, head_dim, dec_heads, grid_d, s, early && !self_row) != cudaSuccess)
                     return CPSA_ERR_CUDA;
             } else if (!make_map_q8(&tk, k_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||
                        !make_map_q8(&tv, v_cache, head_dim, page_size, num_kv_heads, num_pages, rows, dec_heads) ||

@@ -126,6 +126,47 @@ __device__ __forceinline__ int chi(int g)
     return D == 128 ? ((g & 1) | (g & 2) << 1 | (g & 4) >> 1) : g;
 }
 
+// The items of a batch of one decode row: the plan's (plan.cu: decode_splits, request_work).
+struct OneRow {
+    int s, splits, items;   // keys; splits; items (0: nothing to do)
+    __device__ __forceinline__ DecodeItem item(int k, int ngroups) const
+    {
+        const int sp = k / ngroups, tiles = (s + kDecodeChunk - 1) / kDecodeChunk;
+        const int c0 = sp * tiles / splits, c1 = (sp + 1) * tiles / splits;
+        return DecodeItem{0, k - sp * ngroups, c0 * kDecodeChunk, min(c1 * kDecodeChunk, s), sp, splits,
+                          splits > 1 ? 0 : -1, 0};
+    }
+};
+
+// The row's checks and splits; CTA 0 reports, and leaves the combine kernel its list.
+template <int HG>
+__device__ __forceinline__ OneRow one_row(const DecodeParams &p)
+{
+    const int q = __ldg(p.query_lens), s = __ldg(p.seq_lens);
+    uint32_t bad = 0;
+    if (q != 1)
+        bad = CPSA_DEV_TOKENS_MISMATCH;
+    else if (s < 1)
+        bad = CPSA_DEV_SEQ_LT_QUERY;
+    else if ((int64_t)s > (int64_t)p.max_blocks * p.page_size)
+        bad = CPSA_DEV_SEQ_GT_TABLE;
+    OneRow row{s, 1, 0};
+    if (!bad) {
+        row.splits = max(1, min(min((s + p.dec_keys - 1) / p.dec_keys, p.max_splits), (s + kDecodeChunk - 1) / kDecodeChunk));
+        row.items = row.splits * (p.num_kv_heads / HG);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (bad || p.split_clamped)
+            set_dev_error(p.dev_err, bad | (p.split_clamped ? CPSA_DEV_SPLITS_CLAMPED : 0u));
+        const bool merge = row.splits > 1;
+        if (merge)
+            p.citems_w[0] = CombineItem{0, 1, 0, p.num_q_heads, 0, row.splits, 0, 0};
+        p.counts_w[kCntCombine] = merge ? 1 : 0;
+        p.counts_w[kCntCombineUnits] = merge ? p.num_q_heads : 0;
+    }
+    return row;
+}
+
 template <int D, int HG, int ROWS>
 __global__ void __launch_bounds__(288, 1)
 decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constant__ CUtensorMap tm_k,
@@ -149,11 +190,13 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
     }
     pdl_trigger();
     pdl_wait();
-    // this CTA's items: a run of the plan's list, or every gridDim.x-th
+    // this CTA's items: a run of the plan's list, or every gridDim.x-th of it or of the row's own
     const bool runs = p.run_first != nullptr;
+    const OneRow row = p.self_plan ? one_row<HG>(p) : OneRow{0, 0, 0};
     const int it_begin = runs ? p.run_first[blockIdx.x] : blockIdx.x;
-    const int it_end = runs ? p.run_first[blockIdx.x + 1] : p.counts[kCntDecode];
+    const int it_end = p.self_plan ? row.items : runs ? p.run_first[blockIdx.x + 1] : p.counts[kCntDecode];
     const int it_step = runs ? 1 : gridDim.x;
+    auto item = [&](int it) -> DecodeItem { return p.self_plan ? row.item(it, p.num_kv_heads / HG) : p.ditems[it]; };
     __syncthreads();
     volatile int *abort = &bars->abort;
     // rows per box: within a page, and on the 64-key grid that items start on
@@ -175,11 +218,11 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
         bool stop = false;
         DecodeItem w_next{};
         if (it_begin < it_end)
-            w_next = p.ditems[it_begin];
+            w_next = item(it_begin);
         for (int it = it_begin; it < it_end && !stop && !warp_aborted(abort); it += it_step) {
             const DecodeItem w = w_next;
             if (it + it_step < it_end)
-                w_next = p.ditems[it + it_step];
+                w_next = item(it + it_step);
             const int32_t *bt_row = p.block_table + (int64_t)w.r * p.max_blocks;
             const int head0 = w.kvh * HG;
             const int nst = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
@@ -255,7 +298,7 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
     const uint32_t vs_off0 = vkey0 * C::kScRow + vs_piece, vs_off1 = vkey1 * C::kScRow + vs_piece;
     uint32_t gs = 0;
     for (int it = it_begin; it < it_end; it += it_step) {
-        const DecodeItem w = p.ditems[it];
+        const DecodeItem w = item(it);
         const int nst = (w.key1 - w.key0 + C::kKeys - 1) / C::kKeys;
         const int kvh = w.kvh * HG + h;
         // q head g (+ 8) as f16 under its own power of two; k step s of lane t covers

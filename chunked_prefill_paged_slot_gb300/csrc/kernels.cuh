@@ -73,7 +73,15 @@ struct ChunkParams : AttnCommon {
 
 struct DecodeParams : AttnCommon {
     const DecodeItem *ditems;
-    const int32_t *run_first;  // CTA c's items are [run_first[c], run_first[c + 1]) (4-bit cache only); nullptr: dealt round
+    // the 4-bit cache's kernel only:
+    const int32_t *run_first;  // CTA c's items are [run_first[c], run_first[c + 1]); nullptr: dealt round
+    // A batch of one decode row (self_plan != 0): no plan kernel ran; every CTA computes the row's
+    // items from query_lens[0] / seq_lens[0], and CTA 0 leaves the combine kernel its list.
+    int self_plan;
+    int max_splits, dec_keys;  // of the row's splits (max_splits = 1 where partials do not fit)
+    int split_clamped;         // that is the case
+    int32_t *counts_w;
+    CombineItem *citems_w;
     const void *q;             // bf16 [T][Hq][D]
     const void *k_cache_ptr;   // bf16 [pages][Hkv][P][D]
     const void *v_cache_ptr;

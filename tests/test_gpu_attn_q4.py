@@ -72,6 +72,39 @@ def test_small_workspace_clamps_the_splits(cuda_lib):
     check(cuda_lib, s, workspace_bytes=small, expect_flags=cuda_lib.DEV_SPLITS_CLAMPED)
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (64, 14, 2), (128, 24, 24), (128, 16, 1)])
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 128, 129, 1000, 5000])
+def test_one_row_plans_itself(cuda_lib, n, d, hq, hkv):
+    """One decode row: its splits, and one split where the workspace has no room for partial results."""
+    s = spec([n - 1], [1], hq, hkv, d, P=32, seed=720 + n)
+    for splits in (1, 3, 8, 32):
+        check(cuda_lib, s, max_kv_splits=splits)
+    small = cuda_lib.cpp_attn_workspace_min_bytes(1, 1, hq, hkv, d, 8)
+    check(cuda_lib, s, workspace_bytes=small, expect_flags=cuda_lib.DEV_SPLITS_CLAMPED)
+
+
+def test_one_row_that_is_refused_and_one_right_after(cuda_lib):
+    """A single decode row's lengths that cannot be: flagged, its output left alone; the workspace serves the next call."""
+    b, caches = draw(spec([700], [1], hq=8, hkv=2, seed=740))
+    kc, ks, vc, vs = (to_dev(x) for x in caches)
+    ws = torch.full((cuda_lib.cpp_attn_workspace_bytes(1, 1, 8, 2, 128, 8),), 0xAB, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((1, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    ref, vmax = reference(b, caches)
+    q, bt = to_dev_bf16(b.q), to_dev(b.block_table)
+    for ql, sl, want in ((2, 701, cuda_lib.DEV_TOKENS_MISMATCH), (0, 701, cuda_lib.DEV_TOKENS_MISMATCH),
+                         (1, 0, cuda_lib.DEV_SEQ_LT_QUERY), (1, 1 << 20, cuda_lib.DEV_SEQ_GT_TABLE), (1, 701, 0),
+                         (-3, 701, cuda_lib.DEV_TOKENS_MISMATCH), (1, -5, cuda_lib.DEV_SEQ_LT_QUERY)):
+        out.fill_(5.0)
+        lens = [torch.tensor([x], dtype=torch.int32, device="cuda") for x in (ql, sl)]
+        cuda_lib.cpp_chunked_prefill_attn_q4(q, kc, vc, ks, vs, *lens, bt, out, ws, err)
+        assert cuda_lib.cpp_read_device_error(err) == want
+        if want:
+            assert bool((out == 5.0).all())
+        else:
+            close(out.double().cpu().numpy(), ref, vmax)
+
+
 @pytest.mark.parametrize("scale", [0.02, 1.0])
 def test_custom_scale(cuda_lib, scale):
     check(cuda_lib, spec([300, 40, 90], [130, 70, 1], seed=800), scale=scale)
