@@ -293,6 +293,26 @@ def test_read(cuda_lib, T, P, d):
     assert cuda_lib.cpp_read_device_error(err) == (cuda_lib.DEV_SLOT_OUT_OF_RANGE if T > 2 else 0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_into_tensors_on_16_byte_boundaries(cuda_lib, d):
+    """k and v 16 bytes behind a 32-byte boundary: the same values, and nothing beside them."""
+    rng = np.random.default_rng(29)
+    T, hkv, P = 37, 2, 16
+    held = [torch.from_numpy(rng.integers(0, 227, (8, hkv, P, n)).astype(np.uint8)).cuda()
+            for n in (d // 2, d // 2, d // 16, d // 16)]
+    slots = torch.from_numpy(rng.integers(0, 8 * P, T)).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = T * hkv * d
+    whole = [torch.full((n + 16,), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    shifted = [x[8:8 + n].view(T, hkv, d) for x in whole]
+    plain = [torch.empty(T, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert all(x.data_ptr() % 32 == 16 for x in shifted)
+    cuda_lib.cpp_kv_cache_read_q4(*held, slots, *shifted, err)
+    cuda_lib.cpp_kv_cache_read_q4(*held, slots, *plain, err)
+    assert all(torch.equal(a, b) for a, b in zip(shifted, plain))
+    assert all(bool((x[:8] == 3).all()) and bool((x[8 + n:] == 3).all()) for x in whole)
+
+
 def test_q4_cache_beyond_32_bit_offsets(cuda_lib):
     P, hkv, d = 16, 8, 128
     pages = (1 << 32) // (P * hkv * d // 2) + 3
