@@ -601,8 +601,8 @@ int cpp_chunked_prefill_attn_write_kv_events(const void *q, const void *k, const
 
 namespace {
 
-// The attention call over a cache of `bits` a number (k_scale, v_scale: of 8 and 4); k_new != nullptr fuses the KV write (k_new, v_new,
-// slot_mapping non-null then).
+// The attention call over a cache of `bits` a number (k_scale, v_scale: of 8 and 4); k_new != nullptr fuses the KV
+// write (k_new, v_new, slot_mapping non-null then).
 int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t *slot_mapping, void *k_cache,
               void *v_cache, const int32_t *query_lens, const int32_t *seq_lens, const int32_t *block_table,
               int num_reqs, int64_t num_tokens, int max_blocks_per_req, int num_q_heads, int num_kv_heads,
@@ -790,7 +790,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
             return CPSA_ERR_CUDA;
         }
         if (!single_prefill) {
-            DecodeParams dp;
+            DecodeParams dp{};
             static_cast<AttnCommon &>(dp) = ac;
             dp.ditems = ditems;
             dp.q = q;
@@ -869,10 +869,9 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
         return CPSA_ERR_CUDA;
     mark(2, s);
 
-    DecodeParams dp;
+    DecodeParams dp{};
     static_cast<AttnCommon &>(dp) = ac;
     dp.ditems = ditems;
-    dp.run_first = nullptr;
     dp.q = q;
     dp.k_cache_ptr = k_cache;
     dp.v_cache_ptr = v_cache;

@@ -28,6 +28,14 @@
 // of each eight, the eighth chi(g) of the row, the two keys' codes brought into (key, key)
 // bytes by shifts and masks before they are converted. kappa and chi are such that the
 // loads of a warp are free of bank conflicts.
+//
+// Measured (32/8 heads, D 128, pages of 16): 384 rows of 1024 to 8192 keys, 2.03 GB, in 323 us,
+// 6.3 TB/s or 94 % of a plain copy's rate; 345 to 350 us a call with the plan, an empty chunk
+// launch and the combine, 338 us with every stage skipped. A stage of 72 KB takes an SM 1.6 us of
+// arithmetic (conversions, 16-bit multiplications and mma.sync, two of eight warps a scheduler)
+// and 1.7 us of HBM's share; 16 warps or the scores of one stage beside the output of the one
+// before took longer (407 and 402 us), a warp number that the compiler knows to be one per
+// warp, whose arithmetic then leaves the lanes, took 371 us to 350.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "plan.cuh"
