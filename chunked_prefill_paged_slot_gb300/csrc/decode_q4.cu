@@ -29,13 +29,11 @@
 // bytes by shifts and masks before they are converted. kappa and chi are such that the
 // loads of a warp are free of bank conflicts.
 //
-// Measured (32/8 heads, D 128, pages of 16): 384 rows of 1024 to 8192 keys, 2.03 GB, in 323 us,
-// 6.3 TB/s or 94 % of a plain copy's rate; 345 to 350 us a call with the plan, an empty chunk
-// launch and the combine, 338 us with every stage skipped. A stage of 72 KB takes an SM 1.6 us of
-// arithmetic (conversions, 16-bit multiplications and mma.sync, two of eight warps a scheduler)
-// and 1.7 us of HBM's share; 16 warps or the scores of one stage beside the output of the one
-// before took longer (407 and 402 us), a warp number that the compiler knows to be one per
-// warp, whose arithmetic then leaves the lanes, took 371 us to 350.
+// Measured (32/8 heads, D 128, pages of 16): 384 rows of 1024 to 8192 keys, 2.03 GB, 341 us
+// replayed in a graph, 5.9 TB/s or 89 % of a plain copy's rate, and 345 to 355 us a call. That is
+// with the plan, an empty chunk launch and the combine; with the arithmetic skipped a call took
+// 338 us where it took 350, so what is left is loading and those three. Not kept: 16 warps on half stages (407 us),
+// the scores of one stage beside the output of the one before (402 us).
 #include "common.cuh"
 #include "kernels.cuh"
 #include "plan.cuh"

@@ -969,12 +969,12 @@ __device__ __forceinline__ void q4_convert_row(const uint4 &v, uint32_t scales, 
 // Q4: the 4-bit cache's tiles instead. A thread takes 32 columns of a row (two groups) at a
 // time: one load, one of the two scale bytes, sixteen conversions and multiplications, four
 // stores; eight threads in a row (of the warp) store to eight different 16-byte banks.
-// 512 tokens at history 32256 (32/8 heads, D 128): 204 us with Q through registers as above and
-// 160 registers for the softmax, 201 us with Q by TMA and converted in place, 195 us with 176
-// registers, 191 us with a ring of Q tiles (an item's first scores wait for no conversion then:
-// 65.9 instead of 73 us at history 8064). Without any conversion of K and V the first of these
-// took 192 us; over a bf16 cache it is 177 us. A fourth slot, a second stage less or a
-// conversion unrolled by two changed nothing.
+// 512 tokens at history 32256 (32/8 heads, D 128; in brackets at history 8064): 204 us (73) with Q
+// through registers, 201 (69) with Q by TMA and converted in place, 195 (68) with 176 registers
+// for the softmax instead of 160, 191 (66) with a ring of Q tiles, whose next item waits for no
+// conversion; over a bf16 cache 177. With the conversion of K and V skipped the first took 192.
+// A fourth slot changed nothing (204); a conversion unrolled by two neither (191), but fresh 512
+// tokens went from 19.2 to 23.7 us and eight prompts of 2600 from 457 to 444.
 template <int D, int NQ, bool Q4 = false>
 __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, ChunkBars *bars, Tiles<Q4> *q8t,
                                            const PrefillItem *items, int it_begin, int it_end, bool self, int cw,
@@ -1185,7 +1185,7 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
 __device__ __forceinline__ void regs_keep_96() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 __device__ __forceinline__ void regs_take_160() { asm volatile("setmaxnreg.inc.sync.aligned.u32 160;"); }
 // Over the 4-bit cache, whose converters need fewer (256 x 176 + 256 x 80 = 512 x 128): 512 tokens at
-// history 32256 (32/8 heads) 195 us, with 160 and 96 201 us.
+// history 32256 (32/8 heads) 191 us, with 160 and 96 201 us.
 __device__ __forceinline__ void regs_q4_others() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 __device__ __forceinline__ void regs_q4_softmax() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
 

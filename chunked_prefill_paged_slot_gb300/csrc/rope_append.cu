@@ -682,8 +682,9 @@ cudaError_t launch_rope_t(const RopeParams &p, int bits, int num_sms, cudaStream
 // Rows of the 4-bit cache as bf16, gathered by slot: a thread takes one group of 16 columns of
 // one token's k and v of one head, and stores its 32 bytes at once (WIDE: k and v on 32-byte
 // boundaries) or in two halves. Bound by memory: 0.56 bytes in and 2 out per element. (25.6 k
-// rows of 8 heads, D 128, 134 MB: 25.0 us a call, 20.4 us replayed; 26.7 us with eight columns a
-// thread, 30.6 us in two halves.)
+// rows of 8 heads, D 128, 135 MB: over several such inputs in turn 24.9 us, 27.1 us with eight
+// columns a thread; 131 k rows 73 and 83 us. Where one call's rows stay in L2 eight columns are the
+// faster, 19.4 instead of 22.4 us; rows of a cache are rarely there. 30.6 us in two halves.)
 constexpr int kReadThreads = 256;
 
 template <bool WIDE>
