@@ -685,8 +685,7 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
     pp.nq = nq;
     pp.max_splits = max_kv_splits;
     pp.chunk_grid = sms < kMaxChunkGrid ? sms : kMaxChunkGrid;
-    const int dec_heads = scaled ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
-    pp.dec_heads = dec_heads;
+    int dec_heads = scaled ? q8_decode_heads(num_kv_heads) : decode_heads_per_item(num_kv_heads);
     pp.unit_cost = q8 ? unit_cost_q8(head_dim) : kUnitCostTiles;
     pp.dec_keys = dec_heads > 1 ? kDecodeKeysPerSplitGrouped : kDecodeKeysPerSplit;
     if (scaled) {
@@ -697,7 +696,17 @@ int attn_impl(const void *q, const void *k_new, const void *v_new, const int64_t
         pp.dec_stream = q4 && 2 * items >= sms ? 1 : 0;
         pp.dec_grid = (int)(L.max_ditems < pp.chunk_grid ? L.max_ditems : pp.chunk_grid);
         pp.dec_first = reinterpret_cast<int32_t *>(ws + L.off_dec_runs);
+        // Few rows over the 4-bit cache: heads per item are halved while all splits of all rows still
+        // find an SM each, for a warp to a head on few SMs is bound by its arithmetic (one row of
+        // 32768 keys: 118 us a call, 54 with it skipped). 32/8 heads, D 128, pages of 16, replayed,
+        // always eight heads and this: one row of 777 keys 11.2 and 9.7 us, 8192 34.2 and 17.4,
+        // 32768 114.6 and 46.1 (down to two heads 10.2, 19.2, 52.9); nine rows of 777 21.3 and 21.8,
+        // of 777 to 9000 (a call) 51.5 and 40.8.
+        const int64_t splits = (num_reqs < num_tokens ? num_reqs : num_tokens) * (int64_t)max_kv_splits;
+        while (q4 && !pp.dec_stream && dec_heads > 1 && 2 * splits * (num_kv_heads / dec_heads) <= sms)
+            dec_heads /= 2;
     }
+    pp.dec_heads = dec_heads;
     pp.fused = fused ? 1 : 0;
     pp.prow_capacity = cap;
     pp.counts = counts;

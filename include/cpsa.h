@@ -349,7 +349,7 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
  * call can hold enough decode rows to occupy half the GPU, these are cut like prefill
  * units: laid end to end in equal runs, one per CTA, no row in more than max_kv_splits
  * pieces. A decode row's last-bit rounding can then depend on the other requests (it does
- * not depend on timing).
+ * not depend on timing). A call of a single decode row launches no plan kernel.
  * Arithmetic: stored numbers enter the MMAs as f16, exact; q rows as f16 under a power of
  * two of their own; probabilities in f16; partial results of a chunk's split units in
  * bf16, as in cpp_chunked_prefill_attn; everything else in fp32.

@@ -107,3 +107,19 @@ def test_invalid_rows_among_many(cuda_lib):
     keep = np.delete(np.arange(n), [7, 50])
     close(got[keep], ref[keep], vmax[keep])
     assert np.isnan(got[[7, 50]]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (8, 8), (48, 8), (72, 8), (16, 16), (12, 4)])
+def test_few_rows_with_fewer_heads_an_item(cuda_lib, hq, hkv, d):
+    """Rows few enough that an item holds 4, 2 or 1 of the heads that one of more rows would: each number of
+    rows with each number of splits has its own, up to the one row more that has all of them."""
+    for n, splits in ((1, 1), (1, 8), (2, 32), (3, 8), (4, 2), (5, 8), (9, 8), (10, 8), (19, 4), (37, 1), (38, 2)):
+        check(cuda_lib, W.BatchSpec(hist=rows(n, n + hq, long=4000), qlen=[1] * n, num_q_heads=hq, num_kv_heads=hkv,
+                                    head_dim=d, page_size=(16, 64, 256)[(n + hkv) % 3], seed=4600 + n + hq + d),
+              max_kv_splits=splits, spread=12)
+
+
+def test_a_few_rows_beside_a_chunk(cuda_lib):
+    check(cuda_lib, W.BatchSpec(hist=[5000, 3, 900, 0], qlen=[1, 1, 300, 1], num_q_heads=32, num_kv_heads=8,
+                                head_dim=128, page_size=16, seed=4700))
