@@ -271,8 +271,16 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                     tma_load_4d(kdst + C::kTileBytes + lane * box_bytes, &tm_v, &bars->full[stage], 0, off, head0, pg);
                     tma_load_3d(sdst + C::kScTile, &tm_vs, &bars->full[stage], sc_off, head0, pg);
                 } else {
-                    if (live)
+                    if (live) {
+                        // a page outside the cache counts as zeros, as in the chunk kernel: scales of zero
+                        // over whatever codes the stage holds (any code is a finite number)
                         set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        for (uint32_t x = 0; x < sc_bytes; x += 16) {
+                            *reinterpret_cast<uint4 *>(sdst + x) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(sdst + C::kScTile + x) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();   // these before later copies into this stage
+                    }
                     mbar_arrive(&bars->full[stage]);
                 }
                 __syncwarp();

@@ -341,7 +341,8 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
  * k_scale, v_scale bytes [num_pages][num_kv_heads][page_size][head_dim / 16], 16-byte
  * aligned. Places behind a sequence's end may hold anything. A NaN key makes the rows
  * that see it NaN, a NaN value its 16 columns (and it may do so for those columns of
- * earlier rows of the same chunk). Scale bytes above 226 (10240), which the append stores
+ * earlier rows of the same chunk). The keys and values of a page outside the cache
+ * (CPSA_DEV_PAGE_OUT_OF_RANGE) count as zeros. Scale bytes above 226 (10240), which the append stores
  * for NaN alone, stand for numbers that f16 may not hold: infinities and NaN may come of
  * them. (The pages have no counterpart.)
  * Every other argument, the workspace (same size functions), the device flags and CUDA

@@ -1,0 +1,75 @@
+"""Pages outside the cache: flagged, and their keys and values count as zeros, whatever else the call reads. The oracle
+takes the same batch with a page of zeros in their place; nothing of what a kernel had in hand before shows."""
+import dataclasses
+
+import numpy as np
+import pytest
+
+import q4_helpers
+import workloads as W
+from q8_helpers import close
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(32, 8, 128), (16, 4, 128), (8, 2, 64), (6, 3, 128), (16, 1, 64), (1, 1, 128), (24, 8, 64)]
+
+
+def with_zero_page(batch, caches, bad):
+    """(the batch's table with the entries `bad` [(request, page number, what stands there)], the batch and caches that
+    the oracle takes: a page of zeros more, which those entries name)."""
+    table, zeros = batch.block_table.copy(), batch.block_table.copy()
+    for r, i, x in bad:
+        table[r, i], zeros[r, i] = x, batch.num_pages
+    more = [np.concatenate([c, np.zeros_like(c[:1])]) for c in caches]
+    return table, dataclasses.replace(batch, block_table=zeros, num_pages=batch.num_pages + 1), more
+
+
+def bad_entries(batch):
+    """Of every second request the first page, the last and every third in between."""
+    s, out = batch.spec, []
+    for r in range(0, len(s.qlen), 2):
+        n = -(-int(batch.seq_lens[r]) // s.page_size)
+        out += [(r, i, (batch.num_pages, -1, -5, 2 ** 31 - 1, -2 ** 31)[(r + i) % 5]) for i in range(n) if i % 3 == 0 or i == n - 1]
+    return out
+
+
+def check(cpsa, helpers, spec, max_kv_splits=8):
+    b, caches = helpers.draw(spec)
+    table, bz, cz = with_zero_page(b, caches, bad_entries(b))
+    got, flags = helpers.run(cpsa, b, caches, max_kv_splits=max_kv_splits, block_table=table)
+    assert flags == cpsa.DEV_PAGE_OUT_OF_RANGE
+    ref, vmax = helpers.reference(bz, cz)
+    seen = np.broadcast_to(vmax > 0, ref.shape).any((1, 2))     # rows with a page: of the others nothing but zeros is due
+    assert not ref[~seen].any() and not got[~seen].any()
+    if seen.any():
+        close(got[seen], ref[seen], vmax[seen], str(spec))
+
+
+@pytest.mark.parametrize("P", [8, 16, 64, 256])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_4_bit_decode_rows(cuda_lib, hq, hkv, d, P):
+    """Rows of several lengths, so that a stage has held another row's places before; behind the ends stands NaN."""
+    spec = W.BatchSpec(hist=[2999, 700, 1500, 60, 5000], qlen=[1] * 5, num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                       page_size=P, seed=10 + hq + P)
+    check(cuda_lib, q4_helpers, spec)
+    check(cuda_lib, q4_helpers, spec, max_kv_splits=1)
+
+
+@pytest.mark.parametrize("n", [1, 40, 900, 6000])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_4_bit_single_row(cuda_lib, hq, hkv, d, n):
+    check(cuda_lib, q4_helpers, W.BatchSpec(hist=[n - 1], qlen=[1], num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                                            page_size=16, seed=40 + hq + n))
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_4_bit_chunks_beside_decode_rows(cuda_lib, hq, hkv, d):
+    check(cuda_lib, q4_helpers, W.BatchSpec(hist=[700, 300, 33, 0, 900], qlen=[130, 1, 1, 200, 1], num_q_heads=hq,
+                                            num_kv_heads=hkv, head_dim=d, page_size=16, seed=70 + hq))
+
+
+def test_4_bit_many_rows(cuda_lib):
+    """Enough rows for equal runs a CTA, each over several rows."""
+    r = np.random.default_rng(5)
+    check(cuda_lib, q4_helpers, W.BatchSpec(hist=[int(x) for x in r.integers(1, 900, 200)], qlen=[1] * 200, num_q_heads=8,
+                                            num_kv_heads=2, head_dim=128, page_size=16, seed=90))
