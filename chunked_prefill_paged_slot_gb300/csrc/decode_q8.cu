@@ -250,8 +250,16 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                     tma_load_4d(kdst + lane * box_bytes, &tm_k, &bars->full[stage], 0, off, head0, pg);
                     tma_load_4d(kdst + C::kTileBytes + lane * box_bytes, &tm_v, &bars->full[stage], 0, off, head0, pg);
                 } else {
-                    if (live)
+                    if (live) {
+                        // a page outside the cache counts as zeros, as in the chunk kernel
                         set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        for (uint32_t x = 0; x < box_bytes; x += 16) {
+                            uint8_t *row = kdst + lane * box_bytes + x;
+                            *reinterpret_cast<uint4 *>(row) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(row + C::kTileBytes) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();   // these before later copies into this stage
+                    }
                     mbar_arrive(&bars->full[stage]);
                 }
                 s0lo = s1lo; s0hi = s1hi;

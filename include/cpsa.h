@@ -316,7 +316,8 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
  * 2^(scale - 127). Places behind a sequence's end, and the scales of blocks that
  * hold none of its places, may hold anything. A NaN key makes the rows that see
  * it NaN, a NaN value their column (and it may do so for that column of earlier
- * rows of the same chunk). (The pages have no counterpart.)
+ * rows of the same chunk). The keys and values of a page outside the cache
+ * (CPSA_DEV_PAGE_OUT_OF_RANGE) count as zeros. (The pages have no counterpart.)
  * Every other argument, the workspace (same size functions), the device flags
  * and CUDA graph capture are cpp_chunked_prefill_attn's, and so are the splits,
  * but for the keys per split of a decode row: they also go by num_reqs (fewer rows

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import q4_helpers
+import q8_helpers
 import workloads as W
 from q8_helpers import close
 
@@ -73,3 +74,23 @@ def test_4_bit_many_rows(cuda_lib):
     r = np.random.default_rng(5)
     check(cuda_lib, q4_helpers, W.BatchSpec(hist=[int(x) for x in r.integers(1, 900, 200)], qlen=[1] * 200, num_q_heads=8,
                                             num_kv_heads=2, head_dim=128, page_size=16, seed=90))
+
+
+@pytest.mark.parametrize("P", [8, 16, 64, 256])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_8_bit_decode_rows(cuda_lib, hq, hkv, d, P):
+    check(cuda_lib, q8_helpers, W.BatchSpec(hist=[2999, 700, 1500, 60, 5000], qlen=[1] * 5, num_q_heads=hq,
+                                            num_kv_heads=hkv, head_dim=d, page_size=P, seed=110 + hq + P))
+
+
+@pytest.mark.parametrize("n", [1, 40, 900, 6000])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_8_bit_single_row(cuda_lib, hq, hkv, d, n):
+    check(cuda_lib, q8_helpers, W.BatchSpec(hist=[n - 1], qlen=[1], num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                                            page_size=16, seed=140 + hq + n))
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_8_bit_chunks_beside_decode_rows(cuda_lib, hq, hkv, d):
+    check(cuda_lib, q8_helpers, W.BatchSpec(hist=[700, 300, 33, 0, 900], qlen=[130, 1, 1, 200, 1], num_q_heads=hq,
+                                            num_kv_heads=hkv, head_dim=d, page_size=16, seed=170 + hq))
