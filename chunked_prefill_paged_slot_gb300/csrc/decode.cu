@@ -102,6 +102,17 @@ __device__ __forceinline__ uint32_t swz_addr(uint32_t base, int row, int col, in
     return base + half_row_off<D>(row, col >> 6, lg) + ((ch ^ (row & 7)) << 4) + (col & 7) * 2;
 }
 
+// Zeros in place of a box of a stage, K's and V's, by one lane ahead of the stage's arrival.
+__device__ __forceinline__ void zero_box(uint8_t *k, uint8_t *v, uint32_t bytes)
+{
+#pragma unroll 1
+    for (uint32_t x = 0; x < bytes; x += 16) {
+        *reinterpret_cast<uint4 *>(k + x) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(v + x) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();   // these before later copies into the stage
+}
+
 template <int D, bool HI>
 __global__ void __launch_bounds__(DecCfg<D, HI>::kThreads, 1)
 decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -172,16 +183,22 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                     !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort))
                     last = g;
                 const int off = (c0 + lane * PB) % p.page_size;
+                uint8_t *kdst = smem + stage * C::kStageBytes;
+                uint8_t *vdst = kdst + C::kTileBytes;
                 bool valid = false;
                 if (lane < NB && c0 + lane * PB < w.key1) {
                     valid = page >= 0 && page < p.num_pages;
-                    if (!valid)
+                    if (!valid) {
+                        // a page outside the cache counts as zeros
                         set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        if (g < last)
+                            zero_box(kdst + lane * box_bytes, vdst + lane * box_bytes, box_bytes);
+                    }
                 }
                 const uint32_t vmask = __ballot_sync(0xffffffffu, valid);
+                if (vmask != (1u << NB) - 1u)
+                    __syncwarp();   // the zeros, if any, before lane 0's arrival
                 const uint32_t bytes = (uint32_t)__popc(vmask) * box_bytes * 2;
-                uint8_t *kdst = smem + stage * C::kStageBytes;
-                uint8_t *vdst = kdst + C::kTileBytes;
                 const bool patch = knew >= c0 && knew < c0 + kKC;
                 uint64_t *bar = patch ? &bars->patch : &bars->full[stage];
                 if (lane == 0 && g < last)
@@ -571,13 +588,17 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                     bool v0 = false, v1 = false;
                     if (c0 < w.key1) {
                         v0 = pg0 >= 0 && pg0 < p.num_pages;
-                        if (!v0)
+                        if (!v0) {   // a page outside the cache counts as zeros
                             set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                            zero_box(kdst, vdst, box_bytes);
+                        }
                     }
                     if (NBX == 2 && c0 + RB < w.key1) {
                         v1 = pg1 >= 0 && pg1 < p.num_pages;
-                        if (!v1)
+                        if (!v1) {
                             set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                            zero_box(kdst + box_bytes, vdst + box_bytes, box_bytes);
+                        }
                     }
                     mbar_arrive_expect_tx(bar, (uint32_t)((v0 ? 2 : 0) + (v1 ? 2 : 0)) * box_bytes);
 #pragma unroll

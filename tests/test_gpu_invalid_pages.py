@@ -4,15 +4,59 @@ import dataclasses
 
 import numpy as np
 import pytest
+import torch
 
+import oracle
 import q4_helpers
 import q8_helpers
 import workloads as W
+from helpers import bf16_tensor_to_f64, to_dev, to_dev_bf16
 from q8_helpers import close
 
 pytestmark = pytest.mark.gpu
 
 HEADS = [(32, 8, 128), (16, 4, 128), (8, 2, 64), (6, 3, 128), (16, 1, 64), (1, 1, 128), (24, 8, 64)]
+
+
+class bf16_helpers:
+    """draw, run and reference over a bf16 cache, as q8_helpers and q4_helpers have them."""
+
+    @staticmethod
+    def draw(spec):
+        b = W.make_batch(spec, with_history=False)
+        seen = np.zeros((b.num_pages, spec.page_size), bool)
+        for r, n in enumerate(b.seq_lens):
+            j = np.arange(n)
+            seen[b.block_table[r, j // spec.page_size], j % spec.page_size] = True
+        rng, caches = np.random.default_rng(spec.seed), []
+        for _ in "kv":
+            c = W.randn_bf16(rng, (b.num_pages, spec.num_kv_heads, spec.page_size, spec.head_dim))
+            c.transpose(0, 2, 1, 3)[~seen] = W.BF16_NAN_SENTINEL
+            caches.append(c)
+        return b, caches
+
+    @staticmethod
+    def run(cpsa, batch, caches, max_kv_splits=8, block_table=None):
+        s, T = batch.spec, batch.num_tokens
+        ws = torch.empty(cpsa.cpp_attn_workspace_bytes(len(s.qlen), T, s.num_q_heads, s.num_kv_heads, s.head_dim,
+                                                       max_kv_splits), dtype=torch.uint8, device="cuda")
+        out = torch.full((T, s.num_q_heads, s.head_dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cpsa.cpp_chunked_prefill_attn(to_dev_bf16(batch.q), *map(to_dev_bf16, caches), to_dev(batch.query_lens),
+                                      to_dev(batch.seq_lens), to_dev(block_table), out, ws, err,
+                                      max_kv_splits=max_kv_splits)
+        return bf16_tensor_to_f64(out), cpsa.cpp_read_device_error(err)
+
+    @staticmethod
+    def reference(batch, caches):
+        s = batch.spec
+        ref = oracle.paged_attention(batch.q, *caches, batch.query_lens, batch.seq_lens, batch.block_table)
+        v64, vmax = W.bf16_bits_to_f32(caches[1]).astype(np.float64), []
+        for r, (ql, n) in enumerate(zip(batch.query_lens, batch.seq_lens)):
+            j = np.arange(n)
+            m = np.abs(v64[batch.block_table[r, j // s.page_size], :, j % s.page_size]).max((0, 2))
+            vmax += [np.repeat(m, s.num_q_heads // s.num_kv_heads)] * int(ql)
+        return ref, np.array(vmax)[..., None]
 
 
 def with_zero_page(batch, caches, bad):
@@ -94,3 +138,19 @@ def test_8_bit_single_row(cuda_lib, hq, hkv, d, n):
 def test_8_bit_chunks_beside_decode_rows(cuda_lib, hq, hkv, d):
     check(cuda_lib, q8_helpers, W.BatchSpec(hist=[700, 300, 33, 0, 900], qlen=[130, 1, 1, 200, 1], num_q_heads=hq,
                                             num_kv_heads=hkv, head_dim=d, page_size=16, seed=170 + hq))
+
+
+@pytest.mark.parametrize("P", [8, 16, 64, 256])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_bf16_decode_rows(cuda_lib, hq, hkv, d, P):
+    spec = W.BatchSpec(hist=[2999, 700, 1500, 60, 5000], qlen=[1] * 5, num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                       page_size=P, seed=210 + hq + P)
+    check(cuda_lib, bf16_helpers, spec)
+    check(cuda_lib, bf16_helpers, spec, max_kv_splits=1)
+
+
+@pytest.mark.parametrize("n", [1, 40, 900, 6000])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_bf16_single_row(cuda_lib, hq, hkv, d, n):
+    check(cuda_lib, bf16_helpers, W.BatchSpec(hist=[n - 1], qlen=[1], num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                                              page_size=16, seed=240 + hq + n))
