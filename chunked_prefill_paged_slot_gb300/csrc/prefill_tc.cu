@@ -1382,14 +1382,14 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 const bool from_new = kt >= nh;
                 const int key0 = from_new ? hist + (kt - nh) * 128 : kt * 128;
                 const int key_end = from_new ? s_len : hist_end;   // keys [key0, key_end) are used
-                const int page = next_page;
+                int page = next_page;
                 next_page = lookup(kt + 1);
                 const int off = (key0 + box * PB) % p.page_size;
-                bool valid = false;
-                if (!from_new && issuer && key0 + box * PB < key_end) {
-                    valid = page >= 0 && page < p.num_pages;
-                    if (!valid && half == 0)
+                const bool live = !from_new && issuer && key0 + box * PB < key_end;
+                if (live && (page < 0 || page >= p.num_pages)) {
+                    if (half == 0)
                         set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                    page = -1;   // a box ahead of the cache's first: the copies bring zeros
                 }
                 const bool tail = key0 + 128 > key_end;
                 for (int kv = 0; kv < 2 && !stop; ++kv) {
@@ -1413,7 +1413,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         } else if (issuer) {
                             mbar_arrive(bar);
                         }
-                    } else if (valid && kv == 1 && v_pages) {
+                    } else if (live && kv == 1 && v_pages) {
                         // V below page 128: one box per page holding both column halves,
                         // [page][half][PB rows][128 B] (the half-1 lanes only arrive)
                         if (half == 0) {
@@ -1423,7 +1423,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                         } else {
                             mbar_arrive(bar);
                         }
-                    } else if (valid) {
+                    } else if (live) {
                         mbar_arrive_expect_tx(bar, box_bytes);
                         tma_load_3d(dst + half * C::kHalfBytes + box * box_bytes, kv == 0 ? &tm_k : &tm_v, bar,
                                     half * 64, off, page * p.num_kv_heads + kvh);

@@ -66,7 +66,7 @@ extern "C" {
 
 /* ---- device error flags (bits of *dev_err) --------------------------------- */
 #define CPSA_DEV_SLOT_OUT_OF_RANGE 0x01u  /* slot >= num_pages * page_size: token skipped */
-#define CPSA_DEV_PAGE_OUT_OF_RANGE 0x02u  /* block_table entry outside [0, num_pages): tile skipped */
+#define CPSA_DEV_PAGE_OUT_OF_RANGE 0x02u  /* block_table entry outside [0, num_pages): its keys and values count as zeros */
 #define CPSA_DEV_SEQ_LT_QUERY 0x04u       /* seq_len < query_len or query_len < 0: request skipped */
 #define CPSA_DEV_TOKENS_MISMATCH 0x08u    /* sum(query_lens) != num_tokens: nothing computed */
 #define CPSA_DEV_SEQ_GT_TABLE 0x10u       /* seq_len > max_blocks_per_req * page_size: request skipped */
@@ -316,8 +316,7 @@ int cpp_chunked_prefill_attn(const void *q, const void *k_cache, const void *v_c
  * 2^(scale - 127). Places behind a sequence's end, and the scales of blocks that
  * hold none of its places, may hold anything. A NaN key makes the rows that see
  * it NaN, a NaN value their column (and it may do so for that column of earlier
- * rows of the same chunk). The keys and values of a page outside the cache
- * (CPSA_DEV_PAGE_OUT_OF_RANGE) count as zeros. (The pages have no counterpart.)
+ * rows of the same chunk). (The pages have no counterpart.)
  * Every other argument, the workspace (same size functions), the device flags
  * and CUDA graph capture are cpp_chunked_prefill_attn's, and so are the splits,
  * but for the keys per split of a decode row: they also go by num_reqs (fewer rows
@@ -342,8 +341,7 @@ int cpp_chunked_prefill_attn_q8(const void *q, const void *k_cache, const void *
  * k_scale, v_scale bytes [num_pages][num_kv_heads][page_size][head_dim / 16], 16-byte
  * aligned. Places behind a sequence's end may hold anything. A NaN key makes the rows
  * that see it NaN, a NaN value its 16 columns (and it may do so for those columns of
- * earlier rows of the same chunk). The keys and values of a page outside the cache
- * (CPSA_DEV_PAGE_OUT_OF_RANGE) count as zeros. Scale bytes above 226 (10240), which the append stores
+ * earlier rows of the same chunk). Scale bytes above 226 (10240), which the append stores
  * for NaN alone, stand for numbers that f16 may not hold: infinities and NaN may come of
  * them. (The pages have no counterpart.)
  * Every other argument, the workspace (same size functions), the device flags and CUDA

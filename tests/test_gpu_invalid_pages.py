@@ -154,3 +154,19 @@ def test_bf16_decode_rows(cuda_lib, hq, hkv, d, P):
 def test_bf16_single_row(cuda_lib, hq, hkv, d, n):
     check(cuda_lib, bf16_helpers, W.BatchSpec(hist=[n - 1], qlen=[1], num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
                                               page_size=16, seed=240 + hq + n))
+
+
+@pytest.mark.parametrize("P", [8, 16, 64, 256])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_bf16_chunks_beside_decode_rows(cuda_lib, hq, hkv, d, P):
+    check(cuda_lib, bf16_helpers, W.BatchSpec(hist=[700, 300, 33, 0, 900], qlen=[130, 1, 1, 200, 1], num_q_heads=hq,
+                                              num_kv_heads=hkv, head_dim=d, page_size=P, seed=270 + hq + P))
+
+
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("helpers", [bf16_helpers, q8_helpers, q4_helpers], ids=["bf16", "8 bit", "4 bit"])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_one_long_chunk(cuda_lib, hq, hkv, d, helpers, P):
+    """One request, which plans itself; its tiles' slots are used many times over."""
+    check(cuda_lib, helpers, W.BatchSpec(hist=[2500], qlen=[333], num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=P,
+                                         seed=300 + hq + P))
