@@ -102,17 +102,6 @@ __device__ __forceinline__ uint32_t swz_addr(uint32_t base, int row, int col, in
     return base + half_row_off<D>(row, col >> 6, lg) + ((ch ^ (row & 7)) << 4) + (col & 7) * 2;
 }
 
-// Zeros in place of a box of a stage, K's and V's, by one lane ahead of the stage's arrival.
-__device__ __forceinline__ void zero_box(uint8_t *k, uint8_t *v, uint32_t bytes)
-{
-#pragma unroll 1
-    for (uint32_t x = 0; x < bytes; x += 16) {
-        *reinterpret_cast<uint4 *>(k + x) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(v + x) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();   // these before later copies into the stage
-}
-
 template <int D, bool HI>
 __global__ void __launch_bounds__(DecCfg<D, HI>::kThreads, 1)
 decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
@@ -174,7 +163,7 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll
             for (int k = 0; k < kLookahead; ++k) pg[k] = lookup(w.key0 + k * kKC);
             for (int c0 = w.key0; c0 < w.key1; c0 += kKC, ++g) {
-                const int page = pg[0];
+                int page = pg[0];
 #pragma unroll
                 for (int k = 0; k + 1 < kLookahead; ++k) pg[k] = pg[k + 1];
                 pg[kLookahead - 1] = lookup(c0 + kLookahead * kKC);
@@ -183,22 +172,15 @@ decode_attn_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_
                     !mbar_wait(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort))
                     last = g;
                 const int off = (c0 + lane * PB) % p.page_size;
+                const bool live = lane < NB && c0 + lane * PB < w.key1;
+                if (live && (page < 0 || page >= p.num_pages)) {
+                    set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                    page = -1;   // a box ahead of the cache's first: the copies bring zeros
+                }
+                const uint32_t vmask = __ballot_sync(0xffffffffu, live);
+                const uint32_t bytes = (uint32_t)__popc(vmask) * box_bytes * 2;
                 uint8_t *kdst = smem + stage * C::kStageBytes;
                 uint8_t *vdst = kdst + C::kTileBytes;
-                bool valid = false;
-                if (lane < NB && c0 + lane * PB < w.key1) {
-                    valid = page >= 0 && page < p.num_pages;
-                    if (!valid) {
-                        // a page outside the cache counts as zeros
-                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                        if (g < last)
-                            zero_box(kdst + lane * box_bytes, vdst + lane * box_bytes, box_bytes);
-                    }
-                }
-                const uint32_t vmask = __ballot_sync(0xffffffffu, valid);
-                if (vmask != (1u << NB) - 1u)
-                    __syncwarp();   // the zeros, if any, before lane 0's arrival
-                const uint32_t bytes = (uint32_t)__popc(vmask) * box_bytes * 2;
                 const bool patch = knew >= c0 && knew < c0 + kKC;
                 uint64_t *bar = patch ? &bars->patch : &bars->full[stage];
                 if (lane == 0 && g < last)
@@ -585,28 +567,22 @@ decode_group_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                 uint64_t *bar = patch ? &bars->patch : &bars->full[stage];
                 if (lane == 0 && g < last) {
                     // one lane announces the stage's bytes, then issues its copies
-                    bool v0 = false, v1 = false;
-                    if (c0 < w.key1) {
-                        v0 = pg0 >= 0 && pg0 < p.num_pages;
-                        if (!v0) {   // a page outside the cache counts as zeros
-                            set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                            zero_box(kdst, vdst, box_bytes);
-                        }
+                    const bool two = NBX == 2 && c0 + RB < w.key1;
+                    int page0 = pg0, page1 = pg1;
+                    if (page0 < 0 || page0 >= p.num_pages) {
+                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        page0 = -1;   // a box ahead of the cache's first: the copies bring zeros
                     }
-                    if (NBX == 2 && c0 + RB < w.key1) {
-                        v1 = pg1 >= 0 && pg1 < p.num_pages;
-                        if (!v1) {
-                            set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                            zero_box(kdst + box_bytes, vdst + box_bytes, box_bytes);
-                        }
+                    if (two && (page1 < 0 || page1 >= p.num_pages)) {
+                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        page1 = -1;
                     }
-                    mbar_arrive_expect_tx(bar, (uint32_t)((v0 ? 2 : 0) + (v1 ? 2 : 0)) * box_bytes);
+                    mbar_arrive_expect_tx(bar, (two ? 4u : 2u) * box_bytes);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const bool vb = b == 0 ? v0 : v1;
-                        if (!vb)
+                        if (b == 1 && !two)
                             continue;
-                        const int pg = b == 0 ? pg0 : pg1;
+                        const int pg = b == 0 ? page0 : page1;
                         const int off = (c0 + b * RB) % p.page_size;
                         if (C::kHalves == 2) {
                             tma_load_5d(kdst + b * box_bytes, &tm_k, bar, 0, off, 0, head0, pg);

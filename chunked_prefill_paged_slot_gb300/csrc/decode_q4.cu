@@ -248,7 +248,7 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                     cur = nxt;
                     nxt = lookup(window + 1);
                 }
-                const int pg = __shfl_sync(0xffffffffu, cur, (j * NBX + (lane & (NBX - 1))) & 31);
+                int pg = __shfl_sync(0xffffffffu, cur, (j * NBX + (lane & (NBX - 1))) & 31);
                 const int stage = g % C::kStages;
                 if (g >= (uint32_t)C::kStages &&
                     !mbar_wait_warp(&bars->empty[stage], ((g / C::kStages) - 1) & 1, abort)) {
@@ -261,8 +261,11 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                 // same step, before it issues the copies
                 const int key = w.key0 + (box << lgrb);
                 const bool live = lane < NBX && key < w.key1;
-                const bool valid = live && pg >= 0 && pg < p.num_pages;
-                if (valid) {
+                if (live) {
+                    if (pg < 0 || pg >= p.num_pages) {
+                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        pg = -1;   // a box ahead of the cache's first: the copies bring zeros
+                    }
                     mbar_arrive_expect_tx(&bars->full[stage], 2 * (box_bytes + sc_bytes));
                     const int off = key & (p.page_size - 1);
                     const int sc_off = off * (C::kScRow / 4);   // in words
@@ -271,16 +274,6 @@ decode_q4_kernel(const DecodeParams p, const Q4Cache cache, const __grid_constan
                     tma_load_4d(kdst + C::kTileBytes + lane * box_bytes, &tm_v, &bars->full[stage], 0, off, head0, pg);
                     tma_load_3d(sdst + C::kScTile, &tm_vs, &bars->full[stage], sc_off, head0, pg);
                 } else {
-                    if (live) {
-                        // a page outside the cache counts as zeros, as in the chunk kernel: scales of zero
-                        // over whatever codes the stage holds (any code is a finite number)
-                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                        for (uint32_t x = 0; x < sc_bytes; x += 16) {
-                            *reinterpret_cast<uint4 *>(sdst + x) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(sdst + C::kScTile + x) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();   // these before later copies into this stage
-                    }
                     mbar_arrive(&bars->full[stage]);
                 }
                 __syncwarp();

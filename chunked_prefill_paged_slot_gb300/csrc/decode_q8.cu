@@ -221,7 +221,7 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                     nxt = nx2;
                     nx2 = lookup(window + 2);
                 }
-                const int pg = __shfl_sync(0xffffffffu, cur, (j * NBX + (lane & (NBX - 1))) & 31);
+                int pg = __shfl_sync(0xffffffffu, cur, (j * NBX + (lane & (NBX - 1))) & 31);
                 uint32_t s2lo, s2hi;
                 scales_of(j + 2, s2lo, s2hi);
                 const int stage = g % C::kStages;
@@ -243,23 +243,16 @@ decode_q8_kernel(const DecodeParams p, const Q8Cache cache, const __grid_constan
                 // that box's bytes in the same step, before it issues the copies
                 const int key = w.key0 + (box << lgrb);
                 const bool live = lane < NBX && key < w.key1;
-                const bool valid = live && pg >= 0 && pg < p.num_pages;
-                if (valid) {
+                if (live) {
+                    if (pg < 0 || pg >= p.num_pages) {
+                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
+                        pg = -1;   // a box ahead of the cache's first: the copies bring zeros
+                    }
                     mbar_arrive_expect_tx(&bars->full[stage], 2 * box_bytes);
                     const int off = key & (p.page_size - 1);
                     tma_load_4d(kdst + lane * box_bytes, &tm_k, &bars->full[stage], 0, off, head0, pg);
                     tma_load_4d(kdst + C::kTileBytes + lane * box_bytes, &tm_v, &bars->full[stage], 0, off, head0, pg);
                 } else {
-                    if (live) {
-                        // a page outside the cache counts as zeros, as in the chunk kernel
-                        set_dev_error(p.dev_err, CPSA_DEV_PAGE_OUT_OF_RANGE);
-                        for (uint32_t x = 0; x < box_bytes; x += 16) {
-                            uint8_t *row = kdst + lane * box_bytes + x;
-                            *reinterpret_cast<uint4 *>(row) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4 *>(row + C::kTileBytes) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();   // these before later copies into this stage
-                    }
                     mbar_arrive(&bars->full[stage]);
                 }
                 s0lo = s1lo; s0hi = s1hi;
