@@ -13,11 +13,12 @@
 // Pass 1 sums tokens, prefill tiles (W) and decode partial rows and finds the
 // shortest and longest unit, which fix the run length, whether the partials fit
 // the workspace (if not, nothing is split) and whether units are cut at all (see
-// choose_split). Pass 2 walks the requests in chunks of 1024: one block scan
-// gives each request its token and tile offsets, a second its list offsets, and
-// a warp per request then writes that request's entries. Batches of at most 32
-// requests, 8192 tokens and some 400 units (or of one request) take a one-warp kernel
-// that builds the same lists without block barriers.
+// choose_split). Pass 2 gives each request its token and tile offsets, counts its
+// entries (in closed form, and for the units that run boundaries cut a thread a
+// boundary), gives it its list offsets, and a warp per request then writes its
+// entries: plan_kernel for any number of requests, 1024 at a time by block scans;
+// plan_warps_kernel for at most 32, by one warp's scans. Batches of very few requests
+// take a one-warp kernel that builds the same lists in one walk.
 #include "common.cuh"
 #include "plan.cuh"
 
@@ -113,15 +114,96 @@ __device__ __forceinline__ int warp_excl_scan(int x, int lane, int &total)
     return incl - x;
 }
 
-// One request's work, walked by a whole warp (all arguments warp-uniform).
-// With emit == false only the counts are returned (warp-uniform); with
-// emit == true the entries are written at the given offsets, lane l of each pass
-// taking one unit and placing its pieces by a warp scan.
+// A request's counts as long as no run boundary cuts a unit (see add_cuts).
+__device__ Counts request_counts(const PlanParams &p, const Req &rq, int max_splits)
+{
+    Counts c{0, 0, 0, 0, 0, 0};
+    if (!rq.valid || rq.q == 0)
+        return c;
+    if (rq.q > 1) {
+        c.pieces = ceil_div(rq.q, kTileM) * p.Hkv * (p.group / p.nq);
+    } else if (!p.dec_stream) {   // (streamed rows: decode_stream_work)
+        const int ns = decode_splits(rq, max_splits, p.dec_keys);
+        c.ditems = p.Hkv / p.dec_heads * ns;   // decode items per split, times the splits
+        if (ns > 1) {
+            c.prows = p.Hq * ns;
+            c.citems = 1;
+            c.cunits = p.Hq;
+        }
+    }
+    return c;
+}
+
+// The first position of the a-th query tile from the last, behind the request's own: the tiles of
+// query tiles nqt - 1 .. nqt - a (nkv_last, then hb + nqt - a' for a' = 1 .. a - 1) and their units' costs.
+__device__ __forceinline__ int query_tile_pos(const PlanParams &p, int a, int upq, int nqt, int hb, int nkv_last)
+{
+    const int before = a == 0 ? 0 : nkv_last + (a - 1) * (hb + nqt) - (a - 1) * a / 2;
+    return upq * (before + a * p.unit_cost);
+}
+
+// Where run boundaries cut units, without a walk over the units: there is a boundary a CTA, and a
+// thread finds the request and the unit that it falls into by bisection. Of the n requests with
+// lengths q, s and first tiles tile_off, up to tile `end`, cuts[r] (zero before) gets the
+// boundaries inside a unit's tiles, and in its upper half the units that hold them. By the block.
+__device__ void count_cuts(const PlanParams &p, const int *q, const int *s, const int *tile_off, int n, int end, int run,
+                           int *cuts)
+{
+    const int lane = threadIdx.x & 31, k0 = tile_off[0] / run + 1, nb = (end - 1) / run - k0 + 1;
+    for (int i0 = threadIdx.x - lane; i0 < nb; i0 += blockDim.x) {
+        int r = -1;
+        bool inside = false, first = false;   // inside a unit's tiles; and the first one there
+        if (i0 + lane < nb) {
+            const int x = (k0 + i0 + lane) * run;
+            int hi = n - 1;                   // the last request that starts at x or ahead of it
+            r = 0;
+            while (r < hi) {
+                const int mid = (r + hi + 1) / 2;
+                if (tile_off[mid] <= x)
+                    r = mid;
+                else
+                    hi = mid - 1;
+            }
+            const Req rq = make_req(p, q[r], s[r]);
+            const int upq = p.Hkv * (p.group / p.nq), nqt = ceil_div(rq.q, kTileM), hb = ceil_div(rq.hist, kTileN);
+            const int nkv_last = unit_tiles(p, rq, nqt - 1, rq.q - (nqt - 1) * kTileM), y = x - tile_off[r];
+            int a = 0;                        // the last of its query tiles that starts at y or ahead of it
+            hi = nqt - 1;
+            while (a < hi) {
+                const int mid = (a + hi + 1) / 2;
+                if (query_tile_pos(p, mid, upq, nqt, hb, nkv_last) <= y)
+                    a = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int z = (y - query_tile_pos(p, a, upq, nqt, hb, nkv_last)) %
+                          ((a == 0 ? nkv_last : hb + nqt - a) + p.unit_cost);
+            inside = z > p.unit_cost;
+            first = inside && z - run <= p.unit_cost;
+        }
+        const uint32_t alike = __match_any_sync(0xffffffffu, r);   // the warp's boundaries of the same request
+        const uint32_t in = __ballot_sync(0xffffffffu, inside) & alike, units = __ballot_sync(0xffffffffu, first) & alike;
+        if (in != 0 && lane == __ffs(alike) - 1)
+            atomicAdd(&cuts[r], __popc(in) | __popc(units) << 16);
+    }
+}
+
+__device__ __forceinline__ void add_cuts(const PlanParams &p, int cuts, Counts &c)
+{
+    const int in = cuts & 0xffff, units = cuts >> 16;
+    c.pieces += in;
+    c.sunits += units;
+    c.prows += kTileM * p.nq * (in + units);
+}
+
+// One request's work, walked by a whole warp (all arguments warp-uniform): its
+// entries are written at the given offsets, lane l of each pass taking one unit
+// and placing its pieces by a warp scan. Returns their counts.
 // tile_off: global index of the request's first prefill tile; run: tiles per CTA
 // run; cut: whether a run boundary may split a unit (else a unit goes whole to
 // the run that holds its first tile).
 __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int tile_off, int run, bool cut,
-                               int max_splits, bool emit, int q_off, const Counts &off, int lane)
+                               int max_splits, int q_off, const Counts &off, int lane)
 {
     Counts c{0, 0, 0, 0, 0, 0};
     if (!rq.valid || rq.q == 0)
@@ -132,23 +214,16 @@ __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int ti
         const int ns = decode_splits(rq, max_splits, p.dec_keys);
         const int nch = ceil_div(rq.s, kDecodeChunk);
         const int ngroups = p.Hkv / p.dec_heads;   // decode items per split
-        c.ditems = ngroups * ns;
-        if (ns > 1) {
-            c.prows = p.Hq * ns;
-            c.citems = 1;
-            c.cunits = p.Hq;
+        c = request_counts(p, rq, max_splits);
+        for (int k = lane; k < c.ditems; k += 32) {
+            const int sp = k / ngroups, kvh = k % ngroups;
+            const int c0 = sp * nch / ns, c1 = (sp + 1) * nch / ns;
+            const int key1 = min(c1 * kDecodeChunk, rq.s);
+            p.ditems[off.ditems + k] = DecodeItem{r, kvh, c0 * kDecodeChunk, key1, sp, ns,
+                                                  ns > 1 ? off.prows : -1, q_off};
         }
-        if (emit) {
-            for (int k = lane; k < c.ditems; k += 32) {
-                const int sp = k / ngroups, kvh = k % ngroups;
-                const int c0 = sp * nch / ns, c1 = (sp + 1) * nch / ns;
-                const int key1 = min(c1 * kDecodeChunk, rq.s);
-                p.ditems[off.ditems + k] = DecodeItem{r, kvh, c0 * kDecodeChunk, key1, sp, ns,
-                                                      ns > 1 ? off.prows : -1, q_off};
-            }
-            if (ns > 1 && lane == 0)
-                p.citems[off.citems] = CombineItem{q_off, 1, 0, p.Hq, off.prows, ns, off.cunits, 0};
-        }
+        if (ns > 1 && lane == 0)
+            p.citems[off.citems] = CombineItem{q_off, 1, 0, p.Hq, off.prows, ns, off.cunits, 0};
         return c;
     }
     // prefill units in order: query tiles (longest KV range first), kv heads, head
@@ -169,10 +244,8 @@ __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int ti
         const int a = g / upq, j = g - a * upq;
         const int qt = nqt - 1 - a;
         const int nkv = a == 0 ? nkv_last : hb + qt + 1;
-        // tiles of the units of query tiles nqt - 1 .. qt + 1: nkv_last, then hb + nqt - a' for a' = 1 .. a - 1
-        const int before = a == 0 ? 0 : nkv_last + (a - 1) * (hb + nqt) - (a - 1) * a / 2;
         // the unit's positions [u0, u1): unit_cost of fixed cost, then its tiles from t0
-        const int u0 = tile_off + upq * (before + a * p.unit_cost) + j * (nkv + p.unit_cost);
+        const int u0 = tile_off + query_tile_pos(p, a, upq, nqt, hb, nkv_last) + j * (nkv + p.unit_cost);
         const int t0 = u0 + p.unit_cost, u1 = t0 + nkv;
         const int first = t0 / run;
         const int np = active ? (cut ? (u1 - 1) / run - first + 1 : 1) : 0;
@@ -187,7 +260,7 @@ __device__ Counts request_work(const PlanParams &p, int r, const Req &rq, int ti
         const long long tot = __shfl_sync(0xffffffffu, sc, 31);
         const long long ex = sc - ((long long)np | ((long long)(split ? np : 0) << 32));
         const unsigned split_lanes = __ballot_sync(0xffffffffu, split);
-        if (emit && active) {
+        if (active) {
             const int kvh = j / pairs, hp = j - kvh * pairs;
             const int i0 = qt * kTileM;
             const int pi = off.pieces + c.pieces + (int)(ex & 0xffffffffll);
@@ -406,6 +479,7 @@ struct PlanTotals {
     int longest, shortest, dlongest;
 };
 
+template <bool STREAM>
 __device__ __forceinline__ void warp_totals(PlanTotals &t)
 {
 #pragma unroll
@@ -413,10 +487,13 @@ __device__ __forceinline__ void warp_totals(PlanTotals &t)
         t.tok += __shfl_xor_sync(0xffffffffu, t.tok, o);
         t.tiles += __shfl_xor_sync(0xffffffffu, t.tiles, o);
         t.dprows += __shfl_xor_sync(0xffffffffu, t.dprows, o);
-        t.dtiles += __shfl_xor_sync(0xffffffffu, t.dtiles, o);
-        t.longest = max(t.longest, __shfl_xor_sync(0xffffffffu, t.longest, o));
-        t.shortest = min(t.shortest, __shfl_xor_sync(0xffffffffu, t.shortest, o));
-        t.dlongest = max(t.dlongest, __shfl_xor_sync(0xffffffffu, t.dlongest, o));
+    }
+    t.longest = __reduce_max_sync(0xffffffffu, t.longest);
+    t.shortest = __reduce_min_sync(0xffffffffu, t.shortest);
+    if (STREAM) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t.dtiles += __shfl_xor_sync(0xffffffffu, t.dtiles, o);
+        t.dlongest = __reduce_max_sync(0xffffffffu, t.dlongest);
     }
 }
 
@@ -424,21 +501,22 @@ __device__ __forceinline__ void warp_totals(PlanTotals &t)
 __device__ void block_totals(PlanTotals &t)
 {
     __shared__ PlanTotals red[kPlanThreads / 32];
-    warp_totals(t);
+    warp_totals<true>(t);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
     __syncthreads();
     t = red[threadIdx.x & 31];
-    warp_totals(t);
+    warp_totals<true>(t);
 }
 
 // One request's part of the totals.
+template <bool STREAM>
 __device__ __forceinline__ void add_request(const PlanParams &p, const Req &rq, PlanTotals &t)
 {
     t.tok += rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
     t.tiles += prefill_tiles(p, rq);
     t.longest = max(t.longest, longest_unit(p, rq));
     t.shortest = min(t.shortest, shortest_unit(p, rq));
-    if (p.dec_stream) {
+    if (STREAM && p.dec_stream) {
         const int n = decode_tiles(p, rq);
         t.dtiles += (long long)n * (p.Hkv / p.dec_heads);
         t.dlongest = max(t.dlongest, n);
@@ -458,7 +536,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
     for (int base = 0; base < p.num_reqs; base += kPlanThreads) {
         const int r = base + threadIdx.x;
         if (r < p.num_reqs)
-            add_request(p, load_req(p, r), tot);
+            add_request<true>(p, load_req(p, r), tot);
     }
     block_totals(tot);
     const long long tiles = tot.tiles;
@@ -483,7 +561,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
 
     // ---- pass 2: offsets and lists, 1024 requests at a time
     __shared__ int s_qoff[kPlanThreads], s_toff[kPlanThreads], s_q[kPlanThreads], s_s[kPlanThreads];
-    __shared__ int s_cnt[kPlanThreads][kScan];
+    __shared__ int s_cnt[kPlanThreads][kScan], s_cuts[kPlanThreads];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int carry_a[2] = {0, 0};                        // tokens, tiles
     long long carry_d = 0;                          // streamed decode tiles
@@ -493,6 +571,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
         // (a) token and tile offsets: one thread per request
         Req mine{false, 0, 0, 0};
         {
+            s_cuts[threadIdx.x] = 0;
             const int r = base + threadIdx.x;
             int va[2] = {0, 0};
             if (threadIdx.x < nloc) {
@@ -525,31 +604,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
             my_dec = decode_stream_work(p, ds, base + threadIdx.x, mine, my_u0, false, 0, Counts{0, 0, 0, 0, 0, 0});
         }
         __syncthreads();
-        // (b) per-request counts: one warp per request
-        for (int l = warp; l < nloc; l += kPlanThreads / 32) {
-            const Req rq = make_req(p, s_q[l], s_s[l]);
-            const Counts c = request_work(p, base + l, rq, s_toff[l], run, split_prefill, max_splits, false,
-                                          s_qoff[l], Counts{0, 0, 0, 0, 0, 0}, lane);
-            if (lane == 0) {
-                s_cnt[l][0] = c.pieces;
-                s_cnt[l][1] = c.prows;
-                s_cnt[l][2] = c.cunits;
-                s_cnt[l][3] = c.citems;
-                s_cnt[l][4] = c.ditems;
-                s_cnt[l][5] = c.sunits;
-            }
-        }
+        // (b) counts: run boundaries inside units, then one thread per request
+        if (split_prefill)
+            count_cuts(p, s_q, s_s, s_toff, nloc, carry_a[1], run, s_cuts);
         __syncthreads();
         // (c) list offsets: one thread per request
         {
-            int vb[kScan];
-            for (int j = 0; j < kScan; ++j) vb[j] = threadIdx.x < nloc ? s_cnt[threadIdx.x][j] : 0;
-            vb[1] += my_dec.prows;
-            vb[2] += my_dec.cunits;
-            vb[3] += my_dec.citems;
-            vb[4] += my_dec.ditems;
+            Counts c = threadIdx.x < nloc ? request_counts(p, mine, max_splits) : Counts{0, 0, 0, 0, 0, 0};
+            add_cuts(p, s_cuts[threadIdx.x], c);
+            int vb[kScan] = {c.pieces, c.prows + my_dec.prows, c.cunits + my_dec.cunits, c.citems + my_dec.citems,
+                             c.ditems + my_dec.ditems, c.sunits};
             int tb[kScan];
-            block_scan(vb, tb);   // ends with a barrier: s_cnt reads are done
+            block_scan(vb, tb);
             for (int j = 0; j < kScan; ++j) s_cnt[threadIdx.x][j] = carry_b[j] + vb[j];
             for (int j = 0; j < kScan; ++j) carry_b[j] += tb[j];
         }
@@ -563,7 +629,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
         for (int l = warp; l < nloc; l += kPlanThreads / 32) {
             const Req rq = make_req(p, s_q[l], s_s[l]);
             const Counts off{s_cnt[l][0], s_cnt[l][1], s_cnt[l][2], s_cnt[l][3], s_cnt[l][4], s_cnt[l][5]};
-            request_work(p, base + l, rq, s_toff[l], run, split_prefill, max_splits, true, s_qoff[l], off, lane);
+            request_work(p, base + l, rq, s_toff[l], run, split_prefill, max_splits, s_qoff[l], off, lane);
         }
         __syncthreads();
     }
@@ -586,55 +652,55 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
     pdl_trigger();
 }
 
-// The same lists for a batch of at most 32 requests, built by one warp: lane r
-// holds request r, warp scans give the token and tile offsets, and the warp then
-// walks the requests in order, so every request's list offsets are the running
-// totals of the ones before it (one pass, no block-wide barriers).
-__global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
+// A batch of at most 32 requests as one warp, lane r holding request r, has it at first: totals, then
+// offsets by warp scans, and the streamed decode rows' lists (STREAM: dec_stream).
+struct SmallPlan {
+    Req rq;                                   // of the lane's request
+    int tok_off, tile_off, tok_total, tile_total;
+    SplitChoice sc;
+    DecodeStream ds;
+    Counts off;                               // entries ahead of the other requests' lists
+};
+
+// False where the lengths do not add up (the lists are empty then).
+template <bool STREAM>
+__device__ __forceinline__ bool small_plan(const PlanParams &p, int lane, SmallPlan &w)
 {
-    // The attention kernels that follow are released only at the end: CTAs
-    // launched early wait beside this warp and halve its speed (measured), while
-    // what they would overlap is short.
-    pdl_wait();
-    const int lane = threadIdx.x;
     const bool mine = lane < p.num_reqs;
-    Req rq{false, 0, 0, 0};
+    w.rq = Req{false, 0, 0, 0};
     if (mine)
-        rq = load_req(p, lane);
-    const int tok = mine && rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
-    const int tiles = mine ? prefill_tiles(p, rq) : 0;
+        w.rq = load_req(p, lane);
     // totals in 64 bits first: the 32-bit scans below are only used once they fit
     PlanTotals tot{0, 0, 0, 0, 0, 0x7fffffff, 0};
     if (mine)
-        add_request(p, rq, tot);
-    warp_totals(tot);
-    if (p.dec_stream)
-        tot.dprows = decode_stream_bound(p, tot.dprows);
-    const long long tok_sum = tot.tok, tile_sum = tot.tiles;
-    const int grid = max(1, p.chunk_grid);
-    if (tok_sum != p.num_tokens) {
+        add_request<STREAM>(p, w.rq, tot);
+    warp_totals<STREAM>(tot);
+    if (tot.tok != p.num_tokens) {
         if (lane == 0) set_dev_error(p.dev_err, CPSA_DEV_TOKENS_MISMATCH);
         if (lane < kCntSlots) p.counts[lane] = 0;
         for (int c = lane; c <= p.chunk_grid; c += 32) p.run_first[c] = 0;
-        for (int c = lane; p.dec_stream && c <= p.dec_grid; c += 32) p.dec_first[c] = 0;
-        return;
+        if (STREAM)
+            for (int c = lane; c <= p.dec_grid; c += 32) p.dec_first[c] = 0;
+        return false;
     }
-    if (mine && !rq.valid)
-        set_dev_error(p.dev_err, (rq.q < 0 || rq.s < rq.q) ? CPSA_DEV_SEQ_LT_QUERY : CPSA_DEV_SEQ_GT_TABLE);
-    int tok_total, tile_total;
-    const int tok_off = warp_excl_scan(tok, lane, tok_total);
-    const int tile_off = warp_excl_scan(tiles, lane, tile_total);
+    if (mine && !w.rq.valid)
+        set_dev_error(p.dev_err, (w.rq.q < 0 || w.rq.s < w.rq.q) ? CPSA_DEV_SEQ_LT_QUERY : CPSA_DEV_SEQ_GT_TABLE);
+    // (invalid requests still occupy their rows)
+    w.tok_off = warp_excl_scan(mine && w.rq.q > 0 ? w.rq.q : 0, lane, w.tok_total);
+    w.tile_off = warp_excl_scan(mine ? prefill_tiles(p, w.rq) : 0, lane, w.tile_total);
     if (mine)
-        p.cu_q[lane] = tok_off;
-    const SplitChoice sc = choose_split(p, tile_sum, tot.shortest, tot.longest, tot.dprows);
-    if (sc.clamped && lane == 0)
+        p.cu_q[lane] = w.tok_off;
+    if (lane == 0)
+        p.cu_q[p.num_reqs] = w.tok_total;
+    w.sc = choose_split(p, tot.tiles, tot.shortest, tot.longest, STREAM ? decode_stream_bound(p, tot.dprows) : tot.dprows);
+    if (w.sc.clamped && lane == 0)
         set_dev_error(p.dev_err, CPSA_DEV_SPLITS_CLAMPED);
-    Counts off{0, 0, 0, 0, 0, 0};
-    DecodeStream ds{0, 1, false};
-    if (p.dec_stream) {
+    w.off = Counts{0, 0, 0, 0, 0, 0};
+    w.ds = DecodeStream{0, 1, false};
+    if (STREAM) {
         // streamed decode rows: a lane per request, ahead of the prefill requests' lists
-        ds = decode_stream(p, tot.dtiles, tot.dlongest, sc.max_splits);
-        long long u0 = (long long)decode_tiles(p, rq) * (p.Hkv / p.dec_heads);
+        w.ds = decode_stream(p, tot.dtiles, tot.dlongest, w.sc.max_splits);
+        long long u0 = (long long)decode_tiles(p, w.rq) * (p.Hkv / p.dec_heads);
         const long long own = u0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -642,24 +708,63 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
             if (lane >= o) u0 += y;
         }
         u0 -= own;
-        const Counts c = decode_stream_work(p, ds, lane, rq, u0, false, 0, off);
+        const Counts c = decode_stream_work(p, w.ds, lane, w.rq, u0, false, 0, w.off);
         Counts at;
         at.pieces = at.sunits = 0;
-        at.prows = warp_excl_scan(c.prows, lane, off.prows);
-        at.cunits = warp_excl_scan(c.cunits, lane, off.cunits);
-        at.citems = warp_excl_scan(c.citems, lane, off.citems);
-        at.ditems = warp_excl_scan(c.ditems, lane, off.ditems);
-        decode_stream_work(p, ds, lane, rq, u0, true, tok_off, at);
+        at.prows = warp_excl_scan(c.prows, lane, w.off.prows);
+        at.cunits = warp_excl_scan(c.cunits, lane, w.off.cunits);
+        at.citems = warp_excl_scan(c.citems, lane, w.off.citems);
+        at.ditems = warp_excl_scan(c.ditems, lane, w.off.ditems);
+        decode_stream_work(p, w.ds, lane, w.rq, u0, true, w.tok_off, at);
     }
+    return true;
+}
+
+// The lists' ends, with `end` entries in them: by all threads.
+template <bool STREAM>
+__device__ __forceinline__ void finish_plan(const PlanParams &p, const Counts &end, const SplitChoice &sc, const DecodeStream &ds,
+                                            long long tiles, int nthreads)
+{
+    const int n_pieces = (int)min((int64_t)end.pieces, p.max_pitems);
+    fill_run_first(p, n_pieces, max(1, p.chunk_grid), sc.split_prefill, tiles, sc.run, threadIdx.x, nthreads);
+    if (STREAM)
+        decode_stream_tail(p, ds, end.ditems, threadIdx.x, nthreads);
+    if (threadIdx.x == 0) {
+        p.counts[kCntPrefill] = n_pieces;
+        p.counts[kCntCombine] = (int)min((int64_t)end.citems, p.max_citems);
+        p.counts[kCntPartialRows] = end.prows;
+        p.counts[kCntCombineUnits] = end.cunits;
+        p.counts[kCntDecode] = (int)min((int64_t)end.ditems, p.max_ditems);
+        p.counts[kCntRunTiles] = sc.run;
+        p.counts[kCntSplitUnits] = end.sunits;
+    } else if (threadIdx.x > kCntSplitUnits && threadIdx.x < kCntSlots) {
+        p.counts[threadIdx.x] = 0;
+    }
+}
+
+// The same lists by one warp, which walks the requests in order: every request's
+// list offsets are the running totals of the ones before it.
+template <bool STREAM>
+__global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
+{
+    // The attention kernels that follow are released only at the end: CTAs
+    // launched early wait beside this warp and halve its speed (measured), while
+    // what they would overlap is short.
+    pdl_wait();
+    const int lane = threadIdx.x;
+    SmallPlan w;
+    if (!small_plan<STREAM>(p, lane, w))
+        return;
+    Counts off = w.off;
     for (int r = 0; r < p.num_reqs; ++r) {
         Req rr;
-        rr.valid = __shfl_sync(0xffffffffu, rq.valid ? 1 : 0, r) != 0;
-        rr.q = __shfl_sync(0xffffffffu, rq.q, r);
-        rr.s = __shfl_sync(0xffffffffu, rq.s, r);
-        rr.hist = __shfl_sync(0xffffffffu, rq.hist, r);
-        const int qoff = __shfl_sync(0xffffffffu, tok_off, r);
-        const int toff = __shfl_sync(0xffffffffu, tile_off, r);
-        const Counts c = request_work(p, r, rr, toff, sc.run, sc.split_prefill, sc.max_splits, true, qoff, off, lane);
+        rr.valid = __shfl_sync(0xffffffffu, w.rq.valid ? 1 : 0, r) != 0;
+        rr.q = __shfl_sync(0xffffffffu, w.rq.q, r);
+        rr.s = __shfl_sync(0xffffffffu, w.rq.s, r);
+        rr.hist = __shfl_sync(0xffffffffu, w.rq.hist, r);
+        const int qoff = __shfl_sync(0xffffffffu, w.tok_off, r);
+        const int toff = __shfl_sync(0xffffffffu, w.tile_off, r);
+        const Counts c = request_work(p, r, rr, toff, w.sc.run, w.sc.split_prefill, w.sc.max_splits, qoff, off, lane);
         off.pieces += c.pieces;
         off.prows += c.prows;
         off.cunits += c.cunits;
@@ -668,41 +773,86 @@ __global__ void __launch_bounds__(32, 1) plan_small_kernel(PlanParams p)
         off.sunits += c.sunits;
     }
     __syncwarp();   // the warp's piece writes are visible to all its lanes
-    const int n_pieces = (int)min((int64_t)off.pieces, p.max_pitems);
-    fill_run_first(p, n_pieces, grid, sc.split_prefill, tile_sum, sc.run, lane, 32);
-    if (p.dec_stream)
-        decode_stream_tail(p, ds, off.ditems, lane, 32);
-    if (lane == 0) {
-        p.cu_q[p.num_reqs] = tok_total;
-        p.counts[kCntPrefill] = n_pieces;
-        p.counts[kCntCombine] = (int)min((int64_t)off.citems, p.max_citems);
-        p.counts[kCntPartialRows] = off.prows;
-        p.counts[kCntCombineUnits] = off.cunits;
-        p.counts[kCntDecode] = (int)min((int64_t)off.ditems, p.max_ditems);
-        p.counts[kCntRunTiles] = sc.run;
-        p.counts[kCntSplitUnits] = off.sunits;
-    } else if (lane > kCntSplitUnits && lane < kCntSlots) {
-        p.counts[lane] = 0;
+    finish_plan<STREAM>(p, off, w.sc, w.ds, w.tile_total, 32);
+    pdl_trigger();
+}
+
+// The same lists by a warp a request: the first warp begins as the one above; then all threads count
+// the cuts, and every warp adds up the entries ahead of its request's and writes these.
+template <bool STREAM>
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_warps_kernel(PlanParams p)
+{
+    __shared__ int s_q[32], s_s[32], s_qoff[32], s_toff[32], s_cuts[32], s_ok;
+    __shared__ Counts s_cnt[32], s_end;   // a request's entries; all requests'
+    __shared__ SmallPlan s_plan;          // of lane 0
+    pdl_wait();                           // (dependents are released at the end, as above)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp == 0) {
+        SmallPlan w;
+        const bool ok = small_plan<STREAM>(p, lane, w);
+        if (ok) {
+            s_q[lane] = w.rq.q;
+            s_s[lane] = w.rq.s;
+            s_qoff[lane] = w.tok_off;
+            s_toff[lane] = w.tile_off;
+            s_cuts[lane] = 0;
+            s_cnt[lane] = request_counts(p, w.rq, w.sc.max_splits);
+            if (lane == 0)
+                s_plan = w;
+        }
+        if (lane == 0)
+            s_ok = ok;
     }
+    __syncthreads();
+    if (!s_ok)
+        return;
+    const SplitChoice sc = s_plan.sc;
+    if (sc.split_prefill) {
+        count_cuts(p, s_q, s_s, s_toff, p.num_reqs, s_plan.tile_total, sc.run, s_cuts);
+        __syncthreads();
+    }
+    Counts b{0, 0, 0, 0, 0, 0}, off = s_plan.off;
+    if (lane < warp) {                    // the requests ahead
+        b = s_cnt[lane];
+        add_cuts(p, s_cuts[lane], b);
+    }
+    off.pieces += __reduce_add_sync(0xffffffffu, b.pieces);
+    off.prows += __reduce_add_sync(0xffffffffu, b.prows);
+    off.cunits += __reduce_add_sync(0xffffffffu, b.cunits);
+    off.citems += __reduce_add_sync(0xffffffffu, b.citems);
+    off.ditems += __reduce_add_sync(0xffffffffu, b.ditems);
+    off.sunits += __reduce_add_sync(0xffffffffu, b.sunits);
+    const Counts c = request_work(p, warp, make_req(p, s_q[warp], s_s[warp]), s_toff[warp], sc.run, sc.split_prefill,
+                                  sc.max_splits, s_qoff[warp], off, lane);
+    if (warp == p.num_reqs - 1 && lane == 0)
+        s_end = Counts{off.pieces + c.pieces, off.prows + c.prows, off.cunits + c.cunits,
+                       off.citems + c.citems, off.ditems + c.ditems, off.sunits + c.sunits};
+    __syncthreads();                      // the pieces are visible to all warps
+    finish_plan<STREAM>(p, s_end, sc, s_plan.ds, s_plan.tile_total, blockDim.x);
     pdl_trigger();
 }
 
 }  // namespace
 
-// The one-warp kernel walks every request's units itself (about 0.5 us per 32
-// units: 166 us for 32 prompts of 2600 tokens at 32/8 heads), the block kernel
-// gives each request a warp of its own but pays its barriers: one warp while
-// the lists are short or there is one request to walk. (Over the 4-bit cache at 14/2
-// heads, D 64: six ragged prompts of 1187 tokens, about 600 units, 73.7 us by one warp and 68.6 by
-// the block, two of them, 240 units, 43.9 and 47.6.)
-constexpr int64_t kPlanSmallMaxTokens = 8192, kPlanSmallMaxUnits = 400;
+// Which kernel, by the number of requests alone: what else decides (whether one request holds most of
+// the units) the host does not know. One warp walks every request's units itself, about 0.5 us
+// per 32 units and 0.3 us a request; a warp a request walks them side by side, but for the price of
+// barriers and of counting them first. Calls over a bf16 cache, 32/8 heads, D 128, replayed (other
+// caches alike), by one warp and by a warp a request: a decode row and a chunk of 256 tokens at history
+// 3000 56.8 and 58.6 us, three rows and that chunk 75.0 and 75.4, two prompts of 2500 124.3 and 121.3, four of
+// 2000 163.2 and 152.1, four of 300 31.0 and 28.7, five rows 47.1 and 45.6. Past 32 requests, or by the block kernel:
+// eight prompts of 1024 99.3 us, 95.3 by a warp a request; a chunk of 4096 beside eight rows 193.7 (its
+// units walked twice then, once to count them) and 185.4.
+constexpr int kPlanOneWarpReqs = 3;
+constexpr int64_t kPlanOneWarpTokens = 8192;
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s, bool early)
 {
-    const int64_t units = p.num_tokens / kTileM * p.Hkv * (p.group / p.nq);   // about
-    if (p.num_reqs <= 32 &&
-        (p.num_reqs == 1 || (p.num_tokens <= kPlanSmallMaxTokens && units <= kPlanSmallMaxUnits)))
-        return launch_pdl(early, plan_small_kernel, dim3(1), dim3(32), 0, s, p);
+    if (p.num_reqs == 1 || (p.num_reqs <= kPlanOneWarpReqs && p.num_tokens <= kPlanOneWarpTokens))
+        return launch_pdl(early, p.dec_stream ? plan_small_kernel<true> : plan_small_kernel<false>, dim3(1), dim3(32), 0, s, p);
+    if (p.num_reqs <= 32)
+        return launch_pdl(early, p.dec_stream ? plan_warps_kernel<true> : plan_warps_kernel<false>, dim3(1),
+                          dim3(32 * p.num_reqs), 0, s, p);
     return launch_pdl(early, plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
 }
 

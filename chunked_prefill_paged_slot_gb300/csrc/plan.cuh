@@ -2,8 +2,8 @@
 // the attention kernels.
 //
 // One call of cpp_chunked_prefill_attn runs:
-//   plan      one CTA (one warp for up to 32 requests): scan of query_lens,
-//             validation, work lists, split choice
+//   plan      one CTA (a warp a request up to 32, one warp for up to 3): scan of
+//             query_lens, validation, work lists, split choice
 //   chunk     tensor-core kernel over prefill items (query_len >= 2); merges
 //             the units the stream-K cut split
 //   decode    split-KV kernel over decode items (query_len == 1)
