@@ -228,6 +228,11 @@ def _rows(t: torch.Tensor, tokens, heads, d, name, device):
     return t.data_ptr(), (s[0] if tokens > 1 else heads * d)
 
 
+def _shape(t):
+    """A tensor's shape; None where there is no tensor."""
+    return getattr(t, "shape", None)
+
+
 def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cache, q_out, dev_err, interleaved, stream,
                norm=None, per_byte=1):
     """The rotary appends: `caches`(device) gives the addresses of the cache's tensors, `cache` is the k cache; norm:
@@ -236,9 +241,13 @@ def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cach
         raise CpsaError(f"{what}: inconsistent shapes")
     T, Hkv, d = kshape = k.shape
     pages, Hkv2, P, d2 = cache.shape
-    if v.shape != kshape or Hkv2 != Hkv or d2 * per_byte != d or slot_mapping.shape != (T,) or (q is None) != (q_out is None) \
-            or (cos_sin is None) != (positions is None):
+    if _shape(v) != kshape or Hkv2 != Hkv or d2 * per_byte != d or _shape(slot_mapping) != (T,) \
+            or (q is None) != (q_out is None) or (cos_sin is None) != (positions is None):
         raise CpsaError(f"{what}: inconsistent shapes")
+    if norm is not None:
+        q_weight, k_weight, eps = norm
+        if _shape(k_weight) != (d,) or _shape(q_weight) != (None if q is None else (d,)):
+            raise CpsaError(f"{what}: k_weight, and q_weight with q, must have shape ({d},)")
     handle, device = _where(stream, k, "k")
     Hq = qp = qs = qo = top = rot = 0
     pos = cs = None
@@ -257,9 +266,6 @@ def _rope_call(what, fn, caches, q, k, v, positions, cos_sin, slot_mapping, cach
     vp, vs = _rows(v, T, Hkv, d, "v", device)
     more = ()
     if norm is not None:
-        q_weight, k_weight, eps = norm
-        if (q_weight is None) != (q is None) or k_weight.shape != (d,) or (q_weight is not None and q_weight.shape != (d,)):
-            raise CpsaError(f"{what}: k_weight, and q_weight with q, must have shape ({d},)")
         more = (None if q_weight is None else _ptr(q_weight, _F32, "q_weight", device),
                 _ptr(k_weight, _F32, "k_weight", device), float(eps))
     st = fn(qp, kp, vp, qs, ks, vs, *more, pos, cs, top, rot, 1 if interleaved else 0,
@@ -292,8 +298,8 @@ def _q8_pointers(k_cache, v_cache, k_scale, v_scale, device):
         raise CpsaError("k_cache must be [pages, kv heads, page size, head dim]")
     scales = (shape[0], shape[1], shape[2] // max(1, min(16, shape[2])))
     for t, want, name in ((v_cache, shape, "v_cache"), (k_scale, scales, "k_scale"), (v_scale, scales, "v_scale")):
-        if t.shape != want:
-            raise CpsaError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+        if _shape(t) != want:
+            raise CpsaError(f"{name} must have shape {tuple(want)}, got {_shape(t)}")
     return (_ptr(k_cache, _BYTES, "k_cache", device), _ptr(v_cache, _BYTES, "v_cache", device),
             _ptr(k_scale, _SCALES, "k_scale", device), _ptr(v_scale, _SCALES, "v_scale", device))
 
@@ -318,8 +324,8 @@ def _q4_pointers(k_cache, v_cache, k_scale, v_scale, device):
         raise CpsaError("k_cache must be [pages, kv heads, page size, head dim / 2]")
     scales = (shape[0], shape[1], shape[2], shape[3] // 8)
     for t, want, name in ((v_cache, shape, "v_cache"), (k_scale, scales, "k_scale"), (v_scale, scales, "v_scale")):
-        if t.shape != want:
-            raise CpsaError(f"{name} must have shape {tuple(want)}, got {tuple(t.shape)}")
+        if _shape(t) != want:
+            raise CpsaError(f"{name} must have shape {tuple(want)}, got {_shape(t)}")
     return (_ptr(k_cache, _CODES, "k_cache", device), _ptr(v_cache, _CODES, "v_cache", device),
             _ptr(k_scale, _U8, "k_scale", device), _ptr(v_scale, _U8, "v_scale", device))
 
@@ -338,7 +344,7 @@ def cpp_norm_rope_kv_cache_write(q, k, v, q_weight, k_weight, positions, cos_sin
                                  dev_err, eps=1e-6, interleaved=False, stream=None):
     """cpp_rope_kv_cache_write with an RMS norm of every q and k head before its rotation: x / sqrt(mean(x^2) + eps) *
     weight, q_weight and k_weight fp32 [d] (q_weight None where q is). positions = cos_sin = None norms without rotating."""
-    if v_cache.shape != k_cache.shape:
+    if _shape(v_cache) != _shape(k_cache):
         raise CpsaError("cpp_norm_rope_kv_cache_write: inconsistent shapes")
     _rope_call("cpp_norm_rope_kv_cache_write", load().cpp_norm_rope_kv_cache_write,
                lambda dev: (_ptr(k_cache, _BF16, "k_cache", dev), _ptr(v_cache, _BF16, "v_cache", dev)),
@@ -370,9 +376,10 @@ def cpp_kv_cache_read_q4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k, v,
     handle, device = _where(stream, k_cache, "k_cache")
     caches = _q4_pointers(k_cache, v_cache, k_scale, v_scale, device)
     pages, Hkv, P, half = k_cache.shape
-    T, d = k.shape[0], 2 * half
-    if k.shape != (T, Hkv, d) or v.shape != k.shape or slot_mapping.shape != (T,):
+    d, slots = 2 * half, _shape(slot_mapping)
+    if slots is None or len(slots) != 1 or _shape(k) != (*slots, Hkv, d) or _shape(v) != k.shape:
         raise CpsaError("cpp_kv_cache_read_q4: inconsistent shapes")
+    T = slots[0]
     st = load().cpp_kv_cache_read_q4(*caches, _ptr(slot_mapping, _I64, "slot_mapping", device), T, Hkv, d, P, pages,
                                      _ptr(k, _BF16, "k", device), _ptr(v, _BF16, "v", device),
                                      _ptr(dev_err, _I32, "dev_err", device), handle)
@@ -437,12 +444,13 @@ def _attn_call(what, fn, pointers, per_byte, q, k_cache, v_cache, k_scale, v_sca
     """Attention over a cache with scales, `per_byte` columns to a byte."""
     handle, device = _where(stream, k_cache, "k_cache")
     caches = pointers(k_cache, v_cache, k_scale, v_scale, device)
-    T, Hq, d = qshape = q.shape
     pages, Hkv, P, d2 = k_cache.shape
-    B = query_lens.shape[0]
-    table = block_table.shape
-    if out.shape != qshape or d2 * per_byte != d or seq_lens.shape != (B,) or len(table) != 2 or table[0] != B:
+    qshape, lens, table = _shape(q), _shape(query_lens), _shape(block_table)
+    if qshape is None or len(qshape) != 3 or qshape[2] != d2 * per_byte or _shape(out) != qshape or lens is None \
+            or len(lens) != 1 or _shape(seq_lens) != lens or table is None or len(table) != 2 or table[0] != lens[0]:
         raise CpsaError(f"{what}: inconsistent shapes")
+    T, Hq, d = qshape
+    B = lens[0]
     st = fn(
         _ptr(q, _BF16, "q", device), *caches, _ptr(query_lens, _I32, "query_lens", device),
         _ptr(seq_lens, _I32, "seq_lens", device), _ptr(block_table, _I32, "block_table", device), B, T, table[1], Hq,
