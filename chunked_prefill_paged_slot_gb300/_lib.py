@@ -313,8 +313,9 @@ def cpp_rope_kv_cache_write_q8(q, k, v, positions, cos_sin, slot_mapping, k_cach
                q, k, v, positions, cos_sin, slot_mapping, k_cache, q_out, dev_err, interleaved, stream)
 
 
-# The 4-bit cache's bytes hold two codes each: torch's type of that name, or plain bytes.
-_CODES = (torch.uint8, torch.float4_e2m1fn_x2)
+# The 4-bit cache's bytes hold two codes each: torch's type of that name, where it has one, or plain bytes.
+FLOAT4 = getattr(torch, "float4_e2m1fn_x2", None)
+_CODES = (torch.uint8,) if FLOAT4 is None else (torch.uint8, FLOAT4)
 
 
 def _q4_pointers(k_cache, v_cache, k_scale, v_scale, device):

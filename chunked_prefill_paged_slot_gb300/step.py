@@ -44,7 +44,7 @@ class AttentionStep:
                  fused_kv_write: bool = False, kv_dtype: torch.dtype = torch.bfloat16,
                  rope: torch.Tensor | None = None, rope_interleaved: bool = False,
                  q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, norm_eps: float = 1e-6):
-        if kv_dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.float4_e2m1fn_x2):
+        if kv_dtype is None or kv_dtype not in (torch.bfloat16, torch.float8_e4m3fn, _lib.FLOAT4):
             raise _lib.CpsaError("AttentionStep: kv_dtype must be torch.bfloat16, torch.float8_e4m3fn or "
                                  f"torch.float4_e2m1fn_x2, got {kv_dtype}")
         if (q_norm is None) != (k_norm is None):
@@ -54,7 +54,7 @@ class AttentionStep:
                                  "and head norms")
         device = torch.device(device if device is not None else "cuda")
         self.q8 = kv_dtype == torch.float8_e4m3fn
-        self.q4 = kv_dtype == torch.float4_e2m1fn_x2
+        self.q4 = kv_dtype == _lib.FLOAT4
         self.rope = rope
         self.rope_interleaved = rope_interleaved
         self.norm = None if q_norm is None else (q_norm, k_norm)
