@@ -35,9 +35,6 @@ class AttentionStep:
     q_norm, k_norm: fp32 [head_dim] weights of an RMS norm of every q and k head, on their way too, before the rotation;
     norm_eps: what is added to the mean square."""
 
-    q4 = False
-    norm = None
-
     def __init__(self, num_reqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  max_kv_splits: int = 8, device=None, workspace_bytes: int | None = None,
                  two_stream: bool = False, balance_threshold: float = 0.1, length_threshold: int = 256,
@@ -84,7 +81,7 @@ class AttentionStep:
         normed and rotated q goes (the step's own buffer)."""
         if (self.rope is None) != (positions is None):
             raise _lib.CpsaError("AttentionStep.run: positions go with a step built with rope, and only with it")
-        scaled = self.q8 or self.q4
+        scaled = not self.fused_kv_write and (self.q8 or self.q4)   # the fused write is of a bf16 cache
         if scaled != (k_scale is not None) or scaled != (v_scale is not None):
             raise _lib.CpsaError("AttentionStep.run: k_scale and v_scale go with a step of an 8-bit or 4-bit cache, and "
                                  "only with it")
