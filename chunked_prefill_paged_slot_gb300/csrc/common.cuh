@@ -41,8 +41,12 @@ __device__ __forceinline__ void set_dev_error(uint32_t *dev_err, uint32_t bits)
         atomicOr(dev_err, bits);
 }
 
-// One second: no on-chip wait of these kernels should take more than microseconds.
+// One second: the on-chip waits of these kernels take microseconds, but for one that takes as long
+// as a work item (the loader of Q over the 4-bit cache: milliseconds at 10^5 keys, more than a second
+// at 10^8) and whose limit grows with the item's KV tiles, by kWaitTileNs each. (A tile takes 1.6 to
+// 1.8 us: 512 tokens at history 32256, 32/8 heads, 107 tiles a CTA in 190 us.)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr uint64_t kWaitTileNs = 16000;
 
 // ---------------------------------------------------------------------------
 // mbarrier

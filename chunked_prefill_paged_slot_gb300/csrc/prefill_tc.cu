@@ -899,15 +899,22 @@ __device__ __forceinline__ void q4_load_q(const ChunkParams &p, const CUtensorMa
     using C = ChunkCfg<D, NQ, true, true>;
     volatile int *abort = &bars->abort;
     uint32_t u = 0;
+    int ahead[2] = {0, 0};   // KV tiles of the two items before
     bool ok = true;
     for (int it = it_begin; it < it_end && ok && !warp_aborted(abort); ++it) {
         const PrefillItem w = items[it];
+        // The buffers are used up with an item's last scores: a wait as long as the items ahead. (Asleep for 16 to
+        // 256 ns at a time, where the next item's Q is late: a fresh chunk of 4096 tokens 159 us, 150 polling, of 2000
+        // 56 and 53, eight prompts of 2600 447 and 441; 512 tokens at history 32256 185 and 187.)
+        const uint64_t limit = kWaitLimitNs + (uint64_t)(ahead[0] + ahead[1]) * kWaitTileNs;
+        ahead[0] = ahead[1];
+        ahead[1] = w.kt1 - w.kt0;
         const int h0 = (w.kvh_hp & 0xFFFF) * p.group + (w.kvh_hp >> 16) * NQ;
         const int row0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
         for (int n = 0; n < NQ; ++n, ++u) {
             const uint32_t b = u % C::kQRing;
             if (u >= (uint32_t)C::kQRing &&
-                !(ok = mbar_wait_warp(&q4t->q_empty[b], ((u / C::kQRing) - 1) & 1, abort)))
+                !(ok = mbar_wait_warp(&q4t->q_empty[b], ((u / C::kQRing) - 1) & 1, abort, limit)))
                 break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&q4t->q_raw[b], C::kTileBytes);
