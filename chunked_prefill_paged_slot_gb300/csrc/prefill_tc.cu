@@ -94,8 +94,10 @@ struct ChunkCfg {
     static constexpr int kPlanCap = Q8 ? kSelfPlanCapQ8 : kSelfPlanCap;
     static constexpr int kQ8Off = kItemOff + kPlanCap * 32;    // Q8Tiles
     static constexpr int kBarBytes = 256 + kSelfPlanCap * 32 + (Q4 ? 512 : 0);  // barriers + pieces (+ Q8Tiles, Q4Tiles)
-    // Q4: the ring of Q tiles
+    // Q4: the ring of Q tiles, tile u of the CTA's run in buffer q_ring(u)
     static constexpr int kQRing = NQ + 1;
+    __host__ __device__ static constexpr uint32_t q_ring(uint32_t u) { return u % kQRing; }
+    __host__ __device__ static constexpr uint32_t q_parity(uint32_t u) { return (u / kQRing) & 1; }
     __host__ __device__ static constexpr int q_tile(uint32_t i) { return i < (uint32_t)NQ ? (int)i * kTileBytes : kStageOff; }
     static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;   // + alignment slack
     static_assert(kSmemBytes <= 232448, "beyond the 227 KB of shared memory a CTA may have");
@@ -151,6 +153,14 @@ struct Q4Tiles {
     uint64_t q_raw[3], q_full[3], q_empty[3];        // Q tiles: landed as bf16, converted, used up
     uint32_t there[4];                               // per KV tile (modulo 4), bit l: group l of eight keys is loaded
 };
+// Tile u's exponents: entry q4_exps(u). Tile u + kQ4Exps writes them again, once the buffer of tile u + kQ4Exps - kQRing
+// is free, which has to be a tile of a later item than u's (NQ tiles each), for their first MMAs wait for the
+// softmax of u's item.
+constexpr uint32_t kQ4Exps = sizeof(Q4Tiles::qe) / sizeof(Q4Tiles::qe[0]);
+__host__ __device__ constexpr uint32_t q4_exps(uint32_t u) { return u % kQ4Exps; }
+template <int NQ>
+constexpr bool kQ4ExpsKept = (int)kQ4Exps - ChunkCfg<128, NQ, true, true>::kQRing >= NQ;
+static_assert(kQ4ExpsKept<1> && kQ4ExpsKept<2>, "exponents written again while the softmax may read them");
 constexpr int kQ4Room = 512;   // what the 4-bit cache's kernel keeps beyond that of the 8-bit cache's
 static_assert(sizeof(Q4Tiles) <= (kSelfPlanCap - kSelfPlanCapQ8) * 32 + kQ4Room, "in place of the pieces it gave up, and its own");
 template <bool Q4>
@@ -912,9 +922,9 @@ __device__ __forceinline__ void q4_load_q(const ChunkParams &p, const CUtensorMa
         const int h0 = (w.kvh_hp & 0xFFFF) * p.group + (w.kvh_hp >> 16) * NQ;
         const int row0 = (self ? 0 : p.cu_q[w.r]) + w.i0;
         for (int n = 0; n < NQ; ++n, ++u) {
-            const uint32_t b = u % C::kQRing;
+            const uint32_t b = C::q_ring(u);
             if (u >= (uint32_t)C::kQRing &&
-                !(ok = mbar_wait_warp(&q4t->q_empty[b], ((u / C::kQRing) - 1) & 1, abort, limit)))
+                !(ok = mbar_wait_warp(&q4t->q_empty[b], C::q_parity(u - C::kQRing), abort, limit)))
                 break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&q4t->q_raw[b], C::kTileBytes);
@@ -1031,11 +1041,11 @@ __device__ __forceinline__ void q8_convert(const ChunkParams &p, uint8_t *smem, 
             if constexpr (Q4) {
 #pragma unroll 1
                 for (int n = 0; n < NQ; ++n, ++q_uses) {   // q_uses: tiles here
-                    const uint32_t b = q_uses % C::kQRing;
-                    if (!wait(&q8t->q_raw[b], (q_uses / C::kQRing) & 1))
+                    const uint32_t b = C::q_ring(q_uses);
+                    if (!wait(&q8t->q_raw[b], C::q_parity(q_uses)))
                         return false;
                     const int row = cw * 32 + lane;
-                    q8t->qe[q_uses % 6][row] = (int8_t)q4_convert_q_row<D>(smem_u32(smem + C::q_tile(b)), row);
+                    q8t->qe[q4_exps(q_uses)][row] = (int8_t)q4_convert_q_row<D>(smem_u32(smem + C::q_tile(b)), row);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
@@ -1622,7 +1632,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     if constexpr (Q4) {
                         // never 0 or infinite: a masked score times it stays -inf, a zero one 0
                         if (t == 0)
-                            q_sl2 = fminf(fmaxf(sl2 * exp2i(qt->qe[((it - it_begin) * NQ + wg) % 6][row]), 1.2e-38f), 3.0e38f);
+                            q_sl2 = fminf(fmaxf(sl2 * exp2i(qt->qe[q4_exps((it - it_begin) * NQ + wg)][row]), 1.2e-38f), 3.0e38f);
                         tsl2 = q_sl2;
                     } else {
                         // (the lift with the q row's exponent: the K tile's may be the smallest there is)
@@ -1973,7 +1983,7 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                     umma_commit(bar);
             };
             auto issue_qk = [&](int n, int slot) {
-                const uint32_t q_tile = Q4 ? q_addr + C::q_tile((q_uses * NQ + n) % C::kQRing) : q_addr + n * C::kTileBytes;
+                const uint32_t q_tile = Q4 ? q_addr + C::q_tile(C::q_ring(q_uses * NQ + n)) : q_addr + n * C::kTileBytes;
     #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t koff = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
@@ -2020,14 +2030,14 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // Q4: head by head, as its Q tile is there; used up with the item's last scores
                 auto q_done = [&](int qn) {
                     if constexpr (Q4)
-                        commit(&q8t->q_empty[(q_uses * NQ + qn) % C::kQRing]);
+                        commit(&q8t->q_empty[C::q_ring(q_uses * NQ + qn)]);
                 };
                 if constexpr (Q4) {
                     if (!wait_slot(sK))
                         break;
                     for (int qn = 0; qn < NQ && ok; ++qn) {
                         const uint32_t u = q_uses * NQ + qn;
-                        if (!(ok = wait(&q8t->q_full[u % C::kQRing], (u / C::kQRing) & 1)))
+                        if (!(ok = wait(&q8t->q_full[C::q_ring(u)], C::q_parity(u))))
                             break;
                         tc_fence_after_sync();
                         issue_qk(qn, sK);
