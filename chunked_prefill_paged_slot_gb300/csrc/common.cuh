@@ -19,6 +19,14 @@ namespace cpsa {
 constexpr int kTileM = 128;   // query rows per tensor-core tile
 constexpr int kTileN = 128;   // keys per KV tile of the chunk kernel
 constexpr int kMaxGroup = 16; // q heads per kv head handled by the decode kernel
+// Longest sequence: key numbers are ints, and the kernels look some thousand keys ahead.
+constexpr int kMaxSeqLen = 0x7fff0000;
+
+// Whether a request's block_table row, of pages of page_size places, holds s keys.
+__device__ __forceinline__ bool fits_table(int s, int max_blocks, int page_size)
+{
+    return s <= kMaxSeqLen && (int64_t)s <= (int64_t)max_blocks * page_size;
+}
 
 // ---------------------------------------------------------------------------
 // generic helpers

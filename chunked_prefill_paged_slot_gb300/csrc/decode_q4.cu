@@ -154,7 +154,7 @@ __device__ __forceinline__ OneRow one_row(const DecodeParams &p)
         bad = CPSA_DEV_TOKENS_MISMATCH;
     else if (s < 1)
         bad = CPSA_DEV_SEQ_LT_QUERY;
-    else if ((int64_t)s > (int64_t)p.max_blocks * p.page_size)
+    else if (!fits_table(s, p.max_blocks, p.page_size))
         bad = CPSA_DEV_SEQ_GT_TABLE;
     OneRow row{s, 1, 0};
     if (!bad) {

@@ -42,7 +42,7 @@ __device__ Req make_req(const PlanParams &p, int query_len, int seq_len)
     Req q;
     q.q = query_len;
     q.s = seq_len;
-    q.valid = !(q.q < 0 || q.s < q.q) && (int64_t)q.s <= (int64_t)p.max_blocks * p.page_size;
+    q.valid = !(q.q < 0 || q.s < q.q) && fits_table(q.s, p.max_blocks, p.page_size);
     q.hist = q.s - q.q;
     return q;
 }

@@ -301,7 +301,7 @@ __device__ __noinline__ int self_plan_run(const SelfPlanArgs a, PrefillItem *ite
         bad = CPSA_DEV_TOKENS_MISMATCH;
     else if (q < 0 || s < q)
         bad = CPSA_DEV_SEQ_LT_QUERY;
-    else if ((int64_t)s > (int64_t)a.max_blocks * a.page_size)
+    else if (!fits_table(s, a.max_blocks, a.page_size))
         bad = CPSA_DEV_SEQ_GT_TABLE;
     if (blockIdx.x == 0 && lane == 0) {
         if (bad)
