@@ -41,6 +41,6 @@ from ._lib import (  # noqa: F401
     cpp_selftest_warp_wait,
     OnlineChunker, BatchScheduler,
     DEV_SLOT_OUT_OF_RANGE, DEV_PAGE_OUT_OF_RANGE, DEV_SEQ_LT_QUERY, DEV_TOKENS_MISMATCH, DEV_SEQ_GT_TABLE,
-    DEV_SPLITS_CLAMPED, DEV_WAIT_TIMEOUT, DEV_POSITION_OUT_OF_RANGE,
+    DEV_SPLITS_CLAMPED, DEV_WAIT_TIMEOUT, DEV_PLAN_OVERFLOW, DEV_POSITION_OUT_OF_RANGE,
 )
 from .step import AttentionStep, rope_table  # noqa: F401

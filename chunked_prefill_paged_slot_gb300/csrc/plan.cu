@@ -57,15 +57,18 @@ __device__ __forceinline__ int unit_tiles(const PlanParams &p, const Req &rq, in
 }
 
 // Stream-K positions of all prefill units of one request: their KV tiles plus
-// unit_cost per unit (0 for decode / invalid / empty).
-__device__ int prefill_tiles(const PlanParams &p, const Req &rq)
+// unit_cost per unit (0 for decode / invalid / empty). I: in 64 bits until it is
+// known that all requests' together pass kMaxPlanTiles.
+template <typename I = int>
+__device__ I prefill_tiles(const PlanParams &p, const Req &rq)
 {
     if (!rq.valid || rq.q < 2)
         return 0;
     // query tile qt has hb + qt + 1 tiles, but for the last, which may be short
     const int nqt = ceil_div(rq.q, kTileM), hb = ceil_div(rq.hist, kTileN);
     const int last = unit_tiles(p, rq, nqt - 1, rq.q - (nqt - 1) * kTileM);
-    return p.Hkv * (p.group / p.nq) * (last + (nqt - 1) * (hb + 1) + (nqt - 1) * (nqt - 2) / 2 + nqt * p.unit_cost);
+    return (I)(p.Hkv * (p.group / p.nq)) *
+           (last + (I)(nqt - 1) * (hb + 1) + (I)(nqt - 1) * (nqt - 2) / 2 + nqt * p.unit_cost);
 }
 
 // Positions of the request's longest unit (its last query tile), 0 for decode /
@@ -513,7 +516,7 @@ template <bool STREAM>
 __device__ __forceinline__ void add_request(const PlanParams &p, const Req &rq, PlanTotals &t)
 {
     t.tok += rq.q > 0 ? rq.q : 0;   // invalid requests still occupy their rows
-    t.tiles += prefill_tiles(p, rq);
+    t.tiles += prefill_tiles<long long>(p, rq);
     t.longest = max(t.longest, longest_unit(p, rq));
     t.shortest = min(t.shortest, shortest_unit(p, rq));
     if (STREAM && p.dec_stream) {
@@ -525,6 +528,12 @@ __device__ __forceinline__ void add_request(const PlanParams &p, const Req &rq, 
         const int ns = decode_splits(rq, p.max_splits, p.dec_keys);
         if (ns > 1) t.dprows += (long long)p.Hq * ns;
     }
+}
+
+// The flag of a batch of which nothing can be computed; 0: none.
+__device__ __forceinline__ uint32_t plan_refused(const PlanParams &p, const PlanTotals &tot)
+{
+    return tot.tok != p.num_tokens ? CPSA_DEV_TOKENS_MISMATCH : tot.tiles > kMaxPlanTiles ? CPSA_DEV_PLAN_OVERFLOW : 0u;
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
@@ -542,8 +551,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p)
     const long long tiles = tot.tiles;
     if (p.dec_stream)
         tot.dprows = decode_stream_bound(p, tot.dprows);
-    if (tot.tok != p.num_tokens) {
-        if (threadIdx.x == 0) set_dev_error(p.dev_err, CPSA_DEV_TOKENS_MISMATCH);
+    if (const uint32_t bad = plan_refused(p, tot)) {
+        if (threadIdx.x == 0) set_dev_error(p.dev_err, bad);
         if (threadIdx.x < kCntSlots) p.counts[threadIdx.x] = 0;
         for (int c = threadIdx.x; c <= p.chunk_grid; c += kPlanThreads) p.run_first[c] = 0;
         for (int c = threadIdx.x; p.dec_stream && c <= p.dec_grid; c += kPlanThreads) p.dec_first[c] = 0;
@@ -662,7 +671,7 @@ struct SmallPlan {
     Counts off;                               // entries ahead of the other requests' lists
 };
 
-// False where the lengths do not add up (the lists are empty then).
+// False where the batch is refused (the lists are empty then).
 template <bool STREAM>
 __device__ __forceinline__ bool small_plan(const PlanParams &p, int lane, SmallPlan &w)
 {
@@ -675,8 +684,8 @@ __device__ __forceinline__ bool small_plan(const PlanParams &p, int lane, SmallP
     if (mine)
         add_request<STREAM>(p, w.rq, tot);
     warp_totals<STREAM>(tot);
-    if (tot.tok != p.num_tokens) {
-        if (lane == 0) set_dev_error(p.dev_err, CPSA_DEV_TOKENS_MISMATCH);
+    if (const uint32_t bad = plan_refused(p, tot)) {
+        if (lane == 0) set_dev_error(p.dev_err, bad);
         if (lane < kCntSlots) p.counts[lane] = 0;
         for (int c = lane; c <= p.chunk_grid; c += 32) p.run_first[c] = 0;
         if (STREAM)

@@ -67,6 +67,7 @@ __host__ __device__ constexpr bool cut_units(long long shortest, long long longe
 {
     return !(shortest >= run && longest <= run + kCutCostTiles);
 }
+constexpr int kMaxPlanTiles = 1 << 30;      // of a planned batch's units together: their positions are ints
 constexpr int kMaxChunkGrid = 256;          // upper bound of the chunk kernel's grid (SMs)
 constexpr int kDecodeChunk = 64;            // keys per decode pipeline stage
 constexpr int kDecodeKeysPerSplit = 4096;   // keys per decode split (multiple of kDecodeChunk)

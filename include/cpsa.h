@@ -73,7 +73,9 @@ extern "C" {
 #define CPSA_DEV_SPLITS_CLAMPED 0x20u     /* info: partials did not fit the workspace, one KV split used */
 #define CPSA_DEV_WAIT_TIMEOUT 0x40u       /* an on-chip wait hit its limit; outputs of this call invalid */
 #define CPSA_DEV_POSITION_OUT_OF_RANGE 0x100u  /* position >= max_positions: token skipped whole */
-#define CPSA_DEV_PLAN_OVERFLOW 0x80u      /* a self-planned chunk-kernel run held more pieces than it can keep */
+#define CPSA_DEV_PLAN_OVERFLOW 0x80u      /* a self-planned chunk-kernel run held more pieces than it can keep, or a
+                                           * planned batch's prefill units more than 2^30 tiles of 128 keys: nothing
+                                           * computed */
 
 /*
  * Write the new tokens' K and V into their cache slots ([DS] section 3.1,

@@ -35,3 +35,13 @@ def test_too_long(cuda_lib, lens, s, kind):
     assert flags == cuda_lib.DEV_SEQ_GT_TABLE
     assert bool((out[:lens[0]] == 5.0).all())
     assert not bool((out[lens[0]:] == 5.0).any()) and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("others", [0, 1, 5, 40])
+def test_more_tiles_than_an_int_counts(cuda_lib, others, kind):
+    """Many query tiles and heads over a long history: each number an int, their product not. Nothing is computed."""
+    tokens = 12800 if others == 0 else 1280            # alone: more than a batch that plans itself
+    out, flags = call(cuda_lib, kind, [tokens] + [1] * others, [2 ** 30] + [9] * others, heads=64, blocks=1 << 22)
+    assert flags == cuda_lib.DEV_PLAN_OVERFLOW
+    assert bool((out == 5.0).all())
