@@ -1779,8 +1779,8 @@ chunk_attn_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tm_q,
                 // accesses are 512 contiguous bytes. bf16, because three other pieces' partials
                 // of all warps then fit the Q and K/V buffers and the merge reads them from L2 in
                 // one go; it costs a second rounding of half a bf16 step (512 tokens at history
-                // 32256 over the 8-bit cache: 2.4e-3 of the norm from the 64-bit result, 1.7e-3, the
-                // output's own rounding, with whole units). The unit's partial rows keep
+                // 32256 over the 8-bit and the 4-bit cache: 2.4e-3 of the norm from the 64-bit result, 1.7e-3, the
+                // output's own rounding, with whole units, which take 408 us instead of 184 over 4 bits). The unit's partial rows keep
                 // the fp32 row pitch of the workspace (decode partials share it).
                 const int piece = w.piece_np & 0xFFFF;
                 unsigned long long *cnt = p.flags + ((int64_t)w.aux * NQ + wg) * 4 + sub;

@@ -112,8 +112,9 @@ __device__ __forceinline__ int position_state(const RopeParams &p, int64_t t, in
 // are neighbours in a warp: each sums its 16 squares (exact products of bf16 numbers), a
 // butterfly adds up the threads', in an order that does not depend on anything. (By rsqrtf,
 // within two last places: a 32768-token prompt, 32/8 heads, D 128, takes 146 us into the bf16
-// cache, 150 us by a root and a division, 123 us without norms; 2048 tokens 16.4 us, where the
-// chain of loads, sums and rotation is what counts.)
+// cache, 150 us by a root and a division, 123 us without norms; 179 and 148 us into the 8-bit, 168 and
+// 139 into the 4-bit cache. 2048 tokens into bf16 from HBM 14.2 us, 11.5 without norms, 7.7 by their bytes:
+// the position, the slot, the rows, the sum and the weights wait for one another.)
 __device__ __forceinline__ float squares8(const uint4 &x)
 {
     float f[8], a = 0.f;
@@ -302,7 +303,8 @@ __device__ __forceinline__ void rope_items(const RopeParams &p, int64_t first, i
 }
 
 // Seven blocks an SM (72 registers) with norms or 4 bits: a 32768-token prompt (32/8 heads, D 128) into
-// the 4-bit cache takes 142 us, 158 us with the 84 registers the compiler takes by itself.
+// the 4-bit cache takes 139 us, 158 us with the 84 registers the compiler takes by itself. (With norms and
+// 4 bits, two heads a thread, that spills 86 bytes.)
 template <int D, int HPT, int KV, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, KV == kKvQ4 || NORM ? 7 : 0) rope_append_kernel(const RopeParams p)
 {
