@@ -30,7 +30,7 @@
 // loads of a warp are free of bank conflicts.
 //
 // Measured (32/8 heads, D 128, pages of 16): 384 rows of 1024 to 8192 keys, 2.1 GB, 334 us
-// replayed in a graph and a call, 6.3 TB/s or 94 % of a plain copy's rate. That is
+// replayed in a graph, 6.3 TB/s or 94 % of a plain copy's rate, and 334 to 344 us a call. That is
 // with the plan, an empty chunk launch and the combine; with the arithmetic skipped a call took
 // 338 us where it took 350 (by an earlier plan), so what is left is loading and those three. Not kept: 16 warps on half stages (407 us),
 // the scores of one stage beside the output of the one before (402 us).

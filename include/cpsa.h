@@ -404,8 +404,8 @@ int cpp_chunked_prefill_attn_events(const void *q, const void *k_cache, const vo
  * to k_cache / v_cache at slot_mapping[t] with the rules of cpp_kv_cache_write
  * (s < 0 skipped, s past the cache flagged with CPSA_DEV_SLOT_OUT_OF_RANGE and
  * skipped). Rows of requests that fail validation (CPSA_DEV_SEQ_LT_QUERY,
- * CPSA_DEV_SEQ_GT_TABLE, CPSA_DEV_TOKENS_MISMATCH) are neither attended nor
- * stored. The stores of a call become visible to later stream-ordered work; no
+ * CPSA_DEV_SEQ_GT_TABLE, CPSA_DEV_TOKENS_MISMATCH, CPSA_DEV_PLAN_OVERFLOW) are
+ * neither attended nor stored. The stores of a call become visible to later stream-ordered work; no
  * part of the same call reads them. With every h_r a multiple of 128 the output
  * is bit-identical to the two-call sequence; otherwise the chunk's keys are
  * tiled from h_r rather than from a multiple of 128 and the output agrees to

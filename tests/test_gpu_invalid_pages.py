@@ -170,3 +170,36 @@ def test_one_long_chunk(cuda_lib, hq, hkv, d, helpers, P):
     """One request, which plans itself; its tiles' slots are used many times over."""
     check(cuda_lib, helpers, W.BatchSpec(hist=[2500], qlen=[333], num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=P,
                                          seed=300 + hq + P))
+
+
+@pytest.mark.parametrize("P", [8, 16, 128])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_fused_write(cuda_lib, hq, hkv, d, P):
+    """With the KV write fused: the history's bad pages count as zeros, the new rows are the call's own, also where the table
+    has a bad page for them."""
+    spec = W.BatchSpec(hist=[700, 300, 33, 0, 900], qlen=[130, 1, 1, 200, 1], num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                       page_size=P, seed=400 + hq + P)
+    b, caches = bf16_helpers.draw(spec)
+    table = b.block_table.copy()
+    whole = dataclasses.replace(b, block_table=b.block_table.copy())
+    more = []
+    for n, (r, i, x) in enumerate(bad_entries(b)):          # a page of zeros for each
+        table[r, i], whole.block_table[r, i] = x, b.num_pages + n
+        more.append(np.zeros_like(caches[0][:1]))
+    ref_caches = [np.concatenate([c] + more) for c in caches]
+    at = np.concatenate([[0], np.cumsum(spec.qlen)])
+    for r, (h, n) in enumerate(zip(spec.hist, spec.qlen)):
+        j = np.arange(h, h + n)
+        for c, new in zip(ref_caches, (b.k, b.v)):
+            c[whole.block_table[r, j // P], :, j % P] = new[at[r]:at[r + 1]]
+    T, s = b.num_tokens, spec
+    ws = torch.empty(cuda_lib.cpp_attn_workspace_bytes(5, T, hq, hkv, d, 8), dtype=torch.uint8, device="cuda")
+    out = torch.full((T, hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kc, vc = map(to_dev_bf16, caches)
+    cuda_lib.cpp_chunked_prefill_attn_write_kv(to_dev_bf16(b.q), to_dev_bf16(b.k), to_dev_bf16(b.v), to_dev(b.slot_mapping),
+                                               kc, vc, to_dev(b.query_lens), to_dev(b.seq_lens), to_dev(table), out, ws, err)
+    got = bf16_tensor_to_f64(out)
+    assert cuda_lib.cpp_read_device_error(err) == cuda_lib.DEV_PAGE_OUT_OF_RANGE
+    ref, vmax = bf16_helpers.reference(whole, ref_caches)
+    close(got, ref, vmax, str(spec))
